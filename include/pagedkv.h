@@ -49,6 +49,9 @@ extern "C" {
 #define PKV_DEV_WAIT_TIMEOUT 4     /* a bounded wait on a copy gave up; every
                                       output of that launch is then undefined */
 #define PKV_DEV_BAD_POSITION 5     /* position outside its block table */
+#define PKV_DEV_BAD_QUERY_RANGE 7  /* query_start entries that are out of order or past
+                                      num_tokens */
+#define PKV_DEV_NONFINITE 8        /* an infinity or NaN to be stored in 8 bits */
 #define PKV_DEV_BAD_GROUP 6        /* a shared-prefix group whose members do not
                                       share the stated blocks, or too many rows */
 
@@ -368,6 +371,73 @@ int pkv_slot_mapping(const int32_t* block_tables, const int32_t* positions, int 
 int pkv_copy_blocks(void* const* k_caches, void* const* v_caches, int num_layers,
                     const int64_t* block_pairs, int num_pairs, int64_t block_bytes,
                     int64_t num_blocks, int32_t* dev_err, void* stream);
+
+/* ---- 8-bit cache ----------------------------------------------------------- */
+/*
+ * An 8-bit KV cache: codes uint8 [num_blocks, block_size, num_kv_heads, 128],
+ * one tensor for K and one for V, and for each an fp32 scale for every block
+ * and KV head, [num_blocks, scale_stride] with scale_stride >= num_kv_heads.  A
+ * code c stands for c * scale.  (A scale_stride that is a multiple of 4 makes a
+ * row of scales a 16-byte multiple, so pkv_copy_blocks and pkv_swap_blocks move
+ * scales as they move codes.)
+ */
+#define PKV_CODE_INT8 0   /* two's complement, -127 .. 127 */
+#define PKV_CODE_E4M3 1   /* 8-bit floating point, 4 exponent and 3 mantissa bits, max 448 */
+
+/*
+ * The cache write of a packed batch into an 8-bit cache.  Sequence s brings
+ * rows query_start[s] .. query_start[s + 1] - 1 of k and v: the last of its
+ * context_lens[s] tokens (whole prompts, chunks and single decoded tokens
+ * alike; a sequence may bring none).  Row by row they go to the slots their
+ * positions have in the block table.  For every block that receives rows and
+ * every KV head, with s0 the block's scale when it already holds earlier rows
+ * of the sequence, else 0, and M = 127 or 448:
+ *   s       = max(s0, max |x| / M)  over the new rows x
+ *   code(x) = the code nearest to x * (1 / s) (0 where s is 0)
+ *   if s > s0, each earlier code c becomes the code nearest to c * (s0 / s)
+ * with every quotient and product rounded to fp32 and ties to even, so codes
+ * and scales depend on the sequence's own tokens only.  An element is rounded
+ * again each time its block's scale grows.  Rows past the context are left as
+ * they were.
+ *   k, v         fp16 [num_tokens, num_kv_heads, 128], 16-byte aligned
+ *   query_start  int32 [num_seqs + 1] (device), ascending, at most num_tokens;
+ *                rows before its first or past its last entry are not read
+ *   k_cache, v_cache  codes, 16-byte aligned, written; k_scale, v_scale written
+ *   code         PKV_CODE_INT8 or PKV_CODE_E4M3
+ *   block_size   8, 16, 32 or 64
+ * Reported, and left out: a sequence whose query_start entries are out of order
+ * or past num_tokens (PKV_DEV_BAD_QUERY_RANGE) or whose context is shorter than
+ * its rows or longer than its table (PKV_DEV_BAD_CONTEXT_LEN); a block id out
+ * of range (PKV_DEV_BAD_BLOCK_ID).  Infinities and NaN are stored as 0 and
+ * reported (PKV_DEV_NONFINITE).  Two sequences that write into one block race:
+ * give a shared block a private copy first (pkv_copy_blocks on codes and scales).
+ */
+int pkv_reshape_and_cache_q8(const void* k, const void* v, const int32_t* query_start,
+                             const int32_t* block_tables, const int32_t* context_lens,
+                             void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                             int code, int num_tokens, int num_seqs, int num_kv_heads,
+                             int head_dim, int block_size, int64_t num_blocks,
+                             int max_blocks_per_seq, int scale_stride, int32_t* dev_err,
+                             void* stream);
+
+/*
+ * Single-token decode attention over an 8-bit cache: pkv_paged_attention_decode
+ * with K_s[t] = code * k_scale[block of t, g] and V_s[t] likewise.  Same shapes,
+ * workspace, split rule, errors and output; q and out must be 8-byte aligned.
+ * A token in a block whose id is out of range is left out.
+ * fp32 accumulation; the softmax weights, with the V scale folded in and taken
+ * relative to their running maximum, are rounded to fp16 once for the product
+ * with V, the result once.  Scales must be finite and not negative (a zero
+ * scale is a block of zeros); codes past the context may be any bytes.
+ */
+int pkv_paged_attention_decode_q8(void* out, const void* q, const void* k_cache,
+                                  const void* v_cache, const float* k_scale,
+                                  const float* v_scale, int code, const int32_t* block_tables,
+                                  const int32_t* context_lens, int num_seqs, int num_q_heads,
+                                  int num_kv_heads, int head_dim, int block_size,
+                                  int64_t num_blocks, int max_blocks_per_seq, int scale_stride,
+                                  float scale, void* workspace, size_t workspace_bytes,
+                                  int32_t* dev_err, void* stream);
 
 /* ---- swap between pools ---------------------------------------------------- */
 /*

@@ -22,6 +22,11 @@ PKV_DEV_BAD_SLOT = 3
 PKV_DEV_WAIT_TIMEOUT = 4
 PKV_DEV_BAD_POSITION = 5
 PKV_DEV_BAD_GROUP = 6
+PKV_DEV_BAD_QUERY_RANGE = 7
+PKV_DEV_NONFINITE = 8
+
+PKV_CODE_INT8 = 0
+PKV_CODE_E4M3 = 1
 
 # name -> (restype, argtypes); every symbol the header declares.
 _P, _I, _I64, _SZ, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
@@ -49,6 +54,10 @@ SIGNATURES = {
                                               _I64, _I, _F, _P, _SZ, _P, _P]),
     "pkv_paged_attention_decode_noalloc": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I64,
                                                 _I, _F, _P, _P]),
+    "pkv_reshape_and_cache_q8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I,
+                                      _I64, _I, _I, _P, _P]),
+    "pkv_paged_attention_decode_q8": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I,
+                                           _I64, _I, _I, _F, _P, _SZ, _P, _P]),
     "pkv_reshape_and_cache": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I64, _P, _P]),
     "pkv_slot_mapping": (_I, [_P, _P, _I, _I, _I, _I64, _P, _P, _P]),
     "pkv_copy_blocks": (_I, [_P, _P, _I, _P, _I, _I64, _I64, _P, _P]),

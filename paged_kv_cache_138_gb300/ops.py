@@ -9,7 +9,7 @@ import ctypes
 
 import torch
 
-from ._lib import check, lib
+from ._lib import PKV_CODE_E4M3, PKV_CODE_INT8, check, lib
 
 HEAD_DIM = 128
 BLOCK_SIZE = 16
@@ -430,3 +430,97 @@ def paged_attention_decode_grouped_fused(out, q, k_new, v_new, k_cache, v_cache,
             seq_group, group_shared, workspace, dev_err, stream)
     return _issue(lib().pkv_paged_attention_decode_grouped_fused, args,
                   "paged_attention_decode_grouped_fused", keep, prepare, out)
+
+
+# ---- 8-bit cache ----------------------------------------------------------------------
+
+_CODES = {torch.int8: PKV_CODE_INT8, torch.float8_e4m3fn: PKV_CODE_E4M3}
+
+
+def q8_cache(num_blocks, num_kv_heads, block_size=BLOCK_SIZE, dtype=torch.int8, device=None):
+    """A zeroed 8-bit cache of one layer: (k_cache, v_cache, k_scale, v_scale), codes
+    [num_blocks, block_size, num_kv_heads, 128] of ``dtype`` (torch.int8 or
+    torch.float8_e4m3fn) and scales fp32 [num_blocks, stride], stride num_kv_heads
+    rounded up to 4 (the columns past num_kv_heads are padding), which lets
+    copy_blocks and swap_blocks move scales like codes."""
+    if dtype not in _CODES:
+        raise TypeError("an 8-bit cache is torch.int8 or torch.float8_e4m3fn, got %s" % dtype)
+    dev = device or torch.cuda.current_device()
+    shape = (num_blocks, block_size, num_kv_heads, HEAD_DIM)
+    stride = -(-num_kv_heads // 4) * 4
+    return tuple(torch.zeros(shape, dtype=torch.uint8, device=dev).view(dtype) for _ in "kv") + \
+        tuple(torch.zeros((num_blocks, stride), dtype=torch.float32, device=dev) for _ in "kv")
+
+
+def _q8_args(k_cache, v_cache, k_scale, v_scale):
+    code = _CODES.get(k_cache.dtype)
+    if code is None:
+        raise TypeError("k_cache must be torch.int8 or torch.float8_e4m3fn, got %s" % k_cache.dtype)
+    _dev(k_cache, "k_cache", k_cache.dtype, 4)
+    _dev(v_cache, "v_cache", k_cache.dtype, 4)
+    _dev(k_scale, "k_scale", torch.float32, 2)
+    _dev(v_scale, "v_scale", torch.float32, 2)
+    if v_cache.shape != k_cache.shape or v_scale.shape != k_scale.shape:
+        raise ValueError("K and V caches, and their scales, must share one shape")
+    if k_scale.shape[0] != k_cache.shape[0] or k_scale.shape[1] < k_cache.shape[2]:
+        raise ValueError("scales must be [num_blocks, >= num_kv_heads]")
+    return code
+
+
+def reshape_and_cache_q8(k, v, query_start, block_tables, context_lens, k_cache, v_cache, k_scale,
+                         v_scale, dev_err=None, stream=None, prepare=False):
+    """Code the packed rows k, v [T, Hkv, 128] into an 8-bit cache: sequence s brings
+    rows query_start[s] .. query_start[s + 1] - 1, the last of its context_lens[s]
+    tokens.  One scale per (block, KV head): the largest magnitude over 127 (int8) or
+    448 (e4m3); rows a block already holds are coded anew when its scale grows.
+    prepare=True returns a PreparedLaunch instead of launching."""
+    _dev(k, "k", torch.float16, 3)
+    _dev(v, "v", torch.float16, 3)
+    _dev(query_start, "query_start", torch.int32, 1)
+    _dev(block_tables, "block_tables", torch.int32, 2)
+    _dev(context_lens, "context_lens", torch.int32, 1)
+    code = _q8_args(k_cache, v_cache, k_scale, v_scale)
+    T, Hkv, D = k.shape
+    nb, bs, Hkv2, D2 = k_cache.shape
+    S, max_blocks = block_tables.shape
+    if v.shape != k.shape or (Hkv2, D2) != (Hkv, D):
+        raise ValueError("shape mismatch")
+    if query_start.shape[0] != S + 1 or context_lens.shape[0] != S:
+        raise ValueError("query_start must have num_seqs + 1 entries, context_lens num_seqs")
+    args = (_ptr(k), _ptr(v), _ptr(query_start), _ptr(block_tables), _ptr(context_lens),
+            _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), code, T, S, Hkv, D, bs, nb,
+            max_blocks, k_scale.shape[1], _ptr(dev_err), _stream_handle(stream))
+    keep = (k, v, query_start, block_tables, context_lens, k_cache, v_cache, k_scale, v_scale,
+            dev_err, stream)
+    return _issue(lib().pkv_reshape_and_cache_q8, args, "reshape_and_cache_q8", keep, prepare, None)
+
+
+def paged_attention_decode_q8(out, q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                              context_lens, scale, workspace=None, dev_err=None, stream=None,
+                              prepare=False):
+    """paged_attention_decode over an 8-bit cache (see q8_cache, reshape_and_cache_q8);
+    same workspace.  prepare=True returns a PreparedLaunch instead of launching."""
+    _dev(q, "q", torch.float16, 3)
+    _dev(out, "out", torch.float16, 3)
+    _dev(block_tables, "block_tables", torch.int32, 2)
+    _dev(context_lens, "context_lens", torch.int32, 1)
+    code = _q8_args(k_cache, v_cache, k_scale, v_scale)
+    S, Hq, D = q.shape
+    nb, bs, Hkv, D2 = k_cache.shape
+    if out.shape != q.shape or D2 != D:
+        raise ValueError("shape mismatch")
+    if block_tables.shape[0] != S or context_lens.shape[0] != S:
+        raise ValueError("block_tables / context_lens must have num_seqs rows")
+    max_blocks = block_tables.shape[1]
+    need = workspace_bytes(S, Hq, max_blocks, bs, D)
+    if need and workspace is None:
+        workspace = alloc_workspace(S, Hq, max_blocks, q.device, bs)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    args = (_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), code,
+            _ptr(block_tables), _ptr(context_lens), S, Hq, Hkv, D, bs, nb, max_blocks,
+            k_scale.shape[1], float(scale), _ptr(workspace), ws_bytes, _ptr(dev_err),
+            _stream_handle(stream))
+    keep = (out, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, workspace,
+            dev_err, stream)
+    return _issue(lib().pkv_paged_attention_decode_q8, args, "paged_attention_decode_q8", keep,
+                  prepare, out)
