@@ -372,6 +372,64 @@ int pkv_copy_blocks(void* const* k_caches, void* const* v_caches, int num_layers
                     const int64_t* block_pairs, int num_pairs, int64_t block_bytes,
                     int64_t num_blocks, int32_t* dev_err, void* stream);
 
+/* ---- prompt attention ------------------------------------------------------- */
+/*
+ * Causal attention of whole prompts and prompt chunks over the paged cache.
+ * The batch is packed: sequence s owns rows query_start[s] ..
+ * query_start[s + 1] - 1 of q and out (it may own none), the last of its
+ * context_lens[s] tokens; the earlier ones are in the cache only (a prefix-cache
+ * hit, an earlier chunk).  All of the context's K and V must already be in the
+ * cache (pkv_reshape_and_cache).  For row i at position pos and query head h,
+ * with g = h / (num_q_heads / num_kv_heads):
+ *   out[i, h, :] = sum_{t <= pos} softmax_t(scale * <q[i, h, :], K_s[t, g, :]>) V_s[t, g, :]
+ * Chunks of any length, one token (pkv_paged_attention_decode is faster for a
+ * batch of single tokens) to a whole prompt.
+ *   out, q       fp16 [num_tokens, num_q_heads, 128], 16-byte aligned; rows of out
+ *                that no sequence owns are left as they were
+ *   k_cache, v_cache  fp16 [num_blocks, block_size, num_kv_heads, 128], 16-byte
+ *                aligned; rows past a context may hold anything.  K and V of a
+ *                context's own tokens must be finite: a V row that is not also
+ *                spoils rows of q up to 127 positions before it
+ *   block_tables int32 [num_seqs, max_blocks_per_seq] (device)
+ *   context_lens int32 [num_seqs] (device)
+ *   query_start  int32 [num_seqs + 1] (device), ascending, at most num_tokens
+ *   block_size 8, 16, 32 or 64; num_q_heads / num_kv_heads 1, 2, 4 or 8
+ *   workspace    at least pkv_paged_attention_prefill_workspace_bytes(...) (0
+ *                unless the key axis is split); not shared by launches in flight
+ * Reported, and left out: a sequence whose query_start entries are out of order
+ * or past num_tokens (PKV_DEV_BAD_QUERY_RANGE) or whose context is shorter than
+ * its rows or longer than its table (PKV_DEV_BAD_CONTEXT_LEN); its rows of out
+ * stay as they were.  A block whose id is out of range (PKV_DEV_BAD_BLOCK_ID)
+ * counts as zeros.
+ * fp32 scores, maxima, sums and accumulators; the softmax weights are rounded
+ * to fp16 for the product with V, the result once.
+ */
+int pkv_paged_attention_prefill(void* out, const void* q, const void* k_cache,
+                                const void* v_cache, const int32_t* block_tables,
+                                const int32_t* context_lens, const int32_t* query_start,
+                                int num_tokens, int num_seqs, int num_q_heads, int num_kv_heads,
+                                int head_dim, int block_size, int64_t num_blocks,
+                                int max_blocks_per_seq, float scale, void* workspace,
+                                size_t workspace_bytes, int32_t* dev_err, void* stream);
+
+/* Workspace bytes of pkv_paged_attention_prefill for these sizes (host only):
+ * partials of a split key axis, used when the query rows alone cannot fill the
+ * GPU; else 0. */
+size_t pkv_paged_attention_prefill_workspace_bytes(int num_tokens, int num_seqs, int num_q_heads,
+                                                   int num_kv_heads, int max_blocks_per_seq,
+                                                   int block_size);
+
+/*
+ * The same over packed K and V: whole prompts whose tokens are all in this
+ * call (k, v fp16 [num_tokens, num_kv_heads, 128], 16-byte aligned, packed like
+ * q), with no cache read, for instance before they are written to an 8-bit
+ * cache.  Rows of k and v that no sequence owns may hold anything.
+ */
+int pkv_prompt_attention(void* out, const void* q, const void* k, const void* v,
+                         const int32_t* query_start, int num_tokens, int num_seqs,
+                         int num_q_heads, int num_kv_heads, int head_dim, float scale,
+                         int32_t* dev_err, void* stream);
+
 /* ---- 8-bit cache ----------------------------------------------------------- */
 /*
  * An 8-bit KV cache: codes uint8 [num_blocks, block_size, num_kv_heads, 128],

@@ -54,6 +54,10 @@ SIGNATURES = {
                                               _I64, _I, _F, _P, _SZ, _P, _P]),
     "pkv_paged_attention_decode_noalloc": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I64,
                                                 _I, _F, _P, _P]),
+    "pkv_paged_attention_prefill": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I64,
+                                         _I, _F, _P, _SZ, _P, _P]),
+    "pkv_paged_attention_prefill_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "pkv_prompt_attention": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _P]),
     "pkv_reshape_and_cache_q8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I,
                                       _I64, _I, _I, _P, _P]),
     "pkv_paged_attention_decode_q8": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I,

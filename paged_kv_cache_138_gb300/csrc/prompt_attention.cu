@@ -1,0 +1,717 @@
+// Causal attention of whole prompts and prompt chunks (sm_103a, tcgen05).
+//
+// For packed row i of sequence s (position pos, query head h, KV head g):
+//   out[i, h] = sum_{t <= pos} softmax_t(scale <q[i, h], K[t, g]>) V[t, g]
+// with K and V either in the paged fp16 cache (context_lens[s] tokens, the
+// packed rows the last of them) or packed like q.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <atomic>
+#include <climits>
+
+#include "q8_device.cuh"
+
+namespace pkv {
+namespace attn {
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
+}
+namespace prompt {
+
+constexpr int kHeadDim = 128;
+constexpr int kTile = 128;                       // rows of a query tile, tokens of a KV tile
+constexpr int kHalfBytes = kTile * 128;          // 128 rows x 64 dims, 128-byte swizzle
+constexpr int kTileBytes = 2 * kHalfBytes;
+constexpr int kStages = 5;                       // KV tiles in shared memory
+constexpr int kThreads = 384;                    // 2 softmax warpgroups; one of copy and MMA warps
+// Registers a thread after the split: 256 * 224 + 128 * 56 = 384 * 168, what the
+// CTA was launched with (a softmax thread holds a row of 128 scores).
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 224, kOtherRegs = 56;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split");
+constexpr int kCopyWarp = 8, kMmaWarp = 9;
+constexpr float kRescale = 8.f;                  // log2 units
+constexpr float kNoMax = -1e30f;
+
+struct Smem {
+  static constexpr int q = 0;                            // two query tiles
+  static constexpr int kv = q + 2 * kTileBytes;
+  static constexpr int bars = kv + kStages * kTileBytes;
+  static constexpr int q_full = bars;                    // [2]
+  static constexpr int kv_full = q_full + 16;            // [kStages]
+  static constexpr int kv_empty = kv_full + 8 * kStages; // [kStages]
+  static constexpr int s_full = kv_empty + 8 * kStages;  // [2] scores of a tile are in TMEM
+  static constexpr int p_full = s_full + 16;             // [2] weights of a tile are in TMEM
+  static constexpr int o_full = p_full + 16;             // [2] the tile's output is complete
+  static constexpr int v_clean = o_full + 16;            // rows past the context are zero
+  static constexpr int drained = v_clean + 8;
+  static constexpr int tmem = drained + 8;
+  static constexpr int total = tmem + 16;
+  static constexpr int alloc = total + 1024;
+  static_assert(alloc <= 227 * 1024, "shared memory of one CTA");
+};
+
+// TMEM columns: scores (overwritten by the fp16 weights) and outputs of the two tiles
+constexpr uint32_t kColS = 0, kColO = 256;
+
+struct Params {
+  __half* out;
+  const int32_t* query_start;
+  const int32_t* context_lens;   // nullptr: K and V are packed like q
+  const int32_t* block_tables;
+  float* part_o;                 // [rows, splits, 128]
+  float* part_ml;                // [rows, splits, 2]
+  int32_t* dev_err;
+  int64_t num_blocks;
+  int num_tokens, num_seqs, num_q_heads, num_kv_heads, max_blocks;
+  int group_shift;               // log2(num_q_heads / num_kv_heads)
+  int split_tiles;               // KV tiles a unit covers at most
+  int splits;
+  float scale_log2;              // |scale| log2 e
+  uint32_t idesc_qk;
+};
+
+// ---- tcgen05 ------------------------------------------------------------------------
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11,"
+      " %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29,"
+      " %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10,"
+      " %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28,"
+      " %29, %30, %31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31]), "r"(addr)
+      : "memory");
+}
+
+// Shared-memory operand descriptor, 128-byte swizzle.  K-major (Q, K): rows of
+// 128 bytes, 8-row groups `stride` apart.  MN-major (V): 64-dim chunks
+// `lead` apart, 8-token groups `stride` apart.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
+  return static_cast<uint64_t>((addr & 0x3ffff) >> 4) | static_cast<uint64_t>(lead >> 4) << 16 |
+         static_cast<uint64_t>(stride >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+
+constexpr uint32_t kIdescBase = 1u << 4                       // fp32 accumulators, fp16 operands
+                                | (kTile / 8) << 17 | (kTile / 16) << 24;
+constexpr uint32_t kIdescPv = kIdescBase | 1u << 16;          // V is MN-major
+constexpr uint32_t kNegateA = 1u << 13;
+
+// The queries a CTA works on: two tiles of 128 rows, row r of a tile being
+// token r / group, query head g * group + r % group.
+struct Unit {
+  PackedSeq seq;
+  int s, g;
+  int tok0[2];      // first token of each tile (among the sequence's packed rows)
+  int end[2];       // KV tiles [begin, end) of each tile
+  int begin, last;  // all KV tiles of the unit
+};
+
+__device__ __forceinline__ bool make_unit(const Params& p, Unit& u, int64_t max_context) {
+  const int per = 2 * kTile >> p.group_shift;   // tokens of a unit
+  const int units = gridDim.x / p.num_kv_heads;
+  u.g = blockIdx.x % p.num_kv_heads;
+  // later rows of a prompt see more tokens: start with them
+  const int unit = units - 1 - blockIdx.x / p.num_kv_heads;
+  u.s = find_unit_seq(p.query_start, p.num_seqs, unit, per, 1);
+  u.seq = packed_seq(p.query_start, p.context_lens, u.s, p.num_tokens, max_context, p.dev_err, false);
+  const int nth = unit - unit_base(p.query_start, u.s, per, 1);
+  if (!u.seq.ok || nth < 0 || static_cast<int64_t>(nth) * per >= u.seq.n) return false;
+  u.begin = blockIdx.y * p.split_tiles;
+  u.last = u.begin;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    u.tok0[x] = nth * per + x * (kTile >> p.group_shift);
+    const int tok_end = min(u.seq.n, u.tok0[x] + (kTile >> p.group_shift));
+    u.end[x] = u.begin;
+    if (tok_end > u.tok0[x]) {
+      const int last_pos = u.seq.ctx - u.seq.n + tok_end - 1;
+      u.end[x] = max(u.begin, min(u.begin + p.split_tiles, last_pos / kTile + 1));
+    }
+    u.last = max(u.last, u.end[x]);
+  }
+  return u.last > u.begin;
+}
+
+// BS: block size of the paged cache, 0 for packed K and V.
+template <int BS>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
+                            const __grid_constant__ CUtensorMap tmap_k,
+                            const __grid_constant__ CUtensorMap tmap_v, const Params p) {
+  constexpr unsigned kFull = 0xffffffffu;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t max_context = BS ? static_cast<int64_t>(p.max_blocks) * BS : INT32_MAX;
+  if (blockIdx.x == 0 && blockIdx.y == 0)   // every entry is looked at once, used or not
+    for (int s = threadIdx.x; s < p.num_seqs; s += kThreads)
+      packed_seq(p.query_start, p.context_lens, s, p.num_tokens, max_context, p.dev_err, true);
+  Unit u;
+  if (!make_unit(p, u, max_context)) return;
+
+  const auto bar = [&](int at, int i) { return reinterpret_cast<uint64_t*>(smem + at) + i; };
+  if (warp == kCopyWarp && lane == 0) {
+    prefetch_tmap(&tmap_q);
+    prefetch_tmap(&tmap_k);
+    prefetch_tmap(&tmap_v);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(Smem::q_full, i), 1);
+      mbar_init(bar(Smem::s_full, i), 1);
+      mbar_init(bar(Smem::p_full, i), kTile);
+      mbar_init(bar(Smem::o_full, i), 1);
+    }
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(bar(Smem::kv_full, i), 1);
+      mbar_init(bar(Smem::kv_empty, i), 1);
+    }
+    mbar_init(bar(Smem::v_clean, 0), 1);
+    mbar_init(bar(Smem::drained, 0), 1);
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_u32(smem + Smem::tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + Smem::tmem);
+
+  // rows of the last KV tile past the context: whatever the copy brings there,
+  // 0 * NaN must not reach a sum.  (A paged block wholly past the context is
+  // read from past the cache's last row, where the copy engine fills zeros.)
+  const int ctx_tile = (u.seq.ctx - 1) / kTile;
+  const int valid = u.seq.ctx - ctx_tile * kTile;
+  const int dirty_end = BS ? min(kTile, (valid + BS - 1) / (BS ? BS : 1) * BS) : kTile;
+  const bool clean = ctx_tile < u.last && ctx_tile >= u.begin && dirty_end > valid;
+
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  if (warp == kCopyWarp) {
+    // ---- copies: Q, then K and V of each tile through a ring of kStages ----------------
+    if (lane == 0) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (u.end[x] == u.begin) continue;
+        uint64_t* b = bar(Smem::q_full, x);
+        uint8_t* dst = smem + Smem::q + x * kTileBytes;
+        mbar_arrive_expect_tx(b, kTileBytes);
+        for (int h = 0; h < 2; ++h)
+          tma_load_3d(dst + h * kHalfBytes, &tmap_q, 64 * h, u.g << p.group_shift,
+                      u.seq.row0 + u.tok0[x], b);
+      }
+    }
+    constexpr int kBoxes = BS ? kTile / (BS ? BS : 1) : 1;
+    int n = 0;   // copies issued
+    bool ok = true;
+    for (int j = u.begin; j < u.last && ok; ++j) {
+      int row = 0;
+      if (BS == 0) {
+        row = u.seq.row0 + j * kTile;
+      } else if (lane < kBoxes) {
+        const int tok = j * kTile + lane * BS;
+        int64_t r = p.num_blocks * BS;   // past the last row: zeros
+        if (tok < u.seq.ctx) {
+          const int32_t b =
+              __ldg(p.block_tables + static_cast<int64_t>(u.s) * p.max_blocks + tok / (BS ? BS : 1));
+          if (b < 0 || b >= p.num_blocks)
+            report(p.dev_err, PKV_DEV_BAD_BLOCK_ID);
+          else
+            r = static_cast<int64_t>(b) * BS;
+        }
+        row = static_cast<int>(r);
+      }
+      for (int kv = 0; kv < 2; ++kv, ++n) {
+        const int st = n % kStages;
+        if (n >= kStages)
+          ok = mbar_wait_bounded(bar(Smem::kv_empty, st), (n / kStages - 1) & 1, p.dev_err);
+        ok = __all_sync(kFull, ok) != 0;
+        if (!ok) break;
+        uint64_t* b = bar(Smem::kv_full, st);
+        uint8_t* dst = smem + Smem::kv + st * kTileBytes;
+        if (lane == 0) mbar_arrive_expect_tx(b, kTileBytes);
+        __syncwarp();
+        if (lane < kBoxes) {
+          constexpr int kBoxBytes = kHalfBytes / kBoxes;
+          const CUtensorMap* m = kv ? &tmap_v : &tmap_k;
+          tma_load_3d(dst + lane * kBoxBytes, m, 0, u.g, row, b);
+          tma_load_3d(dst + kHalfBytes + lane * kBoxBytes, m, 64, u.g, row, b);
+        }
+        if (kv == 1 && clean && j == ctx_tile) {
+          ok = mbar_wait_bounded(b, (n / kStages) & 1, p.dev_err);
+          ok = __all_sync(kFull, ok) != 0;
+          const uint32_t at = smem_u32(dst);
+          for (int i = lane; ok && i < (dirty_end - valid) * 16; i += 32)
+            st_shared_zero16(at + (i & 8 ? kHalfBytes : 0) + (valid + (i >> 4)) * 128 + (i & 7) * 16);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(Smem::v_clean, 0));
+        }
+      }
+    }
+    if (!ok) {   // a wait gave up: let this CTA's copies land before it goes
+      for (int i = max(0, n - kStages); i < n; ++i)
+        mbar_wait_bounded(bar(Smem::kv_full, i % kStages), (i / kStages) & 1, p.dev_err);
+    }
+  } else if (warp == kMmaWarp) {
+    // ---- matrix products: one thread issues them all ------------------------------------
+    if (lane == 0) {
+      bool ok = true;
+      const uint32_t q_at = smem_u32(smem + Smem::q), kv_at = smem_u32(smem + Smem::kv);
+      const auto qk = [&](int x, int st) {   // S_x = Q_x K^T
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t off = (k >> 2) * kHalfBytes + (k & 3) * 32;
+          mma_ss(tmem + kColS + x * kTile, operand_desc(q_at + x * kTileBytes + off, 16, 1024),
+                 operand_desc(kv_at + st * kTileBytes + off, 16, 1024), p.idesc_qk, k > 0);
+        }
+      };
+      const auto pv = [&](int x, int st, bool acc) {   // O_x += P_x V
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_ts(tmem + kColO + x * kTile, tmem + kColS + x * kTile + 8 * k,
+                 operand_desc(kv_at + st * kTileBytes + k * 2048, kHalfBytes, 1024), kIdescPv,
+                 acc || k > 0);
+      };
+      const auto full = [&](int n) {
+        return mbar_wait_bounded(bar(Smem::kv_full, n % kStages), (n / kStages) & 1, p.dev_err);
+      };
+      ok = full(0);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (ok && u.end[x] > u.begin) {
+          ok = mbar_wait_bounded(bar(Smem::q_full, x), 0, p.dev_err);
+          if (ok) {
+            qk(x, 0);
+            mma_commit(bar(Smem::s_full, x));
+          }
+        }
+      }
+      mma_commit(bar(Smem::kv_empty, 0));
+      for (int j = u.begin; j < u.last && ok; ++j) {
+        const int it = j - u.begin, nv = 2 * it + 1, nk = 2 * it + 2;
+        ok = full(nv);
+        if (ok && clean && j == ctx_tile)
+          ok = mbar_wait_bounded(bar(Smem::v_clean, 0), 0, p.dev_err);
+        if (ok && j + 1 < u.last) ok = full(nk);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (!ok || j >= u.end[x]) continue;
+          ok = mbar_wait_bounded(bar(Smem::p_full, x), it & 1, p.dev_err);
+          if (!ok) continue;
+          fence_after();
+          pv(x, nv % kStages, it > 0);
+          if (j + 1 < u.end[x]) {
+            qk(x, nk % kStages);
+            mma_commit(bar(Smem::s_full, x));
+          } else {
+            mma_commit(bar(Smem::o_full, x));
+          }
+        }
+        mma_commit(bar(Smem::kv_empty, nv % kStages));
+        if (j + 1 < u.last) mma_commit(bar(Smem::kv_empty, nk % kStages));
+      }
+      // every product has completed before the tensor memory is given back
+      mma_commit(bar(Smem::drained, 0));
+      mbar_wait_bounded(bar(Smem::drained, 0), 0, p.dev_err);
+    }
+    __syncwarp();
+  }
+  } else {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+  if (u.end[warp >> 2] > u.begin) {
+    // ---- softmax: one thread per query row ----------------------------------------------
+    const int x = warp >> 2;
+    const int r = threadIdx.x & (kTile - 1);
+    const int tok = u.tok0[x] + (r >> p.group_shift);
+    const int pos0 = u.seq.ctx - u.seq.n + u.tok0[x];             // of the tile's first row
+    const int pos = min(u.seq.ctx - u.seq.n + tok, u.seq.ctx - 1);
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + lanes + kColS + x * kTile;
+    const uint32_t o_at = tmem + lanes + kColO + x * kTile;
+    const float sc = p.scale_log2;
+    float m = kNoMax;
+    float2 l2 = make_float2(0.f, 0.f);
+    bool ok = true;
+    for (int j = u.begin; j < u.end[x]; ++j) {
+      const int it = j - u.begin;
+      ok = mbar_wait_bounded(bar(Smem::s_full, x), it & 1, p.dev_err);
+      ok = __all_sync(kFull, ok) != 0;
+      if (!ok) break;
+      fence_after();
+      float s[kTile];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, reinterpret_cast<uint32_t*>(s + 32 * c));
+      wait_ld();
+      if (j * kTile + kTile - 1 > pos0) {   // some row of the tile does not see all of it
+        const int see = pos - j * kTile;    // columns 0 .. see
+#pragma unroll
+        for (int c = 0; c < kTile; ++c) s[c] = c <= see ? s[c] : -INFINITY;
+      }
+      float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int c = 4; c < kTile; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+      const float bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+      // the maximum moves only when a score passes it by more than 2^8
+      const bool moves = bm > m + kRescale;
+      if (__any_sync(kFull, moves)) {
+        const float nm = moves ? bm : m;
+        const float alpha = exp2_approx(m - nm);
+        m = nm;
+        l2 = fmul2(l2, make_float2(alpha, alpha));
+        if (it > 0) {
+          // the scores of tile j follow the product of tile j - 1: O is at rest
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tmem_ld32(o_at + 32 * c, o);
+            wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st32(o_at + 32 * c, o);
+          }
+        }
+      }
+      const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-m, -m);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          float2 e = ffma2(make_float2(s[64 * c + 2 * i], s[64 * c + 2 * i + 1]), sc2, nm2);
+          e.x = exp2_approx(e.x);
+          e.y = exp2_approx(e.y);
+          w[i] = pack_half2(e.x, e.y);
+          l2 = ffma2(e, make_float2(1.f, 1.f), l2);
+        }
+        tmem_st32(s_at + 32 * c, w);
+      }
+      wait_st();
+      fence_before();
+      mbar_arrive(bar(Smem::p_full, x));
+    }
+    if (ok) ok = mbar_wait_bounded(bar(Smem::o_full, x), 0, p.dev_err);
+    ok = __all_sync(kFull, ok) != 0;
+    if (ok) {
+      fence_after();
+      const float l = l2.x + l2.y;
+      const int head = (u.g << p.group_shift) + (r & ((1 << p.group_shift) - 1));
+      const int64_t row = (static_cast<int64_t>(u.seq.row0) + tok) * p.num_q_heads + head;
+      const bool mine = tok < u.seq.n;
+      // rows whose tokens one unit covers are written, others leave a partial
+      const bool whole = pos / kTile < p.split_tiles;
+      const bool direct = mine && whole && blockIdx.y == 0;
+      const bool part = mine && !whole && pos / kTile >= u.begin;
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const int64_t at = row * p.splits + blockIdx.y;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        tmem_ld32(o_at + 32 * c, o);
+        wait_ld();
+        if (direct) {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + row * kHeadDim + 32 * c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              h[k] = pack_half2(__uint_as_float(o[8 * i + 2 * k]) * inv,
+                                __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
+            dst[i] = make_uint4(h[0], h[1], h[2], h[3]);
+          }
+        } else if (part) {
+          uint4* dst = reinterpret_cast<uint4*>(p.part_o + at * kHeadDim + 32 * c);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+      }
+      if (part) {
+        p.part_ml[2 * at] = m;
+        p.part_ml[2 * at + 1] = l;
+      }
+    }
+  }
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+// Log-sum-exp merge of the rows that several units covered: one warp per row.
+constexpr int kMergeRows = 8;
+__global__ void __launch_bounds__(kMergeRows * 32)
+    prompt_merge_kernel(const Params p, int64_t max_context) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeRows + (threadIdx.x >> 5);
+  if (row >= static_cast<int64_t>(p.num_tokens) * p.num_q_heads) return;
+  const int i = static_cast<int>(row / p.num_q_heads);
+  const int s = find_unit_seq(p.query_start, p.num_seqs, i, 1, 0);
+  const PackedSeq q = packed_seq(p.query_start, p.context_lens, s, p.num_tokens, max_context,
+                                 p.dev_err, false);
+  if (!q.ok || i < q.row0 || i >= q.row0 + q.n) return;
+  const int tile = (q.ctx - q.n + i - q.row0) / kTile;
+  const int n = tile / p.split_tiles + 1;
+  if (n == 1) return;
+  const float* ml = p.part_ml + row * p.splits * 2;
+  const float4* po = reinterpret_cast<const float4*>(p.part_o + row * p.splits * kHeadDim);
+  float M = kNoMax;
+  for (int k = lane; k < n; k += 32) M = fmaxf(M, ml[2 * k]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+  float den = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < n; ++k) {
+    const float c = exp2_approx(ml[2 * k] - M);
+    const float4 v = po[k * (kHeadDim / 4) + lane];
+    num.x += c * v.x;
+    num.y += c * v.y;
+    num.z += c * v.z;
+    num.w += c * v.w;
+    den += c * ml[2 * k + 1];
+  }
+  const float inv = den > 0.f ? 1.f / den : 0.f;
+  uint2 w;
+  w.x = pack_half2(num.x * inv, num.y * inv);
+  w.y = pack_half2(num.z * inv, num.w * inv);
+  *reinterpret_cast<uint2*>(p.out + row * kHeadDim + 4 * lane) = w;
+}
+
+// ---- host -------------------------------------------------------------------------------
+
+// [rows, heads, 128] fp16, boxes of box_rows rows x box_heads heads x 64 dims
+bool make_map(CUtensorMap* map, const void* base, int heads, int64_t rows, int box_heads,
+              int box_rows) {
+  auto fn = attn::encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {kHeadDim, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[2] = {kHeadDim * 2, static_cast<cuuint64_t>(heads) * kHeadDim * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BS>
+int launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const Params& p,
+           int64_t units, cudaStream_t st) {
+  static std::atomic<uint8_t> opted_in[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+  if (dev < 0 || dev >= 64 || !opted_in[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(prompt_attention_kernel<BS>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Smem::alloc) != cudaSuccess)
+      return PKV_ERR_CUDA;
+    if (dev >= 0 && dev < 64) opted_in[dev].store(1, std::memory_order_release);
+  }
+  prompt_attention_kernel<BS>
+      <<<dim3(static_cast<unsigned>(units * p.num_kv_heads), p.splits), kThreads, Smem::alloc, st>>>(
+          mq, mk, mv, p);
+  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+int group_shift_of(int num_q_heads, int num_kv_heads) {
+  if (num_q_heads % num_kv_heads) return -1;
+  switch (num_q_heads / num_kv_heads) {
+    case 1: return 0;
+    case 2: return 1;
+    case 4: return 2;
+    case 8: return 3;
+    default: return -1;
+  }
+}
+
+// Splits of the key axis: 1 unless the units alone leave SMs idle.
+constexpr int kSms = 152;
+constexpr int kMinSplitTiles = 8;
+int64_t units_for(int num_tokens, int num_seqs, int group_shift) {
+  return num_tokens / (2 * kTile >> group_shift) + static_cast<int64_t>(num_seqs);
+}
+int splits_for(int64_t ctas, int64_t max_context, int* split_tiles) {
+  const int64_t tiles = (max_context + kTile - 1) / kTile;
+  int64_t want = std::min<int64_t>(std::max<int64_t>(1, kSms / std::max<int64_t>(ctas, 1)),
+                                   std::max<int64_t>(1, tiles / kMinSplitTiles));
+  const int64_t per = (tiles + want - 1) / want;
+  *split_tiles = static_cast<int>(per);
+  return static_cast<int>((tiles + per - 1) / per);
+}
+
+int run(void* out, const void* q, const void* k, const void* v, const int32_t* block_tables,
+        const int32_t* context_lens, const int32_t* query_start, int num_tokens, int num_seqs,
+        int num_q_heads, int num_kv_heads, int block_size, int64_t num_blocks, int max_blocks,
+        float scale, void* workspace, size_t workspace_bytes, int32_t* dev_err, void* stream) {
+  const int shift = group_shift_of(num_q_heads, num_kv_heads);
+  if (num_seqs == 0 || num_tokens == 0) return PKV_OK;
+  if (!out || !q || !k || !v || !query_start) return PKV_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(q) |
+       reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
+       reinterpret_cast<uintptr_t>(workspace)) &
+      15)
+    return PKV_ERR_INVALID_ARG;
+  const bool paged = block_size > 0;
+  const int64_t units = units_for(num_tokens, num_seqs, shift);
+  if (units * num_kv_heads > INT32_MAX || num_q_heads > 65535) return PKV_ERR_UNSUPPORTED;
+  Params p = {};
+  p.splits = 1;
+  p.split_tiles = INT32_MAX / kTile;
+  if (paged)
+    p.splits = splits_for(units * num_kv_heads, static_cast<int64_t>(max_blocks) * block_size,
+                          &p.split_tiles);
+  if (p.splits > 1) {
+    const size_t rows = static_cast<size_t>(num_tokens) * num_q_heads;
+    if (!workspace || workspace_bytes < rows * p.splits * (kHeadDim + 2) * sizeof(float))
+      return PKV_ERR_INVALID_ARG;
+    p.part_o = static_cast<float*>(workspace);
+    p.part_ml = p.part_o + rows * p.splits * kHeadDim;
+  }
+  p.out = static_cast<__half*>(out);
+  p.query_start = query_start;
+  p.context_lens = context_lens;
+  p.block_tables = block_tables;
+  p.dev_err = dev_err;
+  p.num_blocks = num_blocks;
+  p.num_tokens = num_tokens;
+  p.num_seqs = num_seqs;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.max_blocks = max_blocks;
+  p.group_shift = shift;
+  // a negative scale negates Q in the product, so that a row's maximum is the
+  // largest score either way; a scale of 0 keeps masked scores at -infinity
+  p.idesc_qk = kIdescBase | (scale < 0.f ? kNegateA : 0u);
+  p.scale_log2 = std::max(1e-30f, (scale < 0.f ? -scale : scale) * 1.4426950408889634f);
+
+  CUtensorMap mq, mk, mv;
+  const int64_t rows = paged ? num_blocks * block_size : num_tokens;
+  const int box = paged ? block_size : kTile;
+  if (!make_map(&mq, q, num_q_heads, num_tokens, 1 << shift, kTile >> shift) ||
+      !make_map(&mk, k, num_kv_heads, rows, 1, box) || !make_map(&mv, v, num_kv_heads, rows, 1, box))
+    return PKV_ERR_CUDA;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int rc;
+  switch (block_size) {
+    case 0: rc = launch<0>(mq, mk, mv, p, units, st); break;
+    case 8: rc = launch<8>(mq, mk, mv, p, units, st); break;
+    case 16: rc = launch<16>(mq, mk, mv, p, units, st); break;
+    case 32: rc = launch<32>(mq, mk, mv, p, units, st); break;
+    default: rc = launch<64>(mq, mk, mv, p, units, st); break;
+  }
+  if (rc != PKV_OK || p.splits == 1) return rc;
+  const int64_t all = static_cast<int64_t>(num_tokens) * num_q_heads;
+  prompt_merge_kernel<<<static_cast<unsigned>((all + kMergeRows - 1) / kMergeRows), kMergeRows * 32,
+                        0, st>>>(p, static_cast<int64_t>(max_blocks) * block_size);
+  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+}  // namespace prompt
+}  // namespace pkv
+
+extern "C" size_t pkv_paged_attention_prefill_workspace_bytes(int num_tokens, int num_seqs,
+                                                              int num_q_heads, int num_kv_heads,
+                                                              int max_blocks_per_seq,
+                                                              int block_size) {
+  using namespace pkv::prompt;
+  if (num_tokens <= 0 || num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
+      max_blocks_per_seq <= 0 || block_size <= 0)
+    return 0;
+  const int shift = group_shift_of(num_q_heads, num_kv_heads);
+  if (shift < 0) return 0;
+  int per = 0;
+  const int splits = splits_for(units_for(num_tokens, num_seqs, shift) * num_kv_heads,
+                                static_cast<int64_t>(max_blocks_per_seq) * block_size, &per);
+  return splits > 1 ? static_cast<size_t>(num_tokens) * num_q_heads * splits * (kHeadDim + 2) *
+                          sizeof(float)
+                    : 0;
+}
+
+extern "C" int pkv_paged_attention_prefill(void* out, const void* q, const void* k_cache,
+                                           const void* v_cache, const int32_t* block_tables,
+                                           const int32_t* context_lens,
+                                           const int32_t* query_start, int num_tokens,
+                                           int num_seqs, int num_q_heads, int num_kv_heads,
+                                           int head_dim, int block_size, int64_t num_blocks,
+                                           int max_blocks_per_seq, float scale, void* workspace,
+                                           size_t workspace_bytes, int32_t* dev_err,
+                                           void* stream) {
+  using namespace pkv::prompt;
+  if (num_tokens < 0 || num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_blocks <= 0 ||
+      max_blocks_per_seq <= 0)
+    return PKV_ERR_INVALID_ARG;
+  if (head_dim != kHeadDim ||
+      !(block_size == 8 || block_size == 16 || block_size == 32 || block_size == 64))
+    return PKV_ERR_UNSUPPORTED;
+  if (group_shift_of(num_q_heads, num_kv_heads) < 0) return PKV_ERR_UNSUPPORTED;
+  if (num_blocks > INT32_MAX / block_size ||
+      static_cast<int64_t>(max_blocks_per_seq) * block_size > INT32_MAX - 2 * kTile)
+    return PKV_ERR_UNSUPPORTED;
+  if (num_seqs > 0 && num_tokens > 0 && (!block_tables || !context_lens)) return PKV_ERR_INVALID_ARG;
+  return run(out, q, k_cache, v_cache, block_tables, context_lens, query_start, num_tokens,
+             num_seqs, num_q_heads, num_kv_heads, block_size, num_blocks, max_blocks_per_seq, scale,
+             workspace, workspace_bytes, dev_err, stream);
+}
+
+extern "C" int pkv_prompt_attention(void* out, const void* q, const void* k, const void* v,
+                                    const int32_t* query_start, int num_tokens, int num_seqs,
+                                    int num_q_heads, int num_kv_heads, int head_dim, float scale,
+                                    int32_t* dev_err, void* stream) {
+  using namespace pkv::prompt;
+  if (num_tokens < 0 || num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0)
+    return PKV_ERR_INVALID_ARG;
+  if (head_dim != kHeadDim || group_shift_of(num_q_heads, num_kv_heads) < 0)
+    return PKV_ERR_UNSUPPORTED;
+  if (num_tokens > INT32_MAX - 2 * kTile) return PKV_ERR_UNSUPPORTED;
+  return run(out, q, k, v, nullptr, nullptr, query_start, num_tokens, num_seqs, num_q_heads,
+             num_kv_heads, 0, 0, 0, scale, nullptr, 0, dev_err, stream);
+}

@@ -432,6 +432,72 @@ def paged_attention_decode_grouped_fused(out, q, k_new, v_new, k_cache, v_cache,
                   "paged_attention_decode_grouped_fused", keep, prepare, out)
 
 
+# ---- prompt attention ------------------------------------------------------------------
+
+def prefill_workspace_bytes(num_tokens, num_seqs, num_q_heads, num_kv_heads, max_blocks_per_seq,
+                            block_size=BLOCK_SIZE):
+    """Bytes of partials paged_attention_prefill needs for these sizes (0 unless it
+    splits the key axis)."""
+    return int(lib().pkv_paged_attention_prefill_workspace_bytes(
+        num_tokens, num_seqs, num_q_heads, num_kv_heads, max_blocks_per_seq, block_size))
+
+
+def paged_attention_prefill(out, q, k_cache, v_cache, block_tables, context_lens, query_start,
+                            scale, workspace=None, dev_err=None, stream=None, prepare=False):
+    """Causal attention of packed prompt rows over the paged cache: sequence s owns rows
+    query_start[s] .. query_start[s + 1] - 1 of q and out [T, Hq, 128], the last of its
+    context_lens[s] tokens, all of whose K/V are in the cache.
+    prepare=True returns a PreparedLaunch instead of launching."""
+    _dev(q, "q", torch.float16, 3)
+    _dev(out, "out", torch.float16, 3)
+    _dev(k_cache, "k_cache", torch.float16, 4)
+    _dev(v_cache, "v_cache", torch.float16, 4)
+    _dev(block_tables, "block_tables", torch.int32, 2)
+    _dev(context_lens, "context_lens", torch.int32, 1)
+    _dev(query_start, "query_start", torch.int32, 1)
+    T, Hq, D = q.shape
+    nb, bs, Hkv, D2 = k_cache.shape
+    S, max_blocks = block_tables.shape
+    if out.shape != q.shape or v_cache.shape != k_cache.shape or D2 != D:
+        raise ValueError("shape mismatch")
+    if query_start.shape[0] != S + 1 or context_lens.shape[0] != S:
+        raise ValueError("query_start must have num_seqs + 1 entries, context_lens num_seqs")
+    if workspace is None:
+        need = prefill_workspace_bytes(T, S, Hq, Hkv, max_blocks, bs)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    args = (_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+            _ptr(context_lens), _ptr(query_start), T, S, Hq, Hkv, D, bs, nb, max_blocks,
+            float(scale), _ptr(workspace), ws_bytes, _ptr(dev_err), _stream_handle(stream))
+    keep = (out, q, k_cache, v_cache, block_tables, context_lens, query_start, workspace, dev_err,
+            stream)
+    return _issue(lib().pkv_paged_attention_prefill, args, "paged_attention_prefill", keep,
+                  prepare, out)
+
+
+def prompt_attention(out, q, k, v, query_start, scale, dev_err=None, stream=None, prepare=False):
+    """Causal attention of whole packed prompts: q and out [T, Hq, 128], k and v [T, Hkv,
+    128], sequence s owning rows query_start[s] .. query_start[s + 1] - 1 of each.
+    prepare=True returns a PreparedLaunch instead of launching."""
+    _dev(q, "q", torch.float16, 3)
+    _dev(out, "out", torch.float16, 3)
+    _dev(k, "k", torch.float16, 3)
+    _dev(v, "v", torch.float16, 3)
+    _dev(query_start, "query_start", torch.int32, 1)
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    if out.shape != q.shape or k.shape != (T, Hkv, D) or v.shape != k.shape:
+        raise ValueError("shape mismatch")
+    S = query_start.shape[0] - 1
+    if S < 0:
+        raise ValueError("query_start must have num_seqs + 1 entries")
+    args = (_ptr(out), _ptr(q), _ptr(k), _ptr(v), _ptr(query_start), T, S, Hq, Hkv, D,
+            float(scale), _ptr(dev_err), _stream_handle(stream))
+    keep = (out, q, k, v, query_start, dev_err, stream)
+    return _issue(lib().pkv_prompt_attention, args, "prompt_attention", keep, prepare, out)
+
+
 # ---- 8-bit cache ----------------------------------------------------------------------
 
 _CODES = {torch.int8: PKV_CODE_INT8, torch.float8_e4m3fn: PKV_CODE_E4M3}
