@@ -24,12 +24,13 @@ constexpr int kTile = 128;                       // rows of a query tile, tokens
 constexpr int kHalfBytes = kTile * 128;          // 128 rows x 64 dims, 128-byte swizzle
 constexpr int kTileBytes = 2 * kHalfBytes;
 constexpr int kStages = 5;                       // KV tiles in shared memory
-constexpr int kThreads = 384;                    // 2 softmax warpgroups; one of copy and MMA warps
+constexpr int kThreads = 384;                    // 2 softmax warpgroups; copy, MMA and work warps
 // Registers a thread after the split: 256 * 224 + 128 * 56 = 384 * 168, what the
 // CTA was launched with (a softmax thread holds a row of 128 scores).
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 224, kOtherRegs = 56;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split");
-constexpr int kCopyWarp = 8, kMmaWarp = 9;
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kWorkWarp = 10;
+constexpr int kReaders = 10;                     // warps that read a unit's description
 constexpr float kRescale = 8.f;                  // log2 units
 constexpr float kNoMax = -1e30f;
 
@@ -38,14 +39,20 @@ struct Smem {
   static constexpr int kv = q + 2 * kTileBytes;
   static constexpr int bars = kv + kStages * kTileBytes;
   static constexpr int q_full = bars;                    // [2]
-  static constexpr int kv_full = q_full + 16;            // [kStages]
+  static constexpr int q_empty = q_full + 16;            // [2] the tile's last score product is done
+  static constexpr int kv_full = q_empty + 16;           // [kStages]
   static constexpr int kv_empty = kv_full + 8 * kStages; // [kStages]
   static constexpr int s_full = kv_empty + 8 * kStages;  // [2] scores of a tile are in TMEM
-  static constexpr int p_full = s_full + 16;             // [2] weights of a tile are in TMEM
-  static constexpr int o_full = p_full + 16;             // [2] the tile's output is complete
+  static constexpr int p_full = s_full + 16;             // [2][2] a half's weights are in TMEM
+  static constexpr int o_full = p_full + 32;             // [2] the tile's output is complete
   static constexpr int v_clean = o_full + 16;            // rows past the context are zero
-  static constexpr int drained = v_clean + 8;
-  static constexpr int tmem = drained + 8;
+  static constexpr int unit_full = v_clean + 8;          // the next unit is described
+  static constexpr int unit_empty = unit_full + 8;       // and every warp has read it
+  static constexpr int stolen = unit_empty + 8;          // the scheduler's answer is there
+  static constexpr int drained = stolen + 8;
+  static constexpr int answer = (drained + 8 + 15) / 16 * 16;
+  static constexpr int unit = answer + 16;
+  static constexpr int tmem = unit + 64;
   static constexpr int total = tmem + 16;
   static constexpr int alloc = total + 1024;
   static_assert(alloc <= 227 * 1024, "shared memory of one CTA");
@@ -91,6 +98,11 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
                    smem_u32(bar))
                : "memory");
 }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void fence_before() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
@@ -126,6 +138,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       : "memory");
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Shared-memory operand descriptor, 128-byte swizzle.  K-major (Q, K): rows of
 // 128 bytes, 8-row groups `stride` apart.  MN-major (V): 64-dim chunks
 // `lead` apart, 8-token groups `stride` apart.
@@ -139,35 +157,42 @@ constexpr uint32_t kIdescBase = 1u << 4                       // fp32 accumulato
 constexpr uint32_t kIdescPv = kIdescBase | 1u << 16;          // V is MN-major
 constexpr uint32_t kNegateA = 1u << 13;
 
-// The queries a CTA works on: two tiles of 128 rows, row r of a tile being
-// token r / group, query head g * group + r % group.
+// A piece of work: two query tiles of 128 rows of one KV head, row r of a tile
+// being token r / group, query head g * group + r % group, and the KV tiles
+// [begin, end) each attends to.
 struct Unit {
-  PackedSeq seq;
-  int s, g;
-  int tok0[2];      // first token of each tile (among the sequence's packed rows)
-  int end[2];       // KV tiles [begin, end) of each tile
-  int begin, last;  // all KV tiles of the unit
+  int row0, n, ctx, s;   // the sequence (see PackedSeq) and its index
+  int g, split;
+  int tok0[2];           // first token of each tile (among the sequence's packed rows)
+  int end[2];
+  int begin, last;       // KV tiles of the unit; last == begin: no more work
 };
+static_assert(sizeof(Unit) <= 64 && sizeof(Unit) % 16 == 0, "a unit's place in shared memory");
 
-__device__ __forceinline__ bool make_unit(const Params& p, Unit& u, int64_t max_context) {
+__device__ __forceinline__ bool make_unit(const Params& p, int bx, int by, int64_t max_context,
+                                          Unit& u) {
   const int per = 2 * kTile >> p.group_shift;   // tokens of a unit
   const int units = gridDim.x / p.num_kv_heads;
-  u.g = blockIdx.x % p.num_kv_heads;
   // later rows of a prompt see more tokens: start with them
-  const int unit = units - 1 - blockIdx.x / p.num_kv_heads;
+  const int unit = units - 1 - bx / p.num_kv_heads;
+  u.g = bx % p.num_kv_heads;
+  u.split = by;
   u.s = find_unit_seq(p.query_start, p.num_seqs, unit, per, 1);
-  u.seq = packed_seq(p.query_start, p.context_lens, u.s, p.num_tokens, max_context, p.dev_err, false);
+  const PackedSeq q = packed_seq(p.query_start, p.context_lens, u.s, p.num_tokens, max_context,
+                                 p.dev_err, false);
+  u.row0 = q.row0;
+  u.n = q.n;
+  u.ctx = q.ctx;
   const int nth = unit - unit_base(p.query_start, u.s, per, 1);
-  if (!u.seq.ok || nth < 0 || static_cast<int64_t>(nth) * per >= u.seq.n) return false;
-  u.begin = blockIdx.y * p.split_tiles;
-  u.last = u.begin;
+  u.begin = u.last = by * p.split_tiles;
+  if (!q.ok || nth < 0 || static_cast<int64_t>(nth) * per >= q.n) return false;
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     u.tok0[x] = nth * per + x * (kTile >> p.group_shift);
-    const int tok_end = min(u.seq.n, u.tok0[x] + (kTile >> p.group_shift));
+    const int tok_end = min(q.n, u.tok0[x] + (kTile >> p.group_shift));
     u.end[x] = u.begin;
     if (tok_end > u.tok0[x]) {
-      const int last_pos = u.seq.ctx - u.seq.n + tok_end - 1;
+      const int last_pos = q.ctx - q.n + tok_end - 1;
       u.end[x] = max(u.begin, min(u.begin + p.split_tiles, last_pos / kTile + 1));
     }
     u.last = max(u.last, u.end[x]);
@@ -175,7 +200,29 @@ __device__ __forceinline__ bool make_unit(const Params& p, Unit& u, int64_t max_
   return u.last > u.begin;
 }
 
+// Rows of the last KV tile past the context: whatever the copy brings there,
+// 0 * NaN must not reach a sum.  (A paged block wholly past the context is
+// read from past the cache's last row, where the copy engine fills zeros.)
+template <int BS>
+struct Tail {
+  int tile, valid, dirty_end;
+  bool clean;
+  __device__ __forceinline__ explicit Tail(const Unit& u) {
+    tile = (u.ctx - 1) / kTile;
+    valid = u.ctx - tile * kTile;
+    dirty_end = BS ? min(kTile, (valid + BS - 1) / (BS ? BS : 1) * BS) : kTile;
+    clean = tile < u.last && tile >= u.begin && dirty_end > valid;
+  }
+};
+
 // BS: block size of the paged cache, 0 for packed K and V.
+//
+// One CTA per SM.  Its warps: two softmax warpgroups (one per query tile, one
+// thread per row), a copy warp (TMA), a warp that issues the matrix products
+// and one that fetches work: the grid has a CTA for every unit, and a CTA that
+// runs takes the place of CTAs that have not started (clusterlaunchcontrol), so
+// that the next unit's copies and first products run beside the last
+// unit's softmax and output, and units of any length balance themselves.
 template <int BS>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
@@ -186,21 +233,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t max_context = BS ? static_cast<int64_t>(p.max_blocks) * BS : INT32_MAX;
-  if (blockIdx.x == 0 && blockIdx.y == 0)   // every entry is looked at once, used or not
-    for (int s = threadIdx.x; s < p.num_seqs; s += kThreads)
-      packed_seq(p.query_start, p.context_lens, s, p.num_tokens, max_context, p.dev_err, true);
-  Unit u;
-  if (!make_unit(p, u, max_context)) return;
-
   const auto bar = [&](int at, int i) { return reinterpret_cast<uint64_t*>(smem + at) + i; };
+  // a wait of a whole warp
+  const auto wait = [&](uint64_t* b, uint32_t parity) {
+    return __all_sync(kFull, mbar_wait_bounded(b, parity, p.dev_err)) != 0;
+  };
   if (warp == kCopyWarp && lane == 0) {
     prefetch_tmap(&tmap_q);
     prefetch_tmap(&tmap_k);
     prefetch_tmap(&tmap_v);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(Smem::q_full, i), 1);
+      mbar_init(bar(Smem::q_empty, i), 1);
       mbar_init(bar(Smem::s_full, i), 1);
-      mbar_init(bar(Smem::p_full, i), kTile);
+      mbar_init(bar(Smem::p_full, 2 * i), kTile);
+      mbar_init(bar(Smem::p_full, 2 * i + 1), kTile);
       mbar_init(bar(Smem::o_full, i), 1);
     }
     for (int i = 0; i < kStages; ++i) {
@@ -208,6 +255,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(Smem::kv_empty, i), 1);
     }
     mbar_init(bar(Smem::v_clean, 0), 1);
+    mbar_init(bar(Smem::unit_full, 0), 1);
+    mbar_init(bar(Smem::unit_empty, 0), kReaders);
+    mbar_init(bar(Smem::stolen, 0), 1);
     mbar_init(bar(Smem::drained, 0), 1);
     fence_barrier_init();
   }
@@ -222,233 +272,325 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + Smem::tmem);
 
-  // rows of the last KV tile past the context: whatever the copy brings there,
-  // 0 * NaN must not reach a sum.  (A paged block wholly past the context is
-  // read from past the cache's last row, where the copy engine fills zeros.)
-  const int ctx_tile = (u.seq.ctx - 1) / kTile;
-  const int valid = u.seq.ctx - ctx_tile * kTile;
-  const int dirty_end = BS ? min(kTile, (valid + BS - 1) / (BS ? BS : 1) * BS) : kTile;
-  const bool clean = ctx_tile < u.last && ctx_tile >= u.begin && dirty_end > valid;
+  // the k-th unit, read by a whole warp; false: no more work, or a wait gave up
+  const auto next_unit = [&](int k, Unit& u) {
+    if (!wait(bar(Smem::unit_full, 0), k & 1)) return false;
+    u = *reinterpret_cast<const Unit*>(smem + Smem::unit);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(Smem::unit_empty, 0));
+    return u.last > u.begin;
+  };
 
   if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-  if (warp == kCopyWarp) {
-    // ---- copies: Q, then K and V of each tile through a ring of kStages ----------------
-    if (lane == 0) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (u.end[x] == u.begin) continue;
-        uint64_t* b = bar(Smem::q_full, x);
-        uint8_t* dst = smem + Smem::q + x * kTileBytes;
-        mbar_arrive_expect_tx(b, kTileBytes);
-        for (int h = 0; h < 2; ++h)
-          tma_load_3d(dst + h * kHalfBytes, &tmap_q, 64 * h, u.g << p.group_shift,
-                      u.seq.row0 + u.tok0[x], b);
-      }
-    }
-    constexpr int kBoxes = BS ? kTile / (BS ? BS : 1) : 1;
-    int n = 0;   // copies issued
-    bool ok = true;
-    for (int j = u.begin; j < u.last && ok; ++j) {
-      int row = 0;
-      if (BS == 0) {
-        row = u.seq.row0 + j * kTile;
-      } else if (lane < kBoxes) {
-        const int tok = j * kTile + lane * BS;
-        int64_t r = p.num_blocks * BS;   // past the last row: zeros
-        if (tok < u.seq.ctx) {
-          const int32_t b =
-              __ldg(p.block_tables + static_cast<int64_t>(u.s) * p.max_blocks + tok / (BS ? BS : 1));
-          if (b < 0 || b >= p.num_blocks)
-            report(p.dev_err, PKV_DEV_BAD_BLOCK_ID);
-          else
-            r = static_cast<int64_t>(b) * BS;
-        }
-        row = static_cast<int>(r);
-      }
-      for (int kv = 0; kv < 2; ++kv, ++n) {
-        const int st = n % kStages;
-        if (n >= kStages)
-          ok = mbar_wait_bounded(bar(Smem::kv_empty, st), (n / kStages - 1) & 1, p.dev_err);
-        ok = __all_sync(kFull, ok) != 0;
-        if (!ok) break;
-        uint64_t* b = bar(Smem::kv_full, st);
-        uint8_t* dst = smem + Smem::kv + st * kTileBytes;
-        if (lane == 0) mbar_arrive_expect_tx(b, kTileBytes);
-        __syncwarp();
-        if (lane < kBoxes) {
-          constexpr int kBoxBytes = kHalfBytes / kBoxes;
-          const CUtensorMap* m = kv ? &tmap_v : &tmap_k;
-          tma_load_3d(dst + lane * kBoxBytes, m, 0, u.g, row, b);
-          tma_load_3d(dst + kHalfBytes + lane * kBoxBytes, m, 64, u.g, row, b);
-        }
-        if (kv == 1 && clean && j == ctx_tile) {
-          ok = mbar_wait_bounded(b, (n / kStages) & 1, p.dev_err);
-          ok = __all_sync(kFull, ok) != 0;
-          const uint32_t at = smem_u32(dst);
-          for (int i = lane; ok && i < (dirty_end - valid) * 16; i += 32)
-            st_shared_zero16(at + (i & 8 ? kHalfBytes : 0) + (valid + (i >> 4)) * 128 + (i & 7) * 16);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(Smem::v_clean, 0));
-        }
-      }
-    }
-    if (!ok) {   // a wait gave up: let this CTA's copies land before it goes
-      for (int i = max(0, n - kStages); i < n; ++i)
-        mbar_wait_bounded(bar(Smem::kv_full, i % kStages), (i / kStages) & 1, p.dev_err);
-    }
-  } else if (warp == kMmaWarp) {
-    // ---- matrix products: one thread issues them all ------------------------------------
-    if (lane == 0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kCopyWarp) {
+      // ---- copies: Q, then K and V of each tile through a ring of kStages ----------------
+      constexpr int kBoxes = BS ? kTile / (BS ? BS : 1) : 1;
+      int n = 0;                  // KV copies issued
+      int nq[2] = {0, 0};         // Q copies issued
       bool ok = true;
-      const uint32_t q_at = smem_u32(smem + Smem::q), kv_at = smem_u32(smem + Smem::kv);
-      const auto qk = [&](int x, int st) {   // S_x = Q_x K^T
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t off = (k >> 2) * kHalfBytes + (k & 3) * 32;
-          mma_ss(tmem + kColS + x * kTile, operand_desc(q_at + x * kTileBytes + off, 16, 1024),
-                 operand_desc(kv_at + st * kTileBytes + off, 16, 1024), p.idesc_qk, k > 0);
-        }
-      };
-      const auto pv = [&](int x, int st, bool acc) {   // O_x += P_x V
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_ts(tmem + kColO + x * kTile, tmem + kColS + x * kTile + 8 * k,
-                 operand_desc(kv_at + st * kTileBytes + k * 2048, kHalfBytes, 1024), kIdescPv,
-                 acc || k > 0);
-      };
-      const auto full = [&](int n) {
-        return mbar_wait_bounded(bar(Smem::kv_full, n % kStages), (n / kStages) & 1, p.dev_err);
-      };
-      ok = full(0);
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (ok && u.end[x] > u.begin) {
-          ok = mbar_wait_bounded(bar(Smem::q_full, x), 0, p.dev_err);
-          if (ok) {
-            qk(x, 0);
-            mma_commit(bar(Smem::s_full, x));
-          }
-        }
-      }
-      mma_commit(bar(Smem::kv_empty, 0));
-      for (int j = u.begin; j < u.last && ok; ++j) {
-        const int it = j - u.begin, nv = 2 * it + 1, nk = 2 * it + 2;
-        ok = full(nv);
-        if (ok && clean && j == ctx_tile)
-          ok = mbar_wait_bounded(bar(Smem::v_clean, 0), 0, p.dev_err);
-        if (ok && j + 1 < u.last) ok = full(nk);
+      Unit u;
+      for (int k = 0; ok && next_unit(k, u); ++k) {
+        const Tail<BS> tail(u);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          if (!ok || j >= u.end[x]) continue;
-          ok = mbar_wait_bounded(bar(Smem::p_full, x), it & 1, p.dev_err);
+          if (!ok || u.end[x] == u.begin) continue;
+          if (nq[x] > 0) ok = wait(bar(Smem::q_empty, x), (nq[x] - 1) & 1);
           if (!ok) continue;
-          fence_after();
-          pv(x, nv % kStages, it > 0);
-          if (j + 1 < u.end[x]) {
-            qk(x, nk % kStages);
-            mma_commit(bar(Smem::s_full, x));
-          } else {
-            mma_commit(bar(Smem::o_full, x));
+          ++nq[x];
+          if (lane == 0) {
+            uint64_t* b = bar(Smem::q_full, x);
+            uint8_t* dst = smem + Smem::q + x * kTileBytes;
+            mbar_arrive_expect_tx(b, kTileBytes);
+            for (int h = 0; h < 2; ++h)
+              tma_load_3d(dst + h * kHalfBytes, &tmap_q, 64 * h, u.g << p.group_shift,
+                          u.row0 + u.tok0[x], b);
           }
         }
-        mma_commit(bar(Smem::kv_empty, nv % kStages));
-        if (j + 1 < u.last) mma_commit(bar(Smem::kv_empty, nk % kStages));
+        for (int j = u.begin; j < u.last && ok; ++j) {
+          int row = 0;
+          if (BS == 0) {
+            row = u.row0 + j * kTile;
+          } else if (lane < kBoxes) {
+            const int tok = j * kTile + lane * BS;
+            int64_t r = p.num_blocks * BS;   // past the last row: zeros
+            if (tok < u.ctx) {
+              const int32_t b = __ldg(p.block_tables + static_cast<int64_t>(u.s) * p.max_blocks +
+                                      tok / (BS ? BS : 1));
+              if (b < 0 || b >= p.num_blocks)
+                report(p.dev_err, PKV_DEV_BAD_BLOCK_ID);
+              else
+                r = static_cast<int64_t>(b) * BS;
+            }
+            row = static_cast<int>(r);
+          }
+          for (int kv = 0; kv < 2; ++kv) {
+            const int st = n % kStages;
+            if (n >= kStages) ok = wait(bar(Smem::kv_empty, st), (n / kStages - 1) & 1);
+            if (!ok) break;
+            uint64_t* b = bar(Smem::kv_full, st);
+            uint8_t* dst = smem + Smem::kv + st * kTileBytes;
+            if (lane == 0) mbar_arrive_expect_tx(b, kTileBytes);
+            __syncwarp();
+            if (lane < kBoxes) {
+              constexpr int kBoxBytes = kHalfBytes / kBoxes;
+              const CUtensorMap* m = kv ? &tmap_v : &tmap_k;
+              tma_load_3d(dst + lane * kBoxBytes, m, 0, u.g, row, b);
+              tma_load_3d(dst + kHalfBytes + lane * kBoxBytes, m, 64, u.g, row, b);
+            }
+            if (kv == 1 && tail.clean && j == tail.tile) {
+              ok = wait(b, (n / kStages) & 1);
+              const uint32_t at = smem_u32(dst);
+              for (int i = lane; ok && i < (tail.dirty_end - tail.valid) * 16; i += 32)
+                st_shared_zero16(at + (i & 8 ? kHalfBytes : 0) + (tail.valid + (i >> 4)) * 128 +
+                                 (i & 7) * 16);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(Smem::v_clean, 0));
+            }
+            ++n;
+          }
+        }
+      }
+      if (!ok) {   // a wait gave up: let this CTA's copies land before it goes
+        for (int i = max(0, n - kStages); i < n; ++i)
+          mbar_wait_bounded(bar(Smem::kv_full, i % kStages), (i / kStages) & 1, p.dev_err);
+        for (int x = 0; x < 2; ++x)
+          if (nq[x] > 0) mbar_wait_bounded(bar(Smem::q_full, x), (nq[x] - 1) & 1, p.dev_err);
+      }
+    } else if (warp == kMmaWarp) {
+      // ---- matrix products: the warp runs the loop together, one elected lane issues ---------
+      // (operands stay in uniform registers that way; a loop of one diverged lane took 85
+      // cycles to issue a product that runs for 64)
+      const uint32_t q_at = smem_u32(smem + Smem::q), kv_at = smem_u32(smem + Smem::kv);
+      const auto qk = [&](int x, int st) {   // S_x = Q_x K^T
+        const uint64_t qd = operand_desc(q_at + x * kTileBytes, 16, 1024);
+        const uint64_t kd = operand_desc(kv_at + st * kTileBytes, 16, 1024);
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t off = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
+            mma_ss(tmem + kColS + x * kTile, qd + off, kd + off, p.idesc_qk, k > 0);
+          }
+          mma_commit(bar(Smem::s_full, x));
+        }
+        __syncwarp();
+      };
+      const auto pv = [&](int x, int st, int half, bool acc) {   // O_x += P_x V, 64 tokens
+        const uint64_t vd = operand_desc(kv_at + st * kTileBytes, kHalfBytes, 1024);
+        if (elect_one()) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int k = 4 * half + i;
+            mma_ts(tmem + kColO + x * kTile, tmem + kColS + x * kTile + 8 * k,
+                   vd + k * (2048 >> 4), kIdescPv, acc || k > 0);
+          }
+        }
+        __syncwarp();
+      };
+      const auto commit = [&](uint64_t* b) {
+        if (elect_one()) mma_commit(b);
+        __syncwarp();
+      };
+      const auto full = [&](int i) {
+        return wait(bar(Smem::kv_full, i % kStages), (i / kStages) & 1);
+      };
+      int n = 0;                      // KV tiles taken from the ring
+      int nq[2] = {0, 0}, np[2] = {0, 0}, nclean = 0;
+      bool ok = true;
+      Unit u;
+      for (int k = 0; ok && next_unit(k, u); ++k) {
+        const Tail<BS> tail(u);
+        ok = full(n);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (!ok || u.end[x] == u.begin) continue;
+          ok = wait(bar(Smem::q_full, x), nq[x] & 1);
+          if (!ok) continue;
+          ++nq[x];
+          qk(x, n % kStages);
+          if (u.end[x] == u.begin + 1) commit(bar(Smem::q_empty, x));
+        }
+        commit(bar(Smem::kv_empty, n % kStages));
+        for (int j = u.begin; j < u.last && ok; ++j) {
+          const int nv = n + 1, nk = n + 2;
+          ok = full(nv);
+          if (ok && tail.clean && j == tail.tile) {
+            ok = wait(bar(Smem::v_clean, 0), nclean & 1);
+            ++nclean;
+          }
+          if (ok && j + 1 < u.last) ok = full(nk);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (!ok || j >= u.end[x]) continue;
+            ok = wait(bar(Smem::p_full, 2 * x), np[x] & 1);
+            if (!ok) continue;
+            fence_after();
+            pv(x, nv % kStages, 0, j > u.begin);
+            ok = wait(bar(Smem::p_full, 2 * x + 1), np[x] & 1);
+            if (!ok) continue;
+            ++np[x];
+            fence_after();
+            pv(x, nv % kStages, 1, true);
+            if (j + 1 < u.end[x]) {
+              qk(x, nk % kStages);
+              if (j + 2 == u.end[x]) commit(bar(Smem::q_empty, x));
+            } else {
+              commit(bar(Smem::o_full, x));
+            }
+          }
+          commit(bar(Smem::kv_empty, nv % kStages));
+          if (j + 1 < u.last) commit(bar(Smem::kv_empty, nk % kStages));
+          n += 2;
+        }
       }
       // every product has completed before the tensor memory is given back
-      mma_commit(bar(Smem::drained, 0));
+      commit(bar(Smem::drained, 0));
       mbar_wait_bounded(bar(Smem::drained, 0), 0, p.dev_err);
+      __syncwarp();
+    } else if (warp == kWorkWarp) {
+      // ---- work: the CTA's own unit, then those of CTAs that have not started -------------
+      if (blockIdx.x == 0 && blockIdx.y == 0)   // every entry is looked at once, used or not
+        for (int s = lane; s < p.num_seqs; s += 32)
+          packed_seq(p.query_start, p.context_lens, s, p.num_tokens, max_context, p.dev_err, true);
+      int bx = blockIdx.x, by = blockIdx.y;
+      bool ok = true;
+      int published = 0;
+      for (int tries = 0; ok; ++tries) {
+        Unit u;
+        const bool work = bx >= 0 && make_unit(p, bx, by, max_context, u);
+        if (bx < 0) u.begin = u.last = 0;   // tells the readers to stop
+        if (work || bx < 0) {
+          if (lane == 0) {
+            *reinterpret_cast<Unit*>(smem + Smem::unit) = u;
+            mbar_arrive(bar(Smem::unit_full, 0));
+          }
+          __syncwarp();
+          if (bx < 0) break;
+          ok = wait(bar(Smem::unit_empty, 0), published & 1);
+          ++published;
+          if (!ok) break;
+        }
+        if (lane == 0) {
+          fence_proxy_async_smem();   // the last answer has been read
+          mbar_arrive_expect_tx(bar(Smem::stolen, 0), 16);
+          asm volatile(
+              "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128"
+              " [%0], [%1];" ::"r"(smem_u32(smem + Smem::answer)),
+              "r"(smem_u32(bar(Smem::stolen, 0)))
+              : "memory");
+        }
+        __syncwarp();
+        ok = wait(bar(Smem::stolen, 0), tries & 1);
+        uint32_t got, ax, ay;
+        asm volatile(
+            "{\n .reg .pred p;\n .reg .b128 h;\n .reg .b32 z, w;\n ld.shared.b128 h, [%3];\n"
+            " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n"
+            " selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n mov.u32 %2, 0;\n"
+            " @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, z, w}, h;\n"
+            "}\n"
+            : "=r"(got), "=r"(ax), "=r"(ay)
+            : "r"(smem_u32(smem + Smem::answer))
+            : "memory");
+        __syncwarp();
+        bx = got ? static_cast<int>(ax) : -1;
+        by = static_cast<int>(ay);
+      }
     }
-    __syncwarp();
-  }
   } else {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-  if (u.end[warp >> 2] > u.begin) {
-    // ---- softmax: one thread per query row ----------------------------------------------
+    // ---- softmax: one thread per query row ------------------------------------------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int x = warp >> 2;
     const int r = threadIdx.x & (kTile - 1);
-    const int tok = u.tok0[x] + (r >> p.group_shift);
-    const int pos0 = u.seq.ctx - u.seq.n + u.tok0[x];             // of the tile's first row
-    const int pos = min(u.seq.ctx - u.seq.n + tok, u.seq.ctx - 1);
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + kColS + x * kTile;
     const uint32_t o_at = tmem + lanes + kColO + x * kTile;
     const float sc = p.scale_log2;
-    float m = kNoMax;
-    float2 l2 = make_float2(0.f, 0.f);
+    int ns = 0, no = 0;   // score tiles and outputs taken
     bool ok = true;
-    for (int j = u.begin; j < u.end[x]; ++j) {
-      const int it = j - u.begin;
-      ok = mbar_wait_bounded(bar(Smem::s_full, x), it & 1, p.dev_err);
-      ok = __all_sync(kFull, ok) != 0;
-      if (!ok) break;
-      fence_after();
-      float s[kTile];
+    Unit u;
+    for (int k = 0; ok && next_unit(k, u); ++k) {
+      if (u.end[x] == u.begin) continue;
+      const int tok = u.tok0[x] + (r >> p.group_shift);
+      const int pos0 = u.ctx - u.n + u.tok0[x];             // of the tile's first row
+      const int pos = min(u.ctx - u.n + tok, u.ctx - 1);
+      float m = kNoMax;
+      float2 l2 = make_float2(0.f, 0.f);
+      for (int j = u.begin; j < u.end[x]; ++j) {
+        ok = wait(bar(Smem::s_full, x), ns & 1);
+        if (!ok) break;
+        ++ns;
+        fence_after();
+        float s[kTile];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, reinterpret_cast<uint32_t*>(s + 32 * c));
-      wait_ld();
-      if (j * kTile + kTile - 1 > pos0) {   // some row of the tile does not see all of it
-        const int see = pos - j * kTile;    // columns 0 .. see
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, reinterpret_cast<uint32_t*>(s + 32 * c));
+        wait_ld();
+        if (j * kTile + kTile - 1 > pos0) {   // some row of the tile does not see all of it
+          const int see = pos - j * kTile;    // columns 0 .. see
 #pragma unroll
-        for (int c = 0; c < kTile; ++c) s[c] = c <= see ? s[c] : -INFINITY;
-      }
-      float mx[4] = {s[0], s[1], s[2], s[3]};
+          for (int c = 0; c < kTile; ++c) s[c] = c <= see ? s[c] : -INFINITY;
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-      for (int c = 4; c < kTile; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
-      const float bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-      // the maximum moves only when a score passes it by more than 2^8
-      const bool moves = bm > m + kRescale;
-      if (__any_sync(kFull, moves)) {
-        const float nm = moves ? bm : m;
-        const float alpha = exp2_approx(m - nm);
-        m = nm;
-        l2 = fmul2(l2, make_float2(alpha, alpha));
-        if (it > 0) {
-          // the scores of tile j follow the product of tile j - 1: O is at rest
+        for (int c = 4; c < kTile - 4; c += 8)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
-            tmem_ld32(o_at + 32 * c, o);
-            wait_ld();
+          for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], s[c + i], s[c + 4 + i]);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st32(o_at + 32 * c, o);
+        for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], s[kTile - 4 + i]);
+        const float bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+        // the maximum moves only when a score passes it by more than 2^8
+        const bool moves = bm > m + kRescale;
+        if (__any_sync(kFull, moves)) {
+          const float nm = moves ? bm : m;
+          const float alpha = exp2_approx(m - nm);
+          m = nm;
+          l2 = fmul2(l2, make_float2(alpha, alpha));
+          if (j > u.begin) {
+            // the scores of tile j follow the product of tile j - 1: O is at rest
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[32];
+              tmem_ld32(o_at + 32 * c, o);
+              wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(o_at + 32 * c, o);
+            }
           }
         }
-      }
-      const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-m, -m);
+        const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-m, -m);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t w[32];
+        for (int c = 0; c < 2; ++c) {   // the products start on the first half's weights
+          uint32_t w[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float2 e = ffma2(make_float2(s[64 * c + 2 * i], s[64 * c + 2 * i + 1]), sc2, nm2);
-          e.x = exp2_approx(e.x);
-          e.y = exp2_approx(e.y);
-          w[i] = pack_half2(e.x, e.y);
-          l2 = ffma2(e, make_float2(1.f, 1.f), l2);
+          for (int i = 0; i < 32; ++i) {
+            float2 e = ffma2(make_float2(s[64 * c + 2 * i], s[64 * c + 2 * i + 1]), sc2, nm2);
+            e.x = exp2_approx(e.x);
+            e.y = exp2_approx(e.y);
+            w[i] = pack_half2(e.x, e.y);
+            l2 = ffma2(e, make_float2(1.f, 1.f), l2);
+          }
+          tmem_st32(s_at + 32 * c, w);
+          wait_st();
+          fence_before();
+          mbar_arrive(bar(Smem::p_full, 2 * x + c));
         }
-        tmem_st32(s_at + 32 * c, w);
       }
-      wait_st();
-      fence_before();
-      mbar_arrive(bar(Smem::p_full, x));
-    }
-    if (ok) ok = mbar_wait_bounded(bar(Smem::o_full, x), 0, p.dev_err);
-    ok = __all_sync(kFull, ok) != 0;
-    if (ok) {
+      if (!ok) break;
+      ok = wait(bar(Smem::o_full, x), no & 1);
+      if (!ok) break;
+      ++no;
       fence_after();
       const float l = l2.x + l2.y;
       const int head = (u.g << p.group_shift) + (r & ((1 << p.group_shift) - 1));
-      const int64_t row = (static_cast<int64_t>(u.seq.row0) + tok) * p.num_q_heads + head;
-      const bool mine = tok < u.seq.n;
+      const int64_t row = (static_cast<int64_t>(u.row0) + tok) * p.num_q_heads + head;
+      const bool mine = tok < u.n;
       // rows whose tokens one unit covers are written, others leave a partial
       const bool whole = pos / kTile < p.split_tiles;
-      const bool direct = mine && whole && blockIdx.y == 0;
+      const bool direct = mine && whole && u.split == 0;
       const bool part = mine && !whole && pos / kTile >= u.begin;
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      const int64_t at = row * p.splits + blockIdx.y;
+      const int64_t at = row * p.splits + u.split;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t o[32];
@@ -460,9 +602,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 4; ++i) {
             uint32_t h[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              h[k] = pack_half2(__uint_as_float(o[8 * i + 2 * k]) * inv,
-                                __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
+            for (int e = 0; e < 4; ++e)
+              h[e] = pack_half2(__uint_as_float(o[8 * i + 2 * e]) * inv,
+                                __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
             dst[i] = make_uint4(h[0], h[1], h[2], h[3]);
           }
         } else if (part) {
@@ -476,8 +618,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         p.part_ml[2 * at] = m;
         p.part_ml[2 * at + 1] = l;
       }
+      fence_before();   // O is read: the next unit's products may overwrite it once its weights are there
     }
-  }
   }
   fence_before();
   __syncthreads();

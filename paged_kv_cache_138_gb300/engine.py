@@ -108,7 +108,7 @@ class DecodeStep:
 
     def _prepared(self, kind, i, stream, bufs, make):
         """The launch `kind` of layer i on (stream, bufs), marshalled once."""
-        key = (kind, i, ops._stream_handle(stream).value, id(bufs))
+        key = (kind, i, ops._stream_handle(stream), id(bufs))
         launch = self._launches.get(key)
         if launch is None:
             launch = self._launches[key] = make()
