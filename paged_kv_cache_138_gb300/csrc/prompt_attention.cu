@@ -23,7 +23,7 @@ constexpr int kHeadDim = 128;
 constexpr int kTile = 128;                       // rows of a query tile, tokens of a KV tile
 constexpr int kHalfBytes = kTile * 128;          // 128 rows x 64 dims, 128-byte swizzle
 constexpr int kTileBytes = 2 * kHalfBytes;
-constexpr int kStages = 5;                       // KV tiles in shared memory
+constexpr int kStages = 4;                       // KV tiles in shared memory
 constexpr int kThreads = 384;                    // 2 softmax warpgroups; copy, MMA and work warps
 // Registers a thread after the split: 256 * 224 + 128 * 56 = 384 * 168, what the
 // CTA was launched with (a softmax thread holds a row of 128 scores).
@@ -37,7 +37,8 @@ constexpr float kNoMax = -1e30f;
 struct Smem {
   static constexpr int q = 0;                            // two query tiles
   static constexpr int kv = q + 2 * kTileBytes;
-  static constexpr int bars = kv + kStages * kTileBytes;
+  static constexpr int stage = kv + kStages * kTileBytes;  // output rows, 4 KB a softmax warp
+  static constexpr int bars = stage + 8 * 4096;
   static constexpr int q_full = bars;                    // [2]
   static constexpr int q_empty = q_full + 16;            // [2] the tile's last score product is done
   static constexpr int kv_full = q_empty + 16;           // [kStages]
@@ -45,12 +46,12 @@ struct Smem {
   static constexpr int s_full = kv_empty + 8 * kStages;  // [2] scores of a tile are in TMEM
   static constexpr int p_full = s_full + 16;             // [2][2] a half's weights are in TMEM
   static constexpr int o_full = p_full + 32;             // [2] the tile's output is complete
-  static constexpr int v_clean = o_full + 16;            // rows past the context are zero
-  static constexpr int unit_full = v_clean + 8;          // the next unit is described
+  static constexpr int raw = o_full + 16;                // a V tile to be cleaned has landed
+  static constexpr int unit_full = raw + 8;              // the next unit is described
   static constexpr int unit_empty = unit_full + 8;       // and every warp has read it
   static constexpr int stolen = unit_empty + 8;          // the scheduler's answer is there
   static constexpr int drained = stolen + 8;
-  static constexpr int answer = (drained + 8 + 15) / 16 * 16;
+  static constexpr int answer = (drained + 16 + 15) / 16 * 16;
   static constexpr int unit = answer + 16;
   static constexpr int tmem = unit + 64;
   static constexpr int total = tmem + 16;
@@ -136,6 +137,25 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
       "r"(r[30]), "r"(r[31]), "r"(addr)
       : "memory");
+}
+
+// mbar_wait_bounded of a whole warp: one vote decides, so that no lane branches by
+// itself (30 cycles when the barrier is through already, 90 lane by lane).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* dev_err) {
+  constexpr unsigned kAll = 0xffffffffu;
+  if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
+    if ((i & 63) == 0) {
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) t0 = now;
+      if (__any_sync(kAll, now - t0 > kWaitLimitNs)) {
+        report(dev_err, PKV_DEV_WAIT_TIMEOUT);
+        return false;
+      }
+    }
+  }
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -231,13 +251,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr unsigned kFull = 0xffffffffu;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the same in every lane, which the compiler learns from the shuffle
+  const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int64_t max_context = BS ? static_cast<int64_t>(p.max_blocks) * BS : INT32_MAX;
   const auto bar = [&](int at, int i) { return reinterpret_cast<uint64_t*>(smem + at) + i; };
-  // a wait of a whole warp
-  const auto wait = [&](uint64_t* b, uint32_t parity) {
-    return __all_sync(kFull, mbar_wait_bounded(b, parity, p.dev_err)) != 0;
-  };
+  const auto wait = [&](uint64_t* b, uint32_t parity) { return warp_wait(b, parity, p.dev_err); };
   if (warp == kCopyWarp && lane == 0) {
     prefetch_tmap(&tmap_q);
     prefetch_tmap(&tmap_k);
@@ -246,15 +264,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(Smem::q_full, i), 1);
       mbar_init(bar(Smem::q_empty, i), 1);
       mbar_init(bar(Smem::s_full, i), 1);
-      mbar_init(bar(Smem::p_full, 2 * i), kTile);
-      mbar_init(bar(Smem::p_full, 2 * i + 1), kTile);
+      mbar_init(bar(Smem::p_full, 2 * i), 4);
+      mbar_init(bar(Smem::p_full, 2 * i + 1), 4);
       mbar_init(bar(Smem::o_full, i), 1);
     }
     for (int i = 0; i < kStages; ++i) {
       mbar_init(bar(Smem::kv_full, i), 1);
       mbar_init(bar(Smem::kv_empty, i), 1);
     }
-    mbar_init(bar(Smem::v_clean, 0), 1);
+    mbar_init(bar(Smem::raw, 0), 1);
     mbar_init(bar(Smem::unit_full, 0), 1);
     mbar_init(bar(Smem::unit_empty, 0), kReaders);
     mbar_init(bar(Smem::stolen, 0), 1);
@@ -286,8 +304,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kCopyWarp) {
       // ---- copies: Q, then K and V of each tile through a ring of kStages ----------------
       constexpr int kBoxes = BS ? kTile / (BS ? BS : 1) : 1;
-      int n = 0;                  // KV copies issued
-      int nq[2] = {0, 0};         // Q copies issued
+      int st = 0, round = 0, nraw = 0;   // ring position, cleaned tiles
+      int nq[2] = {0, 0};                // Q copies issued
       bool ok = true;
       Unit u;
       for (int k = 0; ok && next_unit(k, u); ++k) {
@@ -325,10 +343,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             row = static_cast<int>(r);
           }
           for (int kv = 0; kv < 2; ++kv) {
-            const int st = n % kStages;
-            if (n >= kStages) ok = wait(bar(Smem::kv_empty, st), (n / kStages - 1) & 1);
+            if (round > 0) ok = wait(bar(Smem::kv_empty, st), (round - 1) & 1);
             if (!ok) break;
-            uint64_t* b = bar(Smem::kv_full, st);
+            const bool dirty = kv == 1 && tail.clean && j == tail.tile;
+            uint64_t* b = dirty ? bar(Smem::raw, 0) : bar(Smem::kv_full, st);
             uint8_t* dst = smem + Smem::kv + st * kTileBytes;
             if (lane == 0) mbar_arrive_expect_tx(b, kTileBytes);
             __syncwarp();
@@ -338,110 +356,139 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_3d(dst + lane * kBoxBytes, m, 0, u.g, row, b);
               tma_load_3d(dst + kHalfBytes + lane * kBoxBytes, m, 64, u.g, row, b);
             }
-            if (kv == 1 && tail.clean && j == tail.tile) {
-              ok = wait(b, (n / kStages) & 1);
+            if (dirty) {
+              ok = wait(b, nraw & 1);
+              ++nraw;
               const uint32_t at = smem_u32(dst);
               for (int i = lane; ok && i < (tail.dirty_end - tail.valid) * 16; i += 32)
                 st_shared_zero16(at + (i & 8 ? kHalfBytes : 0) + (tail.valid + (i >> 4)) * 128 +
                                  (i & 7) * 16);
               fence_proxy_async_smem();
               __syncwarp();
-              if (lane == 0) mbar_arrive(bar(Smem::v_clean, 0));
+              if (lane == 0) mbar_arrive(bar(Smem::kv_full, st));
             }
-            ++n;
+            if (++st == kStages) {
+              st = 0;
+              ++round;
+            }
           }
         }
       }
       if (!ok) {   // a wait gave up: let this CTA's copies land before it goes
-        for (int i = max(0, n - kStages); i < n; ++i)
-          mbar_wait_bounded(bar(Smem::kv_full, i % kStages), (i / kStages) & 1, p.dev_err);
+        for (int i = 0; i < kStages; ++i) {
+          const int done = round + (i < st);   // copies into stage i
+          if (done > 0) mbar_wait_bounded(bar(Smem::kv_full, i), (done - 1) & 1, p.dev_err);
+        }
         for (int x = 0; x < 2; ++x)
           if (nq[x] > 0) mbar_wait_bounded(bar(Smem::q_full, x), (nq[x] - 1) & 1, p.dev_err);
       }
     } else if (warp == kMmaWarp) {
-      // ---- matrix products: the warp runs the loop together, one elected lane issues ---------
+      // ---- matrix products: the warp runs together, one elected lane issues ------------------
       // (operands stay in uniform registers that way; a loop of one diverged lane took 85
-      // cycles to issue a product that runs for 64)
-      const uint32_t q_at = smem_u32(smem + Smem::q), kv_at = smem_u32(smem + Smem::kv);
-      const auto qk = [&](int x, int st) {   // S_x = Q_x K^T
-        const uint64_t qd = operand_desc(q_at + x * kTileBytes, 16, 1024);
-        const uint64_t kd = operand_desc(kv_at + st * kTileBytes, 16, 1024);
+      // cycles to issue a product that runs for 64).  The tensor core holds some 7 products
+      // in its queue, and a wait takes about 100 cycles even when what it waits for is there:
+      // the waits for K and V are kept out of the stretch between one tile's products and
+      // the other's weights.  One warp issues for both tiles, a whole batch at a time: with a
+      // warp for each their products alternate, end together and the tiles fall into step
+      // (3400 cycles a pair of tiles instead of 2800).
+      struct Ring {
+        int st;
+        uint32_t round;
+        __device__ __forceinline__ Ring after() const {
+          return st + 1 == kStages ? Ring{0, round + 1} : Ring{st + 1, round};
+        }
+      };
+      const uint32_t s_col = tmem + kColS, o_col = tmem + kColO;
+      const uint64_t q_desc = operand_desc(smem_u32(smem + Smem::q), 16, 1024);
+      const uint64_t k_desc = operand_desc(smem_u32(smem + Smem::kv), 16, 1024);
+      const uint64_t v_desc = operand_desc(smem_u32(smem + Smem::kv), kHalfBytes, 1024);
+      const auto full = [&](Ring r) { return wait(bar(Smem::kv_full, r.st), r.round & 1); };
+      const auto commit = [&](uint64_t* b) {
+        if (elect_one()) mma_commit(b);
+        __syncwarp();
+      };
+      const auto qk = [&](int x, Ring r) {           // S_x = Q_x K^T
+        const uint64_t qd = q_desc + x * (kTileBytes >> 4), kd = k_desc + r.st * (kTileBytes >> 4);
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t off = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
-            mma_ss(tmem + kColS + x * kTile, qd + off, kd + off, p.idesc_qk, k > 0);
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t off = ((i >> 2) * kHalfBytes + (i & 3) * 32) >> 4;
+            mma_ss(s_col + x * kTile, qd + off, kd + off, p.idesc_qk, i > 0);
           }
           mma_commit(bar(Smem::s_full, x));
         }
         __syncwarp();
       };
-      const auto pv = [&](int x, int st, int half, bool acc) {   // O_x += P_x V, 64 tokens
-        const uint64_t vd = operand_desc(kv_at + st * kTileBytes, kHalfBytes, 1024);
+      const auto pv = [&](int x, Ring r, int half, bool acc) {   // O_x += P_x V, 64 tokens
+        const uint64_t vd = v_desc + r.st * (kTileBytes >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int k = 4 * half + i;
-            mma_ts(tmem + kColO + x * kTile, tmem + kColS + x * kTile + 8 * k,
-                   vd + k * (2048 >> 4), kIdescPv, acc || k > 0);
+            const int kk = 4 * half + i;
+            mma_ts(o_col + x * kTile, s_col + x * kTile + 8 * kk, vd + kk * (2048 >> 4), kIdescPv,
+                   acc || i > 0);
           }
         }
         __syncwarp();
       };
-      const auto commit = [&](uint64_t* b) {
-        if (elect_one()) mma_commit(b);
-        __syncwarp();
-      };
-      const auto full = [&](int i) {
-        return wait(bar(Smem::kv_full, i % kStages), (i / kStages) & 1);
-      };
-      int n = 0;                      // KV tiles taken from the ring
-      int nq[2] = {0, 0}, np[2] = {0, 0}, nclean = 0;
+      Ring ring = {0, 0};             // of the next tile to take
+      int nq[2] = {0, 0}, np[2] = {0, 0};   // query tiles and weight tiles taken
       bool ok = true;
       Unit u;
       for (int k = 0; ok && next_unit(k, u); ++k) {
-        const Tail<BS> tail(u);
-        ok = full(n);
+        ok = full(ring);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           if (!ok || u.end[x] == u.begin) continue;
           ok = wait(bar(Smem::q_full, x), nq[x] & 1);
           if (!ok) continue;
           ++nq[x];
-          qk(x, n % kStages);
+          qk(x, ring);
           if (u.end[x] == u.begin + 1) commit(bar(Smem::q_empty, x));
         }
-        commit(bar(Smem::kv_empty, n % kStages));
+        commit(bar(Smem::kv_empty, ring.st));
+        ring = ring.after();
+        bool v_there = false;
         for (int j = u.begin; j < u.last && ok; ++j) {
-          const int nv = n + 1, nk = n + 2;
-          ok = full(nv);
-          if (ok && tail.clean && j == tail.tile) {
-            ok = wait(bar(Smem::v_clean, 0), nclean & 1);
-            ++nclean;
-          }
-          if (ok && j + 1 < u.last) ok = full(nk);
+          const Ring rv = ring, rk = rv.after();
+          const bool more = j + 1 < u.last;
+          bool k_there = false;
+          if (!v_there) ok = full(rv);
+          v_there = false;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             if (!ok || j >= u.end[x]) continue;
             ok = wait(bar(Smem::p_full, 2 * x), np[x] & 1);
             if (!ok) continue;
             fence_after();
-            pv(x, nv % kStages, 0, j > u.begin);
-            ok = wait(bar(Smem::p_full, 2 * x + 1), np[x] & 1);
+            pv(x, rv, 0, j > u.begin);
+            if (more && !k_there) {
+              ok = full(rk);
+              k_there = true;
+            }
+            ok = wait(bar(Smem::p_full, 2 * x + 1), np[x] & 1) && ok;
             if (!ok) continue;
             ++np[x];
             fence_after();
-            pv(x, nv % kStages, 1, true);
+            pv(x, rv, 1, true);
             if (j + 1 < u.end[x]) {
-              qk(x, nk % kStages);
+              qk(x, rk);
               if (j + 2 == u.end[x]) commit(bar(Smem::q_empty, x));
             } else {
               commit(bar(Smem::o_full, x));
             }
+            if (x == 0 && more) {     // V of the next tile, if it is there already
+              const Ring r2 = rk.after();
+              v_there = __all_sync(kFull, mbar_try_wait(bar(Smem::kv_full, r2.st), r2.round & 1));
+            }
           }
-          commit(bar(Smem::kv_empty, nv % kStages));
-          if (j + 1 < u.last) commit(bar(Smem::kv_empty, nk % kStages));
-          n += 2;
+          commit(bar(Smem::kv_empty, rv.st));
+          ring = rk;
+          if (more) {
+            if (!k_there && ok) ok = full(rk);
+            commit(bar(Smem::kv_empty, rk.st));
+            ring = rk.after();
+          }
         }
       }
       // every product has completed before the tensor memory is given back
@@ -573,7 +620,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st32(s_at + 32 * c, w);
           wait_st();
           fence_before();
-          mbar_arrive(bar(Smem::p_full, 2 * x + c));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(Smem::p_full, 2 * x + c));
         }
       }
       if (!ok) break;
@@ -591,27 +639,57 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool part = mine && !whole && pos / kTile >= u.begin;
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const int64_t at = row * p.splits + u.split;
+      const uint32_t mine32 = __ballot_sync(kFull, direct);
+      // rows leave through the warp's 4 KB of shared memory, 64 dims at a time (16-byte
+      // chunk index XOR row % 8), so that a store covers whole 128-byte lines; rows of a
+      // thread each took 3700 cycles a tile and held up the other warps' loads
+      const uint32_t box = smem_u32(smem + Smem::stage + warp * 4096);
+      if (mine32) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t o[32];
-        tmem_ld32(o_at + 32 * c, o);
-        wait_ld();
-        if (direct) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + row * kHeadDim + 32 * c);
+        for (int c = 0; c < 2; ++c) {
+          uint32_t h[32];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t h[4];
+          for (int d = 0; d < 2; ++d) {
+            uint32_t o[32];
+            tmem_ld32(o_at + 64 * c + 32 * d, o);
+            wait_ld();
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              h[e] = pack_half2(__uint_as_float(o[8 * i + 2 * e]) * inv,
-                                __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
-            dst[i] = make_uint4(h[0], h[1], h[2], h[3]);
+            for (int i = 0; i < 16; ++i)
+              h[16 * d + i] = pack_half2(__uint_as_float(o[2 * i]) * inv,
+                                         __uint_as_float(o[2 * i + 1]) * inv);
           }
-        } else if (part) {
+          __syncwarp();   // the last half's rows have been read
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             box + lane * 128 + ((i ^ (lane & 7)) << 4)),
+                         "r"(h[4 * i]), "r"(h[4 * i + 1]), "r"(h[4 * i + 2]), "r"(h[4 * i + 3])
+                         : "memory");
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int rr = 4 * i + (lane >> 3), ch = lane & 7;   // row of the warp, chunk
+            const int64_t to = __shfl_sync(kFull, row, rr);
+            uint4 w;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                         : "r"(box + rr * 128 + ((ch ^ (rr & 7)) << 4))
+                         : "memory");
+            if (mine32 >> rr & 1)
+              *reinterpret_cast<uint4*>(p.out + to * kHeadDim + 64 * c + 8 * ch) = w;
+          }
+        }
+      }
+      if (__any_sync(kFull, part)) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          tmem_ld32(o_at + 32 * c, o);
+          wait_ld();
           uint4* dst = reinterpret_cast<uint4*>(p.part_o + at * kHeadDim + 32 * c);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            if (part) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
       }
       if (part) {
