@@ -140,22 +140,19 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
 }
 
 // mbar_wait_bounded of a whole warp: one vote decides, so that no lane branches by
-// itself (30 cycles when the barrier is through already, 90 lane by lane).
+// itself (30 cycles when the barrier is through already, 90 lane by lane), and the
+// limit is counted in clock cycles (2^30, half a second), which are quick to read.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* dev_err) {
   constexpr unsigned kAll = 0xffffffffu;
   if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
-  uint64_t t0 = 0;
-  for (uint32_t i = 1;; ++i) {
-    if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
-    if ((i & 63) == 0) {
-      const uint64_t now = global_timer_ns();
-      if (t0 == 0) t0 = now;
-      if (__any_sync(kAll, now - t0 > kWaitLimitNs)) {
-        report(dev_err, PKV_DEV_WAIT_TIMEOUT);
-        return false;
-      }
+  const uint32_t t0 = clock();
+  while (!__all_sync(kAll, mbar_try_wait(bar, parity))) {
+    if (__any_sync(kAll, static_cast<uint32_t>(clock()) - t0 > 1u << 30)) {
+      report(dev_err, PKV_DEV_WAIT_TIMEOUT);
+      return false;
     }
   }
+  return true;
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -179,7 +176,10 @@ constexpr uint32_t kNegateA = 1u << 13;
 
 // A piece of work: two query tiles of 128 rows of one KV head, row r of a tile
 // being token r / group, query head g * group + r % group, and the KV tiles
-// [begin, end) each attends to.
+// [begin, end) each attends to, taken from the last to the first: the masked
+// tiles come while the last unit's output is still being written, and both
+// query tiles end together.  Tile 0 holds the later tokens (its longer stretch
+// starts first).
 struct Unit {
   int row0, n, ctx, s;   // the sequence (see PackedSeq) and its index
   int g, split;
@@ -208,7 +208,7 @@ __device__ __forceinline__ bool make_unit(const Params& p, int bx, int by, int64
   if (!q.ok || nth < 0 || static_cast<int64_t>(nth) * per >= q.n) return false;
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
-    u.tok0[x] = nth * per + x * (kTile >> p.group_shift);
+    u.tok0[x] = nth * per + (1 - x) * (kTile >> p.group_shift);
     const int tok_end = min(q.n, u.tok0[x] + (kTile >> p.group_shift));
     u.end[x] = u.begin;
     if (tok_end > u.tok0[x]) {
@@ -325,7 +325,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                           u.row0 + u.tok0[x], b);
           }
         }
-        for (int j = u.begin; j < u.last && ok; ++j) {
+        int dirty = -1;   // ring position of a V tile to be cleaned
+        const auto clean = [&] {
+          if (dirty < 0) return;
+          ok = ok && wait(bar(Smem::raw, 0), nraw & 1);
+          ++nraw;
+          const uint32_t at = smem_u32(smem + Smem::kv + dirty * kTileBytes);
+          for (int i = lane; ok && i < (tail.dirty_end - tail.valid) * 16; i += 32)
+            st_shared_zero16(at + (i & 8 ? kHalfBytes : 0) + (tail.valid + (i >> 4)) * 128 +
+                             (i & 7) * 16);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(Smem::kv_full, dirty));
+          dirty = -1;
+        };
+        for (int j = u.last - 1; j >= u.begin && ok; --j) {
           int row = 0;
           if (BS == 0) {
             row = u.row0 + j * kTile;
@@ -342,11 +356,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             row = static_cast<int>(r);
           }
+#pragma unroll 1
           for (int kv = 0; kv < 2; ++kv) {
             if (round > 0) ok = wait(bar(Smem::kv_empty, st), (round - 1) & 1);
             if (!ok) break;
-            const bool dirty = kv == 1 && tail.clean && j == tail.tile;
-            uint64_t* b = dirty ? bar(Smem::raw, 0) : bar(Smem::kv_full, st);
+            const bool raw = kv == 1 && tail.clean && j == tail.tile;
+            uint64_t* b = raw ? bar(Smem::raw, 0) : bar(Smem::kv_full, st);
             uint8_t* dst = smem + Smem::kv + st * kTileBytes;
             if (lane == 0) mbar_arrive_expect_tx(b, kTileBytes);
             __syncwarp();
@@ -356,23 +371,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_3d(dst + lane * kBoxBytes, m, 0, u.g, row, b);
               tma_load_3d(dst + kHalfBytes + lane * kBoxBytes, m, 64, u.g, row, b);
             }
-            if (dirty) {
-              ok = wait(b, nraw & 1);
-              ++nraw;
-              const uint32_t at = smem_u32(dst);
-              for (int i = lane; ok && i < (tail.dirty_end - tail.valid) * 16; i += 32)
-                st_shared_zero16(at + (i & 8 ? kHalfBytes : 0) + (tail.valid + (i >> 4)) * 128 +
-                                 (i & 7) * 16);
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar(Smem::kv_full, st));
-            }
+            if (kv == 0) clean();   // with the next K on its way
+            if (raw) dirty = st;
             if (++st == kStages) {
               st = 0;
               ++round;
             }
           }
         }
+        clean();
       }
       if (!ok) {   // a wait gave up: let this CTA's copies land before it goes
         for (int i = 0; i < kStages; ++i) {
@@ -432,58 +439,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       };
       Ring ring = {0, 0};             // of the next tile to take
-      int nq[2] = {0, 0}, np[2] = {0, 0};   // query tiles and weight tiles taken
+      uint32_t q_parity = 0, p_parity = 0;   // bit x: of tile x's next query tile, weights
       bool ok = true;
       Unit u;
       for (int k = 0; ok && next_unit(k, u); ++k) {
-        ok = full(ring);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (!ok || u.end[x] == u.begin) continue;
-          ok = wait(bar(Smem::q_full, x), nq[x] & 1);
-          if (!ok) continue;
-          ++nq[x];
-          qk(x, ring);
-          if (u.end[x] == u.begin + 1) commit(bar(Smem::q_empty, x));
-        }
-        commit(bar(Smem::kv_empty, ring.st));
-        ring = ring.after();
         bool v_there = false;
-        for (int j = u.begin; j < u.last && ok; ++j) {
-          const Ring rv = ring, rk = rv.after();
-          const bool more = j + 1 < u.last;
+        // tile j's K gives scores, then tile j + 1's weights meet their V: one turn
+        for (int j = u.last; j >= u.begin && ok; --j) {
+          // j == u.last: only the first scores; j == u.begin: only the last outputs
+          const bool first = j == u.last, more = j > u.begin;
+          const Ring rv = ring, rk = first ? ring : ring.after();
           bool k_there = false;
-          if (!v_there) ok = full(rv);
+          if (!first && !v_there) ok = full(rv);
           v_there = false;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            if (!ok || j >= u.end[x]) continue;
-            ok = wait(bar(Smem::p_full, 2 * x), np[x] & 1);
-            if (!ok) continue;
-            fence_after();
-            pv(x, rv, 0, j > u.begin);
+            if (!ok || u.end[x] == u.begin || j > u.end[x]) continue;
+            const bool starts = j == u.end[x];
+            if (!starts) {
+              ok = wait(bar(Smem::p_full, 2 * x), p_parity >> x & 1);
+              if (!ok) continue;
+              fence_after();
+              pv(x, rv, 0, j + 1 < u.end[x]);
+            }
             if (more && !k_there) {
               ok = full(rk);
               k_there = true;
             }
-            ok = wait(bar(Smem::p_full, 2 * x + 1), np[x] & 1) && ok;
-            if (!ok) continue;
-            ++np[x];
-            fence_after();
-            pv(x, rv, 1, true);
-            if (j + 1 < u.end[x]) {
+            if (starts) {
+              ok = ok && wait(bar(Smem::q_full, x), q_parity >> x & 1);
+              if (!ok) continue;
+              q_parity ^= 1u << x;
+            } else {
+              ok = wait(bar(Smem::p_full, 2 * x + 1), p_parity >> x & 1) && ok;
+              if (!ok) continue;
+              p_parity ^= 1u << x;
+              fence_after();
+              pv(x, rv, 1, true);
+            }
+            if (more) {
               qk(x, rk);
-              if (j + 2 == u.end[x]) commit(bar(Smem::q_empty, x));
+              if (j == u.begin + 1) commit(bar(Smem::q_empty, x));
             } else {
               commit(bar(Smem::o_full, x));
             }
-            if (x == 0 && more) {     // V of the next tile, if it is there already
+            if (x == 0 && more) {     // V of tile j, if it is there already
               const Ring r2 = rk.after();
               v_there = __all_sync(kFull, mbar_try_wait(bar(Smem::kv_full, r2.st), r2.round & 1));
             }
           }
-          commit(bar(Smem::kv_empty, rv.st));
-          ring = rk;
+          if (!first) {
+            commit(bar(Smem::kv_empty, rv.st));
+            ring = rk;
+          }
           if (more) {
             if (!k_there && ok) ok = full(rk);
             commit(bar(Smem::kv_empty, rk.st));
@@ -563,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pos = min(u.ctx - u.n + tok, u.ctx - 1);
       float m = kNoMax;
       float2 l2 = make_float2(0.f, 0.f);
-      for (int j = u.begin; j < u.end[x]; ++j) {
+      for (int j = u.end[x] - 1; j >= u.begin; --j) {
         ok = wait(bar(Smem::s_full, x), ns & 1);
         if (!ok) break;
         ++ns;
@@ -573,9 +581,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, reinterpret_cast<uint32_t*>(s + 32 * c));
         wait_ld();
         if (j * kTile + kTile - 1 > pos0) {   // some row of the tile does not see all of it
-          const int see = pos - j * kTile;    // columns 0 .. see
+          const int see = pos - j * kTile;    // columns 0 .. see; lane 0 sees the fewest
+          const int all = __shfl_sync(kFull, see, 0);
 #pragma unroll
-          for (int c = 0; c < kTile; ++c) s[c] = c <= see ? s[c] : -INFINITY;
+          for (int q = 0; q < kTile; q += 32) {
+            if (q + 31 > all) {
+              // one bit a column: a predicate each comes from eight bits at a time
+              const uint32_t bits = see < q ? 0u : 0xffffffffu >> max(0, 31 - (see - q));
+#pragma unroll
+              for (int c = 0; c < 32; ++c) s[q + c] = bits >> c & 1 ? s[q + c] : -INFINITY;
+            }
+          }
         }
         float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -592,9 +608,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float alpha = exp2_approx(m - nm);
           m = nm;
           l2 = fmul2(l2, make_float2(alpha, alpha));
-          if (j > u.begin) {
-            // the scores of tile j follow the product of tile j - 1: O is at rest
-#pragma unroll
+          if (j + 1 < u.end[x]) {
+            // the scores of a tile follow the product of the one before it: O is at rest
+#pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               uint32_t o[32];
               tmem_ld32(o_at + 32 * c, o);
@@ -643,45 +659,49 @@ __global__ void __launch_bounds__(kThreads, 1)
       // rows leave through the warp's 4 KB of shared memory, 64 dims at a time (16-byte
       // chunk index XOR row % 8), so that a store covers whole 128-byte lines; rows of a
       // thread each took 3700 cycles a tile and held up the other warps' loads
-      const uint32_t box = smem_u32(smem + Smem::stage + warp * 4096);
+      uint4* box = reinterpret_cast<uint4*>(smem + Smem::stage + warp * 4096);
       if (mine32) {
+        // the lane's part of the stores: rows 4 i + lane / 8 of the warp, chunk lane % 8
+        const int r4 = (warp & 3) * 32 + (lane >> 3), ch = lane & 7;
+        __half* dst[8];
 #pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rr = r4 + 4 * i;
+          const int64_t to = (static_cast<int64_t>(u.row0) + u.tok0[x] + (rr >> p.group_shift)) *
+                                 p.num_q_heads +
+                             (u.g << p.group_shift) + (rr & ((1 << p.group_shift) - 1));
+          dst[i] = p.out + to * kHeadDim + 8 * ch;
+        }
+#pragma unroll 1
         for (int c = 0; c < 2; ++c) {
+          uint32_t o[64];
+          tmem_ld32(o_at + 64 * c, o);
+          tmem_ld32(o_at + 64 * c + 32, o + 32);
+          wait_ld();
           uint32_t h[32];
 #pragma unroll
-          for (int d = 0; d < 2; ++d) {
-            uint32_t o[32];
-            tmem_ld32(o_at + 64 * c + 32 * d, o);
-            wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              h[16 * d + i] = pack_half2(__uint_as_float(o[2 * i]) * inv,
-                                         __uint_as_float(o[2 * i + 1]) * inv);
-          }
+          for (int i = 0; i < 32; ++i)
+            h[i] = pack_half2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
           __syncwarp();   // the last half's rows have been read
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             box + lane * 128 + ((i ^ (lane & 7)) << 4)),
-                         "r"(h[4 * i]), "r"(h[4 * i + 1]), "r"(h[4 * i + 2]), "r"(h[4 * i + 3])
-                         : "memory");
+            box[lane * 8 + (i ^ (lane & 7))] =
+                make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
           __syncwarp();
+          uint4 w[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int rr = 4 * i + (lane >> 3), ch = lane & 7;   // row of the warp, chunk
-            const int64_t to = __shfl_sync(kFull, row, rr);
-            uint4 w;
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                         : "r"(box + rr * 128 + ((ch ^ (rr & 7)) << 4))
-                         : "memory");
-            if (mine32 >> rr & 1)
-              *reinterpret_cast<uint4*>(p.out + to * kHeadDim + 64 * c + 8 * ch) = w;
+            const int rr = 4 * i + (lane >> 3);
+            w[i] = box[rr * 8 + (ch ^ (rr & 7))];
           }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (mine32 >> (4 * i + (lane >> 3)) & 1)
+              *reinterpret_cast<uint4*>(dst[i] + 64 * c) = w[i];
         }
       }
       if (__any_sync(kFull, part)) {
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t o[32];
           tmem_ld32(o_at + 32 * c, o);
