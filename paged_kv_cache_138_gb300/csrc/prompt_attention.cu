@@ -139,6 +139,33 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       : "memory");
 }
 
+// store a box from shared memory; the buffer may be written again after bulk_wait_read()
+__device__ __forceinline__ void tma_store_3d(const void* tmap, const void* smem_src, int c0, int c1,
+                                             int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(smem_u32(smem_src)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
 // mbar_wait_bounded of a whole warp: one vote decides, so that no lane branches by
 // itself (30 cycles when the barrier is through already, 90 lane by lane), and the
 // limit is counted in clock cycles (2^30, half a second), which are quick to read.
@@ -247,7 +274,8 @@ template <int BS>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                             const __grid_constant__ CUtensorMap tmap_k,
-                            const __grid_constant__ CUtensorMap tmap_v, const Params p) {
+                            const __grid_constant__ CUtensorMap tmap_v,
+                            const __grid_constant__ CUtensorMap tmap_o, const Params p) {
   constexpr unsigned kFull = 0xffffffffu;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -310,21 +338,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       Unit u;
       for (int k = 0; ok && next_unit(k, u); ++k) {
         const Tail<BS> tail(u);
+        const auto copy_q = [&] {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (!ok || u.end[x] == u.begin) continue;
-          if (nq[x] > 0) ok = wait(bar(Smem::q_empty, x), (nq[x] - 1) & 1);
-          if (!ok) continue;
-          ++nq[x];
-          if (lane == 0) {
-            uint64_t* b = bar(Smem::q_full, x);
-            uint8_t* dst = smem + Smem::q + x * kTileBytes;
-            mbar_arrive_expect_tx(b, kTileBytes);
-            for (int h = 0; h < 2; ++h)
-              tma_load_3d(dst + h * kHalfBytes, &tmap_q, 64 * h, u.g << p.group_shift,
-                          u.row0 + u.tok0[x], b);
+          for (int x = 0; x < 2; ++x) {
+            if (!ok || u.end[x] == u.begin) continue;
+            if (nq[x] > 0) ok = wait(bar(Smem::q_empty, x), (nq[x] - 1) & 1);
+            if (!ok) continue;
+            ++nq[x];
+            if (lane == 0) {
+              uint64_t* b = bar(Smem::q_full, x);
+              uint8_t* dst = smem + Smem::q + x * kTileBytes;
+              mbar_arrive_expect_tx(b, kTileBytes);
+              for (int h = 0; h < 2; ++h)
+                tma_load_3d(dst + h * kHalfBytes, &tmap_q, 64 * h, u.g << p.group_shift,
+                            u.row0 + u.tok0[x], b);
+            }
           }
-        }
+        };
         int dirty = -1;   // ring position of a V tile to be cleaned
         const auto clean = [&] {
           if (dirty < 0) return;
@@ -372,6 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_3d(dst + kHalfBytes + lane * kBoxBytes, m, 64, u.g, row, b);
             }
             if (kv == 0) clean();   // with the next K on its way
+            if (kv == 0 && j == u.last - 1) copy_q();
             if (raw) dirty = st;
             if (++st == kStages) {
               st = 0;
@@ -414,89 +445,120 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) mma_commit(b);
         __syncwarp();
       };
-      const auto qk = [&](int x, Ring r) {           // S_x = Q_x K^T
-        const uint64_t qd = q_desc + x * (kTileBytes >> 4), kd = k_desc + r.st * (kTileBytes >> 4);
-        if (elect_one()) {
+      // O_x += P_x V over the first (h0) and last 64 tokens, S_x = Q_x K^T
+      const auto pv4 = [&](int x, int half, uint64_t vd, bool acc) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t off = ((i >> 2) * kHalfBytes + (i & 3) * 32) >> 4;
-            mma_ss(s_col + x * kTile, qd + off, kd + off, p.idesc_qk, i > 0);
-          }
-          mma_commit(bar(Smem::s_full, x));
+        for (int i = 0; i < 4; ++i) {
+          const int kk = 4 * half + i;
+          mma_ts(o_col + x * kTile, s_col + x * kTile + 8 * kk, vd + kk * (2048 >> 4), kIdescPv,
+                 acc || i > 0);
         }
-        __syncwarp();
       };
-      const auto pv = [&](int x, Ring r, int half, bool acc) {   // O_x += P_x V, 64 tokens
-        const uint64_t vd = v_desc + r.st * (kTileBytes >> 4);
-        if (elect_one()) {
+      const auto qk8 = [&](int x, uint64_t kd) {
+        const uint64_t qd = q_desc + x * (kTileBytes >> 4);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int kk = 4 * half + i;
-            mma_ts(o_col + x * kTile, s_col + x * kTile + 8 * kk, vd + kk * (2048 >> 4), kIdescPv,
-                   acc || i > 0);
-          }
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t off = ((i >> 2) * kHalfBytes + (i & 3) * 32) >> 4;
+          mma_ss(s_col + x * kTile, qd + off, kd + off, p.idesc_qk, i > 0);
         }
-        __syncwarp();
+        mma_commit(bar(Smem::s_full, x));
       };
+      const auto k_at = [&](Ring r) { return k_desc + r.st * (kTileBytes >> 4); };
+      const auto v_at = [&](Ring r) { return v_desc + r.st * (kTileBytes >> 4); };
       Ring ring = {0, 0};             // of the next tile to take
       uint32_t q_parity = 0, p_parity = 0;   // bit x: of tile x's next query tile, weights
       bool ok = true;
       Unit u;
       for (int k = 0; ok && next_unit(k, u); ++k) {
         bool v_there = false;
-        // tile j's K gives scores, then tile j + 1's weights meet their V: one turn
-        for (int j = u.last; j >= u.begin && ok; --j) {
-          // j == u.last: only the first scores; j == u.begin: only the last outputs
+        // turn j: tile j - 1's K gives scores, tile j's weights meet their V
+        // (j == u.last: only the first scores; j == u.begin: only the last outputs)
+        int j = u.last;
+        const int both = min(u.end[0], u.end[1]);
+        while (j >= u.begin && ok) {
+          const Ring rv = ring, rk = j == u.last ? ring : ring.after();
+          if (j < both && j > u.begin) {
+            // both tiles in full swing
+            if (!v_there) ok = full(rv);
+            const uint64_t vd = v_at(rv), kd = k_at(rk);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              ok = wait(bar(Smem::p_full, 2 * x), p_parity >> x & 1) && ok;
+              fence_after();
+              if (elect_one()) pv4(x, 0, vd, j + 1 < u.end[x]);
+              __syncwarp();
+              if (x == 0) ok = full(rk) && ok;
+              ok = wait(bar(Smem::p_full, 2 * x + 1), p_parity >> x & 1) && ok;
+              if (!ok) break;
+              fence_after();
+              if (elect_one()) {
+                pv4(x, 1, vd, true);
+                qk8(x, kd);
+              }
+              __syncwarp();
+              if (x == 0) {           // V of tile j - 1, if it is there already
+                const Ring r2 = rk.after();
+                v_there = __all_sync(kFull, mbar_test_wait(bar(Smem::kv_full, r2.st), r2.round & 1));
+              }
+            }
+            if (!ok) break;
+            p_parity ^= 3u;
+            if (elect_one()) {
+              if (j == u.begin + 1) {
+                mma_commit(bar(Smem::q_empty, 0));
+                mma_commit(bar(Smem::q_empty, 1));
+              }
+              mma_commit(bar(Smem::kv_empty, rv.st));
+              mma_commit(bar(Smem::kv_empty, rk.st));
+            }
+            __syncwarp();
+            ring = rk.after();
+            --j;
+            continue;
+          }
+          // a turn in which a tile starts, ends or has no part
           const bool first = j == u.last, more = j > u.begin;
-          const Ring rv = ring, rk = first ? ring : ring.after();
-          bool k_there = false;
           if (!first && !v_there) ok = full(rv);
           v_there = false;
+          if (more && ok) ok = full(rk);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             if (!ok || u.end[x] == u.begin || j > u.end[x]) continue;
             const bool starts = j == u.end[x];
-            if (!starts) {
-              ok = wait(bar(Smem::p_full, 2 * x), p_parity >> x & 1);
-              if (!ok) continue;
-              fence_after();
-              pv(x, rv, 0, j + 1 < u.end[x]);
-            }
-            if (more && !k_there) {
-              ok = full(rk);
-              k_there = true;
-            }
             if (starts) {
-              ok = ok && wait(bar(Smem::q_full, x), q_parity >> x & 1);
+              ok = wait(bar(Smem::q_full, x), q_parity >> x & 1);
               if (!ok) continue;
               q_parity ^= 1u << x;
             } else {
-              ok = wait(bar(Smem::p_full, 2 * x + 1), p_parity >> x & 1) && ok;
+              ok = wait(bar(Smem::p_full, 2 * x), p_parity >> x & 1) &&
+                   wait(bar(Smem::p_full, 2 * x + 1), p_parity >> x & 1);
               if (!ok) continue;
               p_parity ^= 1u << x;
               fence_after();
-              pv(x, rv, 1, true);
             }
-            if (more) {
-              qk(x, rk);
-              if (j == u.begin + 1) commit(bar(Smem::q_empty, x));
-            } else {
-              commit(bar(Smem::o_full, x));
+            if (elect_one()) {
+              if (!starts) {
+                pv4(x, 0, v_at(rv), j + 1 < u.end[x]);
+                pv4(x, 1, v_at(rv), true);
+              }
+              if (more) {
+                qk8(x, k_at(rk));
+                if (j == u.begin + 1) mma_commit(bar(Smem::q_empty, x));
+              } else {
+                mma_commit(bar(Smem::o_full, x));
+              }
             }
-            if (x == 0 && more) {     // V of tile j, if it is there already
-              const Ring r2 = rk.after();
-              v_there = __all_sync(kFull, mbar_try_wait(bar(Smem::kv_full, r2.st), r2.round & 1));
-            }
+            __syncwarp();
           }
           if (!first) {
             commit(bar(Smem::kv_empty, rv.st));
             ring = rk;
           }
           if (more) {
-            if (!k_there && ok) ok = full(rk);
             commit(bar(Smem::kv_empty, rk.st));
             ring = rk.after();
           }
+          --j;
         }
       }
       // every product has completed before the tensor memory is given back
@@ -584,14 +646,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int see = pos - j * kTile;    // columns 0 .. see; lane 0 sees the fewest
           const int all = __shfl_sync(kFull, see, 0);
 #pragma unroll
-          for (int q = 0; q < kTile; q += 32) {
-            if (q + 31 > all) {
-              // one bit a column: a predicate each comes from eight bits at a time
-              const uint32_t bits = see < q ? 0u : 0xffffffffu >> max(0, 31 - (see - q));
+          for (int q = 0; q < kTile; q += 32)
+            if (q + 31 > all)
 #pragma unroll
-              for (int c = 0; c < 32; ++c) s[q + c] = bits >> c & 1 ? s[q + c] : -INFINITY;
-            }
-          }
+              for (int c = q; c < q + 32; ++c) s[c] = c <= see ? s[c] : -INFINITY;
         }
         float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -657,47 +715,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t at = row * p.splits + u.split;
       const uint32_t mine32 = __ballot_sync(kFull, direct);
       // rows leave through the warp's 4 KB of shared memory, 64 dims at a time (16-byte
-      // chunk index XOR row % 8), so that a store covers whole 128-byte lines; rows of a
-      // thread each took 3700 cycles a tile and held up the other warps' loads
+      // chunk index XOR row % 8, as the copy engine reads them), while the warp goes on to
+      // the next unit; stores of its own took 3700 cycles a tile (a row for each thread) or
+      // 2700 (whole lines)
       uint4* box = reinterpret_cast<uint4*>(smem + Smem::stage + warp * 4096);
       if (mine32) {
-        // the lane's part of the stores: rows 4 i + lane / 8 of the warp, chunk lane % 8
-        const int r4 = (warp & 3) * 32 + (lane >> 3), ch = lane & 7;
-        __half* dst[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int rr = r4 + 4 * i;
-          const int64_t to = (static_cast<int64_t>(u.row0) + u.tok0[x] + (rr >> p.group_shift)) *
-                                 p.num_q_heads +
-                             (u.g << p.group_shift) + (rr & ((1 << p.group_shift) - 1));
-          dst[i] = p.out + to * kHeadDim + 8 * ch;
-        }
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
           uint32_t o[64];
           tmem_ld32(o_at + 64 * c, o);
           tmem_ld32(o_at + 64 * c + 32, o + 32);
+          if (lane == 0) bulk_wait_read();   // the last rows have left the buffer
+          __syncwarp();
           wait_ld();
           uint32_t h[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             h[i] = pack_half2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
-          __syncwarp();   // the last half's rows have been read
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             box[lane * 8 + (i ^ (lane & 7))] =
                 make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+          fence_proxy_async_smem();
           __syncwarp();
-          uint4 w[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int rr = 4 * i + (lane >> 3);
-            w[i] = box[rr * 8 + (ch ^ (rr & 7))];
+          if (mine32 == kFull) {
+            if (lane == 0)
+              tma_store_3d(&tmap_o, box, 64 * c, u.g << p.group_shift,
+                           u.row0 + u.tok0[x] + ((warp & 3) * 32 >> p.group_shift));
+          } else {   // the sequence's last rows: only those
+            for (int i = 0; i < 8; ++i) {
+              const int rr = 4 * i + (lane >> 3), ch = lane & 7;
+              const int64_t to = __shfl_sync(kFull, row, rr);
+              if (mine32 >> rr & 1)
+                *reinterpret_cast<uint4*>(p.out + to * kHeadDim + 64 * c + 8 * ch) =
+                    box[rr * 8 + (ch ^ (rr & 7))];
+            }
+            __syncwarp();
           }
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (mine32 >> (4 * i + (lane >> 3)) & 1)
-              *reinterpret_cast<uint4*>(dst[i] + 64 * c) = w[i];
         }
       }
       if (__any_sync(kFull, part)) {
@@ -718,6 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_before();   // O is read: the next unit's products may overwrite it once its weights are there
     }
+    if (lane == 0) bulk_wait();
   }
   fence_before();
   __syncthreads();
@@ -784,8 +839,8 @@ bool make_map(CUtensorMap* map, const void* base, int heads, int64_t rows, int b
 }
 
 template <int BS>
-int launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const Params& p,
-           int64_t units, cudaStream_t st) {
+int launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+           const CUtensorMap& mo, const Params& p, int64_t units, cudaStream_t st) {
   static std::atomic<uint8_t> opted_in[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
@@ -798,7 +853,7 @@ int launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, 
   }
   prompt_attention_kernel<BS>
       <<<dim3(static_cast<unsigned>(units * p.num_kv_heads), p.splits), kThreads, Smem::alloc, st>>>(
-          mq, mk, mv, p);
+          mq, mk, mv, mo, p);
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
@@ -873,20 +928,21 @@ int run(void* out, const void* q, const void* k, const void* v, const int32_t* b
   p.idesc_qk = kIdescBase | (scale < 0.f ? kNegateA : 0u);
   p.scale_log2 = std::max(1e-30f, (scale < 0.f ? -scale : scale) * 1.4426950408889634f);
 
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mk, mv, mo;
   const int64_t rows = paged ? num_blocks * block_size : num_tokens;
   const int box = paged ? block_size : kTile;
   if (!make_map(&mq, q, num_q_heads, num_tokens, 1 << shift, kTile >> shift) ||
+      !make_map(&mo, out, num_q_heads, num_tokens, 1 << shift, 32 >> shift) ||
       !make_map(&mk, k, num_kv_heads, rows, 1, box) || !make_map(&mv, v, num_kv_heads, rows, 1, box))
     return PKV_ERR_CUDA;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   int rc;
   switch (block_size) {
-    case 0: rc = launch<0>(mq, mk, mv, p, units, st); break;
-    case 8: rc = launch<8>(mq, mk, mv, p, units, st); break;
-    case 16: rc = launch<16>(mq, mk, mv, p, units, st); break;
-    case 32: rc = launch<32>(mq, mk, mv, p, units, st); break;
-    default: rc = launch<64>(mq, mk, mv, p, units, st); break;
+    case 0: rc = launch<0>(mq, mk, mv, mo, p, units, st); break;
+    case 8: rc = launch<8>(mq, mk, mv, mo, p, units, st); break;
+    case 16: rc = launch<16>(mq, mk, mv, mo, p, units, st); break;
+    case 32: rc = launch<32>(mq, mk, mv, mo, p, units, st); break;
+    default: rc = launch<64>(mq, mk, mv, mo, p, units, st); break;
   }
   if (rc != PKV_OK || p.splits == 1) return rc;
   const int64_t all = static_cast<int64_t>(num_tokens) * num_q_heads;
