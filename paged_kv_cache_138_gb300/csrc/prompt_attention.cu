@@ -38,7 +38,9 @@ struct Smem {
   static constexpr int q = 0;                            // two query tiles
   static constexpr int kv = q + 2 * kTileBytes;
   static constexpr int stage = kv + kStages * kTileBytes;  // output rows, 4 KB a softmax warp
-  static constexpr int bars = stage + 8 * 4096;
+  static constexpr int lm = stage + 8 * 4096;            // float2 [128]: sums and maxima of a
+                                                         // row that both warpgroups work on
+  static constexpr int bars = lm + kTile * 8;
   static constexpr int q_full = bars;                    // [2]
   static constexpr int q_empty = q_full + 16;            // [2] the tile's last score product is done
   static constexpr int kv_full = q_empty + 16;           // [kStages]
@@ -46,7 +48,9 @@ struct Smem {
   static constexpr int s_full = kv_empty + 8 * kStages;  // [2] scores of a tile are in TMEM
   static constexpr int p_full = s_full + 16;             // [2][2] a half's weights are in TMEM
   static constexpr int o_full = p_full + 32;             // [2] the tile's output is complete
-  static constexpr int raw = o_full + 16;                // a V tile to be cleaned has landed
+  static constexpr int lm_full = o_full + 16;            // lm is written
+  static constexpr int lm_free = lm_full + 8;            // and read, tile 1's output too
+  static constexpr int raw = lm_free + 8;                // a V tile to be cleaned has landed
   static constexpr int unit_full = raw + 8;              // the next unit is described
   static constexpr int unit_empty = unit_full + 8;       // and every warp has read it
   static constexpr int stolen = unit_empty + 8;          // the scheduler's answer is there
@@ -207,12 +211,18 @@ constexpr uint32_t kNegateA = 1u << 13;
 // tiles come while the last unit's output is still being written, and both
 // query tiles end together.  Tile 0 holds the later tokens (its longer stretch
 // starts first).
-struct Unit {
+// A unit with rows in one tile only (a short chunk, the rest of a prompt) is a
+// pair: both warpgroups work on tile 0's rows, on every other KV tile each, and
+// the first joins the two results.  Alone a tile waits for its own products and
+// weights in turn, 3100 cycles a KV tile instead of 1200.
+struct alignas(16) Unit {
   int row0, n, ctx, s;   // the sequence (see PackedSeq) and its index
   int g, split;
   int tok0[2];           // first token of each tile (among the sequence's packed rows)
   int end[2];
   int begin, last;       // KV tiles of the unit; last == begin: no more work
+  int pair;
+  __device__ __forceinline__ bool has(int x) const { return pair || end[x] > begin; }
 };
 static_assert(sizeof(Unit) <= 64 && sizeof(Unit) % 16 == 0, "a unit's place in shared memory");
 
@@ -243,6 +253,12 @@ __device__ __forceinline__ bool make_unit(const Params& p, int bx, int by, int64
       u.end[x] = max(u.begin, min(u.begin + p.split_tiles, last_pos / kTile + 1));
     }
     u.last = max(u.last, u.end[x]);
+  }
+  u.pair = (u.end[0] == u.begin || u.end[1] == u.begin) && u.last - u.begin >= 2;
+  if (u.pair) {
+    u.tok0[0] = u.tok0[1] = u.end[0] > u.begin ? u.tok0[0] : u.tok0[1];
+    u.end[0] = u.last;
+    u.end[1] = u.begin;
   }
   return u.last > u.begin;
 }
@@ -300,6 +316,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(Smem::kv_full, i), 1);
       mbar_init(bar(Smem::kv_empty, i), 1);
     }
+    mbar_init(bar(Smem::lm_full, 0), 4);
+    mbar_init(bar(Smem::lm_free, 0), 4);
     mbar_init(bar(Smem::raw, 0), 1);
     mbar_init(bar(Smem::unit_full, 0), 1);
     mbar_init(bar(Smem::unit_empty, 0), kReaders);
@@ -313,6 +331,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+  // launched as a programmatic dependent of the stream's previous kernel: nothing is
+  // read before this wait, which returns once that kernel's writes are visible
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   fence_before();
   __syncthreads();
   fence_after();
@@ -369,46 +390,69 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(bar(Smem::kv_full, dirty));
           dirty = -1;
         };
-        for (int j = u.last - 1; j >= u.begin && ok; --j) {
-          int row = 0;
-          if (BS == 0) {
-            row = u.row0 + j * kTile;
-          } else if (lane < kBoxes) {
-            const int tok = j * kTile + lane * BS;
-            int64_t r = p.num_blocks * BS;   // past the last row: zeros
-            if (tok < u.ctx) {
-              const int32_t b = __ldg(p.block_tables + static_cast<int64_t>(u.s) * p.max_blocks +
-                                      tok / (BS ? BS : 1));
-              if (b < 0 || b >= p.num_blocks)
-                report(p.dev_err, PKV_DEV_BAD_BLOCK_ID);
-              else
-                r = static_cast<int64_t>(b) * BS;
-            }
-            row = static_cast<int>(r);
+        // the block id of this lane's part of tile j (paged): loaded ahead, looked at when
+        // the tile's turn comes
+        const auto id_of = [&](int j) {
+          const int tok = j * kTile + lane * BS;
+          return BS && lane < kBoxes && j >= u.begin && tok < u.ctx
+                     ? __ldg(p.block_tables + static_cast<int64_t>(u.s) * p.max_blocks +
+                             tok / (BS ? BS : 1))
+                     : -1;
+        };
+        const auto row_of = [&](int j, int32_t id) {
+          if (BS == 0) return u.row0 + j * kTile;
+          if (id >= 0 && id < p.num_blocks) return id * BS;
+          if (lane < kBoxes && j * kTile + lane * BS < u.ctx)
+            report(p.dev_err, PKV_DEV_BAD_BLOCK_ID);
+          return static_cast<int>(p.num_blocks * BS);   // past the last row: zeros
+        };
+        const auto load = [&](int kv, int j, int row) {
+          if (round > 0 && ok) ok = wait(bar(Smem::kv_empty, st), (round - 1) & 1);
+          if (!ok) return;
+          const bool raw = kv == 1 && tail.clean && j == tail.tile;
+          uint64_t* b = raw ? bar(Smem::raw, 0) : bar(Smem::kv_full, st);
+          uint8_t* dst = smem + Smem::kv + st * kTileBytes;
+          if (lane == 0) mbar_arrive_expect_tx(b, kTileBytes);
+          __syncwarp();
+          if (lane < kBoxes) {
+            constexpr int kBoxBytes = kHalfBytes / kBoxes;
+            const CUtensorMap* m = kv ? &tmap_v : &tmap_k;
+            tma_load_3d(dst + lane * kBoxBytes, m, 0, u.g, row, b);
+            tma_load_3d(dst + kHalfBytes + lane * kBoxBytes, m, 64, u.g, row, b);
           }
+          if (kv == 0) clean();   // with the next K on its way
+          if (kv == 0 && j == u.last - 1) copy_q();
+          if (raw) dirty = st;
+          if (++st == kStages) {
+            st = 0;
+            ++round;
+          }
+        };
+        // a tile's V follows its K, in a pair the next tile's K; K of tile j - ahead then
+        // comes with V of tile j
+        const int ahead = u.pair ? 2 : 1;
+        int32_t id0 = id_of(u.last - 1), id1 = id_of(u.last - 2);
+        int row0 = row_of(u.last - 1, id0), row1 = 0;
+        int32_t id2 = id_of(u.last - 3);
+        load(0, u.last - 1, row0);
+        if (u.pair) {
+          row1 = row_of(u.last - 2, id1);
+          load(0, u.last - 2, row1);
+        }
 #pragma unroll 1
-          for (int kv = 0; kv < 2; ++kv) {
-            if (round > 0) ok = wait(bar(Smem::kv_empty, st), (round - 1) & 1);
-            if (!ok) break;
-            const bool raw = kv == 1 && tail.clean && j == tail.tile;
-            uint64_t* b = raw ? bar(Smem::raw, 0) : bar(Smem::kv_full, st);
-            uint8_t* dst = smem + Smem::kv + st * kTileBytes;
-            if (lane == 0) mbar_arrive_expect_tx(b, kTileBytes);
-            __syncwarp();
-            if (lane < kBoxes) {
-              constexpr int kBoxBytes = kHalfBytes / kBoxes;
-              const CUtensorMap* m = kv ? &tmap_v : &tmap_k;
-              tma_load_3d(dst + lane * kBoxBytes, m, 0, u.g, row, b);
-              tma_load_3d(dst + kHalfBytes + lane * kBoxBytes, m, 64, u.g, row, b);
-            }
-            if (kv == 0) clean();   // with the next K on its way
-            if (kv == 0 && j == u.last - 1) copy_q();
-            if (raw) dirty = st;
-            if (++st == kStages) {
-              st = 0;
-              ++round;
-            }
+        for (int j = u.last - 1; j >= u.begin && ok; --j) {
+          const int32_t id3 = id_of(j - 3);
+          load(1, j, row0);
+          if (j - ahead >= u.begin) {
+            const int next = row_of(j - ahead, u.pair ? id2 : id1);
+            load(0, j - ahead, next);
+            row0 = u.pair ? row1 : next;
+            row1 = next;
+          } else {
+            row0 = row1;
           }
+          id1 = id2;
+          id2 = id3;
         }
         clean();
       }
@@ -454,8 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                  acc || i > 0);
         }
       };
-      const auto qk8 = [&](int x, uint64_t kd) {
-        const uint64_t qd = q_desc + x * (kTileBytes >> 4);
+      const auto qk8 = [&](int x, uint64_t qd, uint64_t kd) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const uint32_t off = ((i >> 2) * kHalfBytes + (i & 3) * 32) >> 4;
@@ -470,6 +513,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       Unit u;
       for (int k = 0; ok && next_unit(k, u); ++k) {
+        if (u.pair) {
+          const int n = u.last - u.begin;
+          ok = wait(bar(Smem::q_full, 0), q_parity & 1);
+          q_parity ^= 1u;
+#pragma unroll 1
+          for (int i = -2; i < n && ok; ++i) {   // tile i's weights, tile i + 2's scores
+            const int x = i & 1;
+            const bool more = i + 2 < n;
+            const Ring rv = ring, rk = i < 0 ? ring : ring.after();
+            if (i >= 0) {
+              ok = full(rv) && wait(bar(Smem::p_full, 2 * x), p_parity >> x & 1);
+              if (!ok) break;
+              fence_after();
+              if (elect_one()) pv4(x, 0, v_at(rv), i >= 2);
+              __syncwarp();
+            }
+            if (more) ok = full(rk);
+            if (i >= 0) {
+              ok = wait(bar(Smem::p_full, 2 * x + 1), p_parity >> x & 1) && ok;
+              p_parity ^= 1u << x;
+              fence_after();
+            }
+            if (!ok) break;
+            if (elect_one()) {
+              if (i >= 0) pv4(x, 1, v_at(rv), true);
+              if (more)
+                qk8(x, q_desc, k_at(rk));
+              else
+                mma_commit(bar(Smem::o_full, x));
+              if (i + 3 == n) mma_commit(bar(Smem::q_empty, 0));
+              if (i >= 0) mma_commit(bar(Smem::kv_empty, rv.st));
+              if (more) mma_commit(bar(Smem::kv_empty, rk.st));
+            }
+            __syncwarp();
+            ring = more ? rk.after() : rk;
+          }
+          continue;
+        }
         bool v_there = false;
         // turn j: tile j - 1's K gives scores, tile j's weights meet their V
         // (j == u.last: only the first scores; j == u.begin: only the last outputs)
@@ -493,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               fence_after();
               if (elect_one()) {
                 pv4(x, 1, vd, true);
-                qk8(x, kd);
+                qk8(x, q_desc + x * (kTileBytes >> 4), kd);
               }
               __syncwarp();
               if (x == 0) {           // V of tile j - 1, if it is there already
@@ -542,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pv4(x, 1, v_at(rv), true);
               }
               if (more) {
-                qk8(x, k_at(rk));
+                qk8(x, q_desc + x * (kTileBytes >> 4), k_at(rk));
                 if (j == u.begin + 1) mma_commit(bar(Smem::q_empty, x));
               } else {
                 mma_commit(bar(Smem::o_full, x));
@@ -623,17 +704,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_at = tmem + lanes + kColS + x * kTile;
     const uint32_t o_at = tmem + lanes + kColO + x * kTile;
     const float sc = p.scale_log2;
-    int ns = 0, no = 0;   // score tiles and outputs taken
+    int ns = 0, npair = 0;      // score tiles and pairs taken
+    int turn[2] = {0, 0};       // outputs of either tile so far
     bool ok = true;
     Unit u;
     for (int k = 0; ok && next_unit(k, u); ++k) {
-      if (u.end[x] == u.begin) continue;
+      const int o_turn[2] = {turn[0], turn[1]};
+      turn[0] += u.has(0);
+      turn[1] += u.has(1);
+      if (!u.has(x)) continue;
       const int tok = u.tok0[x] + (r >> p.group_shift);
       const int pos0 = u.ctx - u.n + u.tok0[x];             // of the tile's first row
       const int pos = min(u.ctx - u.n + tok, u.ctx - 1);
       float m = kNoMax;
       float2 l2 = make_float2(0.f, 0.f);
-      for (int j = u.end[x] - 1; j >= u.begin; --j) {
+      const int step = u.pair ? 2 : 1, top = u.pair ? u.last - 1 - x : u.end[x] - 1;
+      for (int j = top; j >= u.begin; j -= step) {
         ok = wait(bar(Smem::s_full, x), ns & 1);
         if (!ok) break;
         ++ns;
@@ -666,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float alpha = exp2_approx(m - nm);
           m = nm;
           l2 = fmul2(l2, make_float2(alpha, alpha));
-          if (j + 1 < u.end[x]) {
+          if (j != top) {
             // the scores of a tile follow the product of the one before it: O is at rest
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
@@ -699,11 +785,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      ok = wait(bar(Smem::o_full, x), no & 1);
+      float l = l2.x + l2.y, other = 0.f;   // other: the second warpgroup's share of a pair
+      if (u.pair) {
+        float2* lm = reinterpret_cast<float2*>(smem + Smem::lm) + r;
+        if (x == 1) {
+          *lm = make_float2(l, m);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(Smem::lm_full, 0));
+          // its output may go once the first warpgroup has read it
+          ok = wait(bar(Smem::lm_free, 0), npair & 1);
+          ++npair;
+          continue;
+        }
+        ok = wait(bar(Smem::lm_full, 0), npair & 1) && wait(bar(Smem::o_full, 1), o_turn[1] & 1);
+        if (!ok) break;
+        ++npair;
+        const float2 b = *lm;
+        const float M = fmaxf(m, b.y), ca = exp2_approx(m - M), cb = exp2_approx(b.y - M);
+        l = l * ca + b.x * cb;
+        m = M;
+        l2.x = ca;          // weights of the two outputs
+        other = cb;
+      }
+      ok = wait(bar(Smem::o_full, x), o_turn[x] & 1);
       if (!ok) break;
-      ++no;
       fence_after();
-      const float l = l2.x + l2.y;
       const int head = (u.g << p.group_shift) + (r & ((1 << p.group_shift) - 1));
       const int64_t row = (static_cast<int64_t>(u.row0) + tok) * p.num_q_heads + head;
       const bool mine = tok < u.n;
@@ -712,6 +818,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool direct = mine && whole && u.split == 0;
       const bool part = mine && !whole && pos / kTile >= u.begin;
       const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float mul = u.pair ? l2.x : 1.f;
+      // 32 columns of the output, in units of 2^m
+      const auto take = [&](int col, uint32_t* o) {
+        tmem_ld32(o_at + col, o);
+        if (u.pair) {
+          uint32_t o1[32];
+          tmem_ld32(o_at + kTile + col, o1);
+          wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            o[i] = __float_as_uint(__uint_as_float(o[i]) * mul + __uint_as_float(o1[i]) * other);
+        } else {
+          wait_ld();
+        }
+      };
       const int64_t at = row * p.splits + u.split;
       const uint32_t mine32 = __ballot_sync(kFull, direct);
       // rows leave through the warp's 4 KB of shared memory, 64 dims at a time (16-byte
@@ -722,16 +843,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (mine32) {
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
-          uint32_t o[64];
-          tmem_ld32(o_at + 64 * c, o);
-          tmem_ld32(o_at + 64 * c + 32, o + 32);
-          if (lane == 0) bulk_wait_read();   // the last rows have left the buffer
-          __syncwarp();
-          wait_ld();
           uint32_t h[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            h[i] = pack_half2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+          for (int d = 0; d < 2; ++d) {
+            uint32_t o[32];
+            take(64 * c + 32 * d, o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              h[16 * d + i] = pack_half2(__uint_as_float(o[2 * i]) * inv,
+                                         __uint_as_float(o[2 * i + 1]) * inv);
+          }
+          if (lane == 0) bulk_wait_read();   // the last rows have left the buffer
+          __syncwarp();
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             box[lane * 8 + (i ^ (lane & 7))] =
@@ -758,8 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t o[32];
-          tmem_ld32(o_at + 32 * c, o);
-          wait_ld();
+          take(32 * c, o);
           uint4* dst = reinterpret_cast<uint4*>(p.part_o + at * kHeadDim + 32 * c);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -771,6 +893,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         p.part_ml[2 * at + 1] = l;
       }
       fence_before();   // O is read: the next unit's products may overwrite it once its weights are there
+      if (u.pair) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(Smem::lm_free, 0));
+      }
     }
     if (lane == 0) bulk_wait();
   }
@@ -786,6 +912,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kMergeRows = 8;
 __global__ void __launch_bounds__(kMergeRows * 32)
     prompt_merge_kernel(const Params p, int64_t max_context) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeRows + (threadIdx.x >> 5);
   if (row >= static_cast<int64_t>(p.num_tokens) * p.num_q_heads) return;
@@ -838,6 +966,23 @@ bool make_map(CUtensorMap* map, const void* base, int heads, int64_t rows, int b
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// a programmatic dependent launch: see the waits at the kernels' entries
+template <class Kernel, class... Args>
+int launch_dependent(Kernel kernel, dim3 grid, int threads, int smem, cudaStream_t st,
+                     const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
 template <int BS>
 int launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
            const CUtensorMap& mo, const Params& p, int64_t units, cudaStream_t st) {
@@ -851,10 +996,9 @@ int launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
       return PKV_ERR_CUDA;
     if (dev >= 0 && dev < 64) opted_in[dev].store(1, std::memory_order_release);
   }
-  prompt_attention_kernel<BS>
-      <<<dim3(static_cast<unsigned>(units * p.num_kv_heads), p.splits), kThreads, Smem::alloc, st>>>(
-          mq, mk, mv, mo, p);
-  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  return launch_dependent(prompt_attention_kernel<BS>,
+                          dim3(static_cast<unsigned>(units * p.num_kv_heads), p.splits), kThreads,
+                          Smem::alloc, st, mq, mk, mv, mo, p);
 }
 
 int group_shift_of(int num_q_heads, int num_kv_heads) {
@@ -868,7 +1012,8 @@ int group_shift_of(int num_q_heads, int num_kv_heads) {
   }
 }
 
-// Splits of the key axis: 1 unless the units alone leave SMs idle.
+// Splits of the key axis: 1 unless the units alone leave SMs idle; then two units
+// for each SM, of at least 8 KV tiles.
 constexpr int kSms = 152;
 constexpr int kMinSplitTiles = 8;
 int64_t units_for(int num_tokens, int num_seqs, int group_shift) {
@@ -876,8 +1021,8 @@ int64_t units_for(int num_tokens, int num_seqs, int group_shift) {
 }
 int splits_for(int64_t ctas, int64_t max_context, int* split_tiles) {
   const int64_t tiles = (max_context + kTile - 1) / kTile;
-  int64_t want = std::min<int64_t>(std::max<int64_t>(1, kSms / std::max<int64_t>(ctas, 1)),
-                                   std::max<int64_t>(1, tiles / kMinSplitTiles));
+  const int64_t fill = ctas < kSms ? 2 * kSms / std::max<int64_t>(ctas, 1) : 1;
+  const int64_t want = std::min(fill, std::max<int64_t>(1, tiles / kMinSplitTiles));
   const int64_t per = (tiles + want - 1) / want;
   *split_tiles = static_cast<int>(per);
   return static_cast<int>((tiles + per - 1) / per);
@@ -946,9 +1091,9 @@ int run(void* out, const void* q, const void* k, const void* v, const int32_t* b
   }
   if (rc != PKV_OK || p.splits == 1) return rc;
   const int64_t all = static_cast<int64_t>(num_tokens) * num_q_heads;
-  prompt_merge_kernel<<<static_cast<unsigned>((all + kMergeRows - 1) / kMergeRows), kMergeRows * 32,
-                        0, st>>>(p, static_cast<int64_t>(max_blocks) * block_size);
-  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  return launch_dependent(prompt_merge_kernel,
+                          dim3(static_cast<unsigned>((all + kMergeRows - 1) / kMergeRows)),
+                          kMergeRows * 32, 0, st, p, static_cast<int64_t>(max_blocks) * block_size);
 }
 
 }  // namespace prompt

@@ -37,6 +37,10 @@ template <class Code, int BS>
 __global__ void __launch_bounds__(kWarps * 32) write_q8_kernel(const WriteParams p) {
   constexpr int kPasses = BS / 2;   // two rows a pass
   const int lane = threadIdx.x & 31;
+  // a programmatic dependent of the stream's previous kernel, and the next one (the
+  // attention) may place its CTAs while this grid runs: each reads after its wait
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (blockIdx.x == 0 && blockIdx.y == 0)   // every entry is looked at once, used or not
     for (int s = threadIdx.x; s < p.num_seqs; s += kWarps * 32)
       packed_seq(p.query_start, p.context_lens, s, p.num_tokens,
@@ -147,13 +151,23 @@ __global__ void __launch_bounds__(kWarps * 32) write_q8_kernel(const WriteParams
 template <class Code>
 int launch_write(const WriteParams& p, int block_size, int64_t units, cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>(units), (2 * p.num_kv_heads + kWarps - 1) / kWarps);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t rc;
   switch (block_size) {
-    case 8: write_q8_kernel<Code, 8><<<grid, kWarps * 32, 0, st>>>(p); break;
-    case 16: write_q8_kernel<Code, 16><<<grid, kWarps * 32, 0, st>>>(p); break;
-    case 32: write_q8_kernel<Code, 32><<<grid, kWarps * 32, 0, st>>>(p); break;
-    default: write_q8_kernel<Code, 64><<<grid, kWarps * 32, 0, st>>>(p); break;
+    case 8: rc = cudaLaunchKernelEx(&cfg, write_q8_kernel<Code, 8>, p); break;
+    case 16: rc = cudaLaunchKernelEx(&cfg, write_q8_kernel<Code, 16>, p); break;
+    case 32: rc = cudaLaunchKernelEx(&cfg, write_q8_kernel<Code, 32>, p); break;
+    default: rc = cudaLaunchKernelEx(&cfg, write_q8_kernel<Code, 64>, p); break;
   }
-  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  return rc == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 }  // namespace q8
