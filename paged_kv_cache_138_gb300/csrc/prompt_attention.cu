@@ -24,13 +24,13 @@ constexpr int kTile = 128;                       // rows of a query tile, tokens
 constexpr int kHalfBytes = kTile * 128;          // 128 rows x 64 dims, 128-byte swizzle
 constexpr int kTileBytes = 2 * kHalfBytes;
 constexpr int kStages = 4;                       // KV tiles in shared memory
-constexpr int kThreads = 384;                    // 2 softmax warpgroups; copy, MMA and work warps
+constexpr int kThreads = 384;                    // 2 softmax warpgroups; 2 copy, MMA and work warps
 // Registers a thread after the split: 256 * 224 + 128 * 56 = 384 * 168, what the
 // CTA was launched with (a softmax thread holds a row of 128 scores).
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 224, kOtherRegs = 56;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split");
-constexpr int kCopyWarp = 8, kMmaWarp = 9, kWorkWarp = 10;
-constexpr int kReaders = 10;                     // warps that read a unit's description
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kWorkWarp = 10, kCopyVWarp = 11;
+constexpr int kReaders = 11;                     // warps that read a unit's description
 constexpr float kRescale = 8.f;                  // log2 units
 constexpr float kNoMax = -1e30f;
 
@@ -350,8 +350,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kCopyWarp) {
-      // ---- copies: Q, then K and V of each tile through a ring of kStages ----------------
+    if (warp == kCopyWarp || warp == kCopyVWarp) {
+      // ---- copies: K and V of each tile through a ring of kStages -----------------------------
+      // One warp brings Q and K, one V: both count through the whole sequence.  A warp starts
+      // a 16-row box every 73 cycles, so one alone needs 2300 cycles for the 32 boxes of a turn,
+      // as long as the turn's products; two together start one every 47.
+      const int mine = warp == kCopyVWarp;
       constexpr int kBoxes = BS ? kTile / (BS ? BS : 1) : 1;
       int st = 0, round = 0, nraw = 0;   // ring position, cleaned tiles
       int nq[2] = {0, 0};                // Q copies issued
@@ -376,20 +380,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         };
-        int dirty = -1;   // ring position of a V tile to be cleaned
-        const auto clean = [&] {
-          if (dirty < 0) return;
-          ok = ok && wait(bar(Smem::raw, 0), nraw & 1);
-          ++nraw;
-          const uint32_t at = smem_u32(smem + Smem::kv + dirty * kTileBytes);
-          for (int i = lane; ok && i < (tail.dirty_end - tail.valid) * 16; i += 32)
-            st_shared_zero16(at + (i & 8 ? kHalfBytes : 0) + (tail.valid + (i >> 4)) * 128 +
-                             (i & 7) * 16);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(Smem::kv_full, dirty));
-          dirty = -1;
-        };
         // the block id of this lane's part of tile j (paged): loaded ahead, looked at when
         // the tile's turn comes
         const auto id_of = [&](int j) {
@@ -407,22 +397,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           return static_cast<int>(p.num_blocks * BS);   // past the last row: zeros
         };
         const auto load = [&](int kv, int j, int row) {
-          if (round > 0 && ok) ok = wait(bar(Smem::kv_empty, st), (round - 1) & 1);
-          if (!ok) return;
-          const bool raw = kv == 1 && tail.clean && j == tail.tile;
-          uint64_t* b = raw ? bar(Smem::raw, 0) : bar(Smem::kv_full, st);
-          uint8_t* dst = smem + Smem::kv + st * kTileBytes;
-          if (lane == 0) mbar_arrive_expect_tx(b, kTileBytes);
-          __syncwarp();
-          if (lane < kBoxes) {
-            constexpr int kBoxBytes = kHalfBytes / kBoxes;
-            const CUtensorMap* m = kv ? &tmap_v : &tmap_k;
-            tma_load_3d(dst + lane * kBoxBytes, m, 0, u.g, row, b);
-            tma_load_3d(dst + kHalfBytes + lane * kBoxBytes, m, 64, u.g, row, b);
+          if (kv == mine && ok) {
+            if (round > 0) ok = wait(bar(Smem::kv_empty, st), (round - 1) & 1);
+            if (!ok) return;
+            const bool raw = kv == 1 && tail.clean && j == tail.tile;
+            uint64_t* b = raw ? bar(Smem::raw, 0) : bar(Smem::kv_full, st);
+            uint8_t* dst = smem + Smem::kv + st * kTileBytes;
+            if (lane == 0) mbar_arrive_expect_tx(b, kTileBytes);
+            __syncwarp();
+            if (lane < kBoxes) {
+              constexpr int kBoxBytes = kHalfBytes / kBoxes;
+              const CUtensorMap* m = kv ? &tmap_v : &tmap_k;
+              tma_load_3d(dst + lane * kBoxBytes, m, 0, u.g, row, b);
+              tma_load_3d(dst + kHalfBytes + lane * kBoxBytes, m, 64, u.g, row, b);
+            }
+            if (kv == 0 && j == u.last - 1) copy_q();
+            if (raw) {   // zeros in the rows past the context, then the tile may be used
+              ok = wait(b, nraw & 1);
+              ++nraw;
+              const uint32_t at = smem_u32(dst);
+              for (int i = lane; ok && i < (tail.dirty_end - tail.valid) * 16; i += 32)
+                st_shared_zero16(at + (i & 8 ? kHalfBytes : 0) + (tail.valid + (i >> 4)) * 128 +
+                                 (i & 7) * 16);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(Smem::kv_full, st));
+            }
           }
-          if (kv == 0) clean();   // with the next K on its way
-          if (kv == 0 && j == u.last - 1) copy_q();
-          if (raw) dirty = st;
           if (++st == kStages) {
             st = 0;
             ++round;
@@ -454,7 +455,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           id1 = id2;
           id2 = id3;
         }
-        clean();
       }
       if (!ok) {   // a wait gave up: let this CTA's copies land before it goes
         for (int i = 0; i < kStages; ++i) {
