@@ -394,6 +394,58 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   });
 }
 
+// Log-sum-exp merge of a row of many splits: a CTA for the row, warp w takes
+// splits w, w + 8, ..., their sums join in warp order.  (One warp a row, as the fp16
+// launches have it, spent 48 us on the 118 splits of 64 rows.)
+constexpr int kWideSplits = 16;   // from here on
+constexpr int kWideWarps = 8;
+__global__ void __launch_bounds__(kWideWarps * 32) q8_wide_merge_kernel(const Params p) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ float4 part[kWideWarps][32];
+  __shared__ float dens[kWideWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row = blockIdx.x;
+  const int s = static_cast<int>(row / p.num_q_heads);
+  const int cap = p.max_blocks * p.block_size;
+  const int L = max(0, min(__ldg(p.context_lens + s), cap));
+  const int n = splits_for_tiles(p, (L + kTile - 1) / kTile);
+  if (n <= 1) return;   // written by its only split
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + row * p.max_splits;
+  const float4* po = reinterpret_cast<const float4*>(p.part_o) + row * p.max_splits * 32 + lane;
+  float M = -INFINITY;
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, ml[i].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+  float den = 0.f;
+#pragma unroll 8
+  for (int i = warp; i < n; i += kWideWarps) {
+    const float2 w = ml[i];
+    const float4 v = po[static_cast<int64_t>(i) * 32];
+    const float c = exp2_approx(w.x - M);
+    num.x += c * v.x;
+    num.y += c * v.y;
+    num.z += c * v.z;
+    num.w += c * v.w;
+    den += c * w.y;
+  }
+  part[warp][lane] = num;
+  if (lane == 0) dens[warp] = den;
+  __syncthreads();
+  if (warp) return;
+#pragma unroll
+  for (int w = 1; w < kWideWarps; ++w) {
+    const float4 v = part[w][lane];
+    num.x += v.x;
+    num.y += v.y;
+    num.z += v.z;
+    num.w += v.w;
+    den += dens[w];
+  }
+  store_out4(p.out + row * kHeadDim + 4 * lane, den, num);
+}
+
 // The cache as [num_blocks * BS rows, Hkv, 128 bytes]; a box is min(BS, 32)
 // rows of one head under the 128-byte swizzle.
 bool make_q8_map(CUtensorMap* map, const void* base, int num_kv_heads, int64_t num_blocks,
@@ -529,5 +581,15 @@ extern "C" int pkv_paged_attention_decode_q8(void* out, const void* q, const voi
                      ? launch_q8_bs<Int8Half, false>(block_size, mk, mv, qp, splits, st)
                      : launch_q8_bs<E4m3Half, true>(block_size, mk, mv, qp, splits, st);
   if (rc != PKV_OK) return rc;
-  return p.max_splits > 1 ? launch_merge(p, st) : PKV_OK;
+  if (p.max_splits < kWideSplits) return p.max_splits > 1 ? launch_merge(p, st) : PKV_OK;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(num_seqs) * num_q_heads));
+  cfg.blockDim = dim3(kWideWarps * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, q8_wide_merge_kernel, p) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
