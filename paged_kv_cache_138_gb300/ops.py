@@ -20,12 +20,13 @@ BLOCK_SIZE = 16
 # ctypes as plain integers, and the current stream is asked for without building a
 # torch.cuda.Stream (2.8 us of a 14 us call).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream_handle(stream):
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_get_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -36,7 +37,13 @@ def _ptr(t):
     return t.data_ptr() if t is not None else None
 
 
+_Tensor = torch.Tensor
+
+
 def _dev(t, name, dtype, ndim=None):
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous() and \
+            (ndim is None or t.dim() == ndim):
+        return t
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
     if t.dtype != dtype:
@@ -65,6 +72,16 @@ class PreparedLaunch:
         rc = self._fn(*self._args)
         if rc != 0:
             check(rc, self._what)
+
+
+def _run(fn, args, what, prepare, keep, result):
+    """Launch, or with prepare a PreparedLaunch that holds the tensors keep."""
+    if prepare:
+        return PreparedLaunch(fn, args, what, keep)
+    rc = fn(*args)
+    if rc:
+        check(rc, what)
+    return result
 
 
 def _issue(fn, args, what, keep, prepare, result):
@@ -482,9 +499,8 @@ def paged_attention_prefill(out, q, k_cache, v_cache, block_tables, context_lens
             _ptr(context_lens), _ptr(query_start), T, S, Hq, Hkv, D, bs, nb, max_blocks,
             float(scale), _ptr(workspace), ws_bytes, _ptr(dev_err), _stream_handle(stream))
     keep = (out, q, k_cache, v_cache, block_tables, context_lens, query_start, workspace, dev_err,
-            stream)
-    return _issue(lib().pkv_paged_attention_prefill, args, "paged_attention_prefill", keep,
-                  prepare, out)
+            stream) if prepare else None
+    return _run(lib().pkv_paged_attention_prefill, args, "paged_attention_prefill", prepare, keep, out)
 
 
 def prompt_attention(out, q, k, v, query_start, scale, dev_err=None, stream=None, prepare=False):
@@ -505,8 +521,8 @@ def prompt_attention(out, q, k, v, query_start, scale, dev_err=None, stream=None
         raise ValueError("query_start must have num_seqs + 1 entries")
     args = (_ptr(out), _ptr(q), _ptr(k), _ptr(v), _ptr(query_start), T, S, Hq, Hkv, D,
             float(scale), _ptr(dev_err), _stream_handle(stream))
-    keep = (out, q, k, v, query_start, dev_err, stream)
-    return _issue(lib().pkv_prompt_attention, args, "prompt_attention", keep, prepare, out)
+    keep = (out, q, k, v, query_start, dev_err, stream) if prepare else None
+    return _run(lib().pkv_prompt_attention, args, "prompt_attention", prepare, keep, out)
 
 
 # ---- 8-bit cache ----------------------------------------------------------------------
@@ -537,11 +553,13 @@ def _q8_args(k_cache, v_cache, k_scale, v_scale):
     _dev(v_cache, "v_cache", k_cache.dtype, 4)
     _dev(k_scale, "k_scale", torch.float32, 2)
     _dev(v_scale, "v_scale", torch.float32, 2)
-    if v_cache.shape != k_cache.shape or v_scale.shape != k_scale.shape:
+    shape, (rows, stride) = k_cache.shape, k_scale.shape
+    if v_cache.shape != shape or v_scale.shape != (rows, stride):
         raise ValueError("K and V caches, and their scales, must share one shape")
-    if k_scale.shape[0] != k_cache.shape[0] or k_scale.shape[1] < k_cache.shape[2]:
+    nb, bs, Hkv, D = shape
+    if rows != nb or stride < Hkv:
         raise ValueError("scales must be [num_blocks, >= num_kv_heads]")
-    return code
+    return code, nb, bs, Hkv, D, stride
 
 
 def reshape_and_cache_q8(k, v, query_start, block_tables, context_lens, k_cache, v_cache, k_scale,
@@ -556,20 +574,19 @@ def reshape_and_cache_q8(k, v, query_start, block_tables, context_lens, k_cache,
     _dev(query_start, "query_start", torch.int32, 1)
     _dev(block_tables, "block_tables", torch.int32, 2)
     _dev(context_lens, "context_lens", torch.int32, 1)
-    code = _q8_args(k_cache, v_cache, k_scale, v_scale)
-    T, Hkv, D = k.shape
-    nb, bs, Hkv2, D2 = k_cache.shape
+    code, nb, bs, Hkv, D, stride = _q8_args(k_cache, v_cache, k_scale, v_scale)
+    T = k.shape[0]
     S, max_blocks = block_tables.shape
-    if v.shape != k.shape or (Hkv2, D2) != (Hkv, D):
+    if k.shape != (T, Hkv, D) or v.shape != (T, Hkv, D):
         raise ValueError("shape mismatch")
     if query_start.shape[0] != S + 1 or context_lens.shape[0] != S:
         raise ValueError("query_start must have num_seqs + 1 entries, context_lens num_seqs")
     args = (_ptr(k), _ptr(v), _ptr(query_start), _ptr(block_tables), _ptr(context_lens),
             _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), code, T, S, Hkv, D, bs, nb,
-            max_blocks, k_scale.shape[1], _ptr(dev_err), _stream_handle(stream))
+            max_blocks, stride, _ptr(dev_err), _stream_handle(stream))
     keep = (k, v, query_start, block_tables, context_lens, k_cache, v_cache, k_scale, v_scale,
-            dev_err, stream)
-    return _issue(lib().pkv_reshape_and_cache_q8, args, "reshape_and_cache_q8", keep, prepare, None)
+            dev_err, stream) if prepare else None
+    return _run(lib().pkv_reshape_and_cache_q8, args, "reshape_and_cache_q8", prepare, keep, None)
 
 
 def paged_attention_decode_q8(out, q, k_cache, v_cache, k_scale, v_scale, block_tables,
@@ -581,23 +598,21 @@ def paged_attention_decode_q8(out, q, k_cache, v_cache, k_scale, v_scale, block_
     _dev(out, "out", torch.float16, 3)
     _dev(block_tables, "block_tables", torch.int32, 2)
     _dev(context_lens, "context_lens", torch.int32, 1)
-    code = _q8_args(k_cache, v_cache, k_scale, v_scale)
-    S, Hq, D = q.shape
-    nb, bs, Hkv, D2 = k_cache.shape
-    if out.shape != q.shape or D2 != D:
+    code, nb, bs, Hkv, D, stride = _q8_args(k_cache, v_cache, k_scale, v_scale)
+    S, Hq, D2 = q.shape
+    if out.shape != (S, Hq, D) or D2 != D:
         raise ValueError("shape mismatch")
-    if block_tables.shape[0] != S or context_lens.shape[0] != S:
+    rows, max_blocks = block_tables.shape
+    if rows != S or context_lens.shape[0] != S:
         raise ValueError("block_tables / context_lens must have num_seqs rows")
-    max_blocks = block_tables.shape[1]
     need = workspace_bytes(S, Hq, max_blocks, bs, D)
     if need and workspace is None:
         workspace = alloc_workspace(S, Hq, max_blocks, q.device, bs)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     args = (_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), code,
             _ptr(block_tables), _ptr(context_lens), S, Hq, Hkv, D, bs, nb, max_blocks,
-            k_scale.shape[1], float(scale), _ptr(workspace), ws_bytes, _ptr(dev_err),
+            stride, float(scale), _ptr(workspace), ws_bytes, _ptr(dev_err),
             _stream_handle(stream))
     keep = (out, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, workspace,
-            dev_err, stream)
-    return _issue(lib().pkv_paged_attention_decode_q8, args, "paged_attention_decode_q8", keep,
-                  prepare, out)
+            dev_err, stream) if prepare else None
+    return _run(lib().pkv_paged_attention_decode_q8, args, "paged_attention_decode_q8", prepare, keep, out)
