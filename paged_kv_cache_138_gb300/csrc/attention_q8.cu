@@ -55,24 +55,24 @@ struct Int8Half {
   }
   static __device__ __forceinline__ uint32_t lo(uint32_t w) { return pair(w, 0x4140); }
   static __device__ __forceinline__ uint32_t hi(uint32_t w) { return pair(w, 0x4342); }
+  // K keeps the bias: a byte alone in a half is the subnormal u 2^-24, and the scores start at
+  // -128 2^-24 sum q instead of 0.  Bias and codes are of one size, so the sum loses
+  // nothing by it (under V, where tokens average out, it would).
+  static constexpr float kScoreUnit = 16777216.f, kScoreBias = -128.f / 16777216.f;
+  static __device__ __forceinline__ uint32_t k_lo(uint32_t w) { return __byte_perm(w, 0u, 0x4140); }
+  static __device__ __forceinline__ uint32_t k_hi(uint32_t w) { return __byte_perm(w, 0u, 0x4342); }
 };
 struct E4m3Half {
   static __device__ __forceinline__ uint32_t bias(uint32_t w) { return w; }
   static __device__ __forceinline__ uint32_t lo(uint32_t w) { return E4m3Code::half2_of(w & 0xffffu); }
   static __device__ __forceinline__ uint32_t hi(uint32_t w) { return E4m3Code::half2_of(w >> 16); }
+  static constexpr float kScoreUnit = 1.f, kScoreBias = 0.f;
+  static __device__ __forceinline__ uint32_t k_lo(uint32_t w) { return lo(w); }
+  static __device__ __forceinline__ uint32_t k_hi(uint32_t w) { return hi(w); }
 };
 
-__device__ __forceinline__ uint32_t q8_chunk(uint32_t half, int row, int c) {
-  return half + row * 128 + ((c ^ (row & 7)) << 4);
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
+__device__ __forceinline__ uint4 q8_chunk(const uint8_t* half, int row, int c) {
+  return *reinterpret_cast<const uint4*>(half + row * 128 + ((c ^ (row & 7)) << 4));
 }
 
 // transpose an 8x8 fp16 matrix held one row per four lanes
@@ -96,7 +96,8 @@ constexpr int kLeftOut = 0x7fc0dead;  // in place of a K scale: the block has no
 // One stage of 32 tokens.  ks[j] / lv[j]: K scale * scale * log2 e and
 // log2 of the V scale of box j (boxes of BS, at most 32, tokens).
 template <class Half, int BOXES>
-__device__ __forceinline__ void q8_tile(uint32_t st, const uint32_t (&qb)[8][2],
+__device__ __forceinline__ void q8_tile(const uint8_t* st, const uint32_t (&qb)[8][2],
+                                        const float (&s0)[2],
                                         const float (&ks)[BOXES], const float (&lv)[BOXES],
                                         int valid, int lane, Q8State& a) {
   constexpr unsigned kFull = 0xffffffffu;
@@ -104,17 +105,17 @@ __device__ __forceinline__ void q8_tile(uint32_t st, const uint32_t (&qb)[8][2],
   float x[2][4];   // [16-token half][token r head 0, head 1, token r + 8 head 0, head 1]
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    float s[4] = {s0[0], s0[1], s0[0], s0[1]};
     const int t0 = 16 * h + r, t1 = t0 + 8;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint4 w0 = lds128(q8_chunk(st, t0, 2 * c + i));
-      const uint4 w1 = lds128(q8_chunk(st, t1, 2 * c + i));
+      const uint4 w0 = q8_chunk(st, t0, 2 * c + i);
+      const uint4 w1 = q8_chunk(st, t1, 2 * c + i);
       const uint32_t u0[4] = {w0.x, w0.y, w0.z, w0.w}, u1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint32_t b0 = Half::bias(u0[j]), b1 = Half::bias(u1[j]);
-        mma_16816_full(s, Half::lo(b0), Half::lo(b1), Half::hi(b0), Half::hi(b1),
+        mma_16816_full(s, Half::k_lo(b0), Half::k_lo(b1), Half::k_hi(b0), Half::k_hi(b1),
                        qb[4 * i + j][0], qb[4 * i + j][1]);
       }
     }
@@ -181,7 +182,7 @@ __device__ __forceinline__ void q8_tile(uint32_t st, const uint32_t (&qb)[8][2],
     uint32_t t[4][4];   // tokens 2 c, 2 c + 1, 2 c + 8, 2 c + 9 of the half, 16 dims each
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const uint4 w = lds128(q8_chunk(st + kQ8HalfBytes, 16 * h + 2 * c + (k & 1) + 8 * (k >> 1), r));
+      const uint4 w = q8_chunk(st + kQ8HalfBytes, 16 * h + 2 * c + (k & 1) + 8 * (k >> 1), r);
       t[k][0] = w.x;
       t[k][1] = w.y;
       t[k][2] = w.z;
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       } else {
         row[i] = b * BS + tok % BS;
         const int64_t at = static_cast<int64_t>(b) * qp.scale_stride + g;
-        ksv[i] = __ldg(qp.k_scale + at) * p.scale_log2;
+        ksv[i] = __ldg(qp.k_scale + at) * p.scale_log2 * Half::kScoreUnit;
         lvv[i] = __log2f(__ldg(qp.v_scale + at));
       }
     }
@@ -315,6 +316,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
   }
 
+  // where the scores of the lane's two heads start
+  float s0[2] = {0.f, 0.f};
+  if (Half::kScoreBias != 0.f) {
+    float sum = 0.f;   // of head lane / 4 over the lane's 32 dims, then over the four lanes
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum += sum_half2(qb[k][0]) + sum_half2(qb[k][1]);
+    sum += __shfl_xor_sync(kFull, sum, 1);
+    sum += __shfl_xor_sync(kFull, sum, 2);
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+      s0[n] = __shfl_sync(kFull, sum, 4 * (2 * (lane & 3) + n)) * Half::kScoreBias;
+  }
+
   Q8State a;
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
@@ -329,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     const bool landed = mbar_wait_bounded(&bars[k % kStages], (k / kStages) & 1, p.dev_err);
     ok = __all_sync(kFull, ok && landed) != 0;
     if (ok) {
-      const uint32_t st = smem_u32(ring + (k % kStages) * kStageBytes);
+      const uint8_t* st = ring + (k % kStages) * kStageBytes;
       float ks[kBoxes], lv[kBoxes];
 #pragma unroll
       for (int b = 0; b < kBoxes; ++b) {
@@ -348,11 +362,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         // rows past the context may hold any byte, and e4m3 has NaN codes: 0 * NaN
         // would poison the sums
         for (int i = lane; i < (kQ8Tile - valid) * 8; i += 32)
-          st_shared_zero16(st + kQ8HalfBytes + valid * kHeadDim + i * 16);
+          st_shared_zero16(smem_u32(st) + kQ8HalfBytes + valid * kHeadDim + i * 16);
         fence_proxy_async_smem();
         __syncwarp();
       }
-      q8_tile<Half, kBoxes>(st, qb, ks, lv, valid, lane, a);
+      q8_tile<Half, kBoxes>(st, qb, s0, ks, lv, valid, lane, a);
     }
     __syncwarp();
     if (ok && issued < mine) {
