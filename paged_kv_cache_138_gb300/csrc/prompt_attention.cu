@@ -63,6 +63,17 @@ struct Smem {
   static_assert(alloc <= 227 * 1024, "shared memory of one CTA");
 };
 
+// A KV tile in shared memory is made of 1 KB atoms of 8 tokens x 64 dims (128-byte
+// swizzle).  Paged: the atoms of both halves of the dims lie side by side, 8 tokens
+// after 8 tokens, so that one box brings a whole block (half the boxes, whose number
+// bounds the copies of 16-token blocks).  Packed: one half, then the other, as two
+// boxes of 128 tokens (packed rows start anywhere, not at multiples of 8).
+template <int BS>
+struct KvLayout {
+  static constexpr uint32_t kHalf = BS ? 1024 : kHalfBytes;   // to the other half of the dims
+  static constexpr uint32_t kEight = BS ? 2048 : 1024;        // to the next 8 tokens
+};
+
 // TMEM columns: scores (overwritten by the fp16 weights) and outputs of the two tiles
 constexpr uint32_t kColS = 0, kColO = 256;
 
@@ -140,6 +151,16 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
       "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
       "r"(r[30]), "r"(r[31]), "r"(addr)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_5d(void* smem_dst, const void* tmap, int c0, int c1, int c2,
+                                            int c3, int c4, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4),
+      "r"(smem_u32(bar))
       : "memory");
 }
 
@@ -292,6 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const __grid_constant__ CUtensorMap tmap_k,
                             const __grid_constant__ CUtensorMap tmap_v,
                             const __grid_constant__ CUtensorMap tmap_o, const Params p) {
+  using Kv = KvLayout<BS>;
   constexpr unsigned kFull = 0xffffffffu;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -353,8 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kCopyWarp || warp == kCopyVWarp) {
       // ---- copies: K and V of each tile through a ring of kStages -----------------------------
       // One warp brings Q and K, one V: both count through the whole sequence.  A warp starts
-      // a 16-row box every 73 cycles, so one alone needs 2300 cycles for the 32 boxes of a turn,
-      // as long as the turn's products; two together start one every 47.
+      // a box of 16 rows every 73 cycles.
       const int mine = warp == kCopyVWarp;
       constexpr int kBoxes = BS ? kTile / (BS ? BS : 1) : 1;
       int st = 0, round = 0, nraw = 0;   // ring position, cleaned tiles
@@ -406,19 +427,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive_expect_tx(b, kTileBytes);
             __syncwarp();
             if (lane < kBoxes) {
-              constexpr int kBoxBytes = kHalfBytes / kBoxes;
               const CUtensorMap* m = kv ? &tmap_v : &tmap_k;
-              tma_load_3d(dst + lane * kBoxBytes, m, 0, u.g, row, b);
-              tma_load_3d(dst + kHalfBytes + lane * kBoxBytes, m, 64, u.g, row, b);
+              if (BS) {
+                tma_load_5d(dst + lane * (kTileBytes / kBoxes), m, 0, 0, 0, row >> 3, u.g, b);
+              } else {
+                tma_load_3d(dst, m, 0, u.g, row, b);
+                tma_load_3d(dst + kHalfBytes, m, 64, u.g, row, b);
+              }
             }
             if (kv == 0 && j == u.last - 1) copy_q();
             if (raw) {   // zeros in the rows past the context, then the tile may be used
               ok = wait(b, nraw & 1);
               ++nraw;
               const uint32_t at = smem_u32(dst);
-              for (int i = lane; ok && i < (tail.dirty_end - tail.valid) * 16; i += 32)
-                st_shared_zero16(at + (i & 8 ? kHalfBytes : 0) + (tail.valid + (i >> 4)) * 128 +
-                                 (i & 7) * 16);
+              for (int i = lane; ok && i < (tail.dirty_end - tail.valid) * 16; i += 32) {
+                const int r = tail.valid + (i >> 4);
+                st_shared_zero16(at + (i & 8 ? Kv::kHalf : 0) + (r >> 3) * Kv::kEight +
+                                 (r & 7) * 128 + (i & 7) * 16);
+              }
               fence_proxy_async_smem();
               __syncwarp();
               if (lane == 0) mbar_arrive(bar(Smem::kv_full, st));
@@ -482,8 +508,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       const uint32_t s_col = tmem + kColS, o_col = tmem + kColO;
       const uint64_t q_desc = operand_desc(smem_u32(smem + Smem::q), 16, 1024);
-      const uint64_t k_desc = operand_desc(smem_u32(smem + Smem::kv), 16, 1024);
-      const uint64_t v_desc = operand_desc(smem_u32(smem + Smem::kv), kHalfBytes, 1024);
+      const uint64_t k_desc = operand_desc(smem_u32(smem + Smem::kv), 16, Kv::kEight);
+      const uint64_t v_desc = operand_desc(smem_u32(smem + Smem::kv), Kv::kHalf, Kv::kEight);
       const auto full = [&](Ring r) { return wait(bar(Smem::kv_full, r.st), r.round & 1); };
       const auto commit = [&](uint64_t* b) {
         if (elect_one()) mma_commit(b);
@@ -494,15 +520,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int kk = 4 * half + i;
-          mma_ts(o_col + x * kTile, s_col + x * kTile + 8 * kk, vd + kk * (2048 >> 4), kIdescPv,
-                 acc || i > 0);
+          mma_ts(o_col + x * kTile, s_col + x * kTile + 8 * kk, vd + kk * (2 * Kv::kEight >> 4),
+                 kIdescPv, acc || i > 0);
         }
       };
       const auto qk8 = [&](int x, uint64_t qd, uint64_t kd) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const uint32_t off = ((i >> 2) * kHalfBytes + (i & 3) * 32) >> 4;
-          mma_ss(s_col + x * kTile, qd + off, kd + off, p.idesc_qk, i > 0);
+          const uint32_t step = (i & 3) * 32;
+          mma_ss(s_col + x * kTile, qd + (((i >> 2) * kHalfBytes + step) >> 4),
+                 kd + (((i >> 2) * Kv::kHalf + step) >> 4), p.idesc_qk, i > 0);
         }
         mma_commit(bar(Smem::s_full, x));
       };
@@ -983,6 +1010,21 @@ int launch_dependent(Kernel kernel, dim3 grid, int threads, int smem, cudaStream
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
+// the cache as [head][8 tokens][half][token of 8][64 dims]: a box is a block of one head,
+// laid down as KvLayout wants it
+bool make_block_map(CUtensorMap* map, const void* base, int heads, int64_t rows, int block_size) {
+  auto fn = attn::encode_fn();
+  if (!fn) return false;
+  const cuuint64_t row = static_cast<cuuint64_t>(heads) * kHeadDim * 2;
+  cuuint64_t dims[5] = {64, 8, 2, static_cast<cuuint64_t>(rows) / 8, static_cast<cuuint64_t>(heads)};
+  cuuint64_t strides[4] = {row, 128, 8 * row, kHeadDim * 2};
+  cuuint32_t box[5] = {64, 8, 2, static_cast<cuuint32_t>(block_size) / 8, 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int BS>
 int launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
            const CUtensorMap& mo, const Params& p, int64_t units, cudaStream_t st) {
@@ -1074,11 +1116,13 @@ int run(void* out, const void* q, const void* k, const void* v, const int32_t* b
   p.scale_log2 = std::max(1e-30f, (scale < 0.f ? -scale : scale) * 1.4426950408889634f);
 
   CUtensorMap mq, mk, mv, mo;
-  const int64_t rows = paged ? num_blocks * block_size : num_tokens;
-  const int box = paged ? block_size : kTile;
+  const int64_t rows = num_blocks * block_size;
   if (!make_map(&mq, q, num_q_heads, num_tokens, 1 << shift, kTile >> shift) ||
       !make_map(&mo, out, num_q_heads, num_tokens, 1 << shift, 32 >> shift) ||
-      !make_map(&mk, k, num_kv_heads, rows, 1, box) || !make_map(&mv, v, num_kv_heads, rows, 1, box))
+      !(paged ? make_block_map(&mk, k, num_kv_heads, rows, block_size) &&
+                    make_block_map(&mv, v, num_kv_heads, rows, block_size)
+              : make_map(&mk, k, num_kv_heads, num_tokens, 1, kTile) &&
+                    make_map(&mv, v, num_kv_heads, num_tokens, 1, kTile)))
     return PKV_ERR_CUDA;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   int rc;
