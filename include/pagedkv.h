@@ -393,13 +393,14 @@ int pkv_copy_blocks(void* const* k_caches, void* const* v_caches, int num_layers
  *   block_tables int32 [num_seqs, max_blocks_per_seq] (device)
  *   context_lens int32 [num_seqs] (device)
  *   query_start  int32 [num_seqs + 1] (device), ascending, at most num_tokens
- *   block_size 8, 16, 32 or 64; num_q_heads / num_kv_heads 1, 2, 4 or 8
+ *   block_size 8, 16, 32 or 64; num_q_heads / num_kv_heads 1, 2, 4 or 8;
+ *   max_blocks_per_seq * block_size at most 2^25
  *   workspace    at least pkv_paged_attention_prefill_workspace_bytes(...) (0
  *                unless the key axis is split); not shared by launches in flight
  * Reported, and left out: a sequence whose query_start entries are out of order
- * or past num_tokens (PKV_DEV_BAD_QUERY_RANGE) or whose context is shorter than
- * its rows or longer than its table (PKV_DEV_BAD_CONTEXT_LEN); its rows of out
- * stay as they were.  A block whose id is out of range (PKV_DEV_BAD_BLOCK_ID)
+ * or past num_tokens (PKV_DEV_BAD_QUERY_RANGE; sequences beside it may be left out
+ * too) or whose context is shorter than its rows or longer than its table
+ * (PKV_DEV_BAD_CONTEXT_LEN); its rows of out stay as they were.  A block whose id is out of range (PKV_DEV_BAD_BLOCK_ID)
  * counts as zeros.
  * fp32 scores, maxima, sums and accumulators; the softmax weights are rounded
  * to fp16 for the product with V, the result once.
@@ -422,8 +423,8 @@ size_t pkv_paged_attention_prefill_workspace_bytes(int num_tokens, int num_seqs,
 /*
  * The same over packed K and V: whole prompts whose tokens are all in this
  * call (k, v fp16 [num_tokens, num_kv_heads, 128], 16-byte aligned, packed like
- * q), with no cache read, for instance before they are written to an 8-bit
- * cache.  Rows of k and v that no sequence owns may hold anything.
+ * q; at most 2^25), with no cache read, for instance before they are written to
+ * an 8-bit cache.  Rows of k and v that no sequence owns may hold anything.
  */
 int pkv_prompt_attention(void* out, const void* q, const void* k, const void* v,
                          const int32_t* query_start, int num_tokens, int num_seqs,
@@ -464,11 +465,12 @@ int pkv_prompt_attention(void* out, const void* q, const void* k, const void* v,
  *   code         PKV_CODE_INT8 or PKV_CODE_E4M3
  *   block_size   8, 16, 32 or 64
  * Reported, and left out: a sequence whose query_start entries are out of order
- * or past num_tokens (PKV_DEV_BAD_QUERY_RANGE) or whose context is shorter than
- * its rows or longer than its table (PKV_DEV_BAD_CONTEXT_LEN); a block id out
- * of range (PKV_DEV_BAD_BLOCK_ID).  Infinities and NaN are stored as 0 and
- * reported (PKV_DEV_NONFINITE).  Two sequences that write into one block race:
- * give a shared block a private copy first (pkv_copy_blocks on codes and scales).
+ * or past num_tokens (PKV_DEV_BAD_QUERY_RANGE; sequences beside it may be left out
+ * too) or whose context is shorter than its rows or longer than its table
+ * (PKV_DEV_BAD_CONTEXT_LEN); a block id out of range (PKV_DEV_BAD_BLOCK_ID).
+ * Infinities and NaN are stored as 0 and reported (PKV_DEV_NONFINITE).  Two
+ * sequences that write into one block race: give a shared block a private copy
+ * first (pkv_copy_blocks on codes and scales).
  */
 int pkv_reshape_and_cache_q8(const void* k, const void* v, const int32_t* query_start,
                              const int32_t* block_tables, const int32_t* context_lens,

@@ -1058,6 +1058,9 @@ int group_shift_of(int num_q_heads, int num_kv_heads) {
 // for each SM, of at least 8 KV tiles.
 constexpr int kSms = 152;
 constexpr int kMinSplitTiles = 8;
+// The longest context: a warp that waits for a whole unit of it (2400 cycles for 128
+// tokens) stays within half the waits' limit.
+constexpr int64_t kMaxContext = 1 << 25;
 int64_t units_for(int num_tokens, int num_seqs, int group_shift) {
   return num_tokens / (2 * kTile >> group_shift) + static_cast<int64_t>(num_seqs);
 }
@@ -1178,8 +1181,8 @@ extern "C" int pkv_paged_attention_prefill(void* out, const void* q, const void*
       !(block_size == 8 || block_size == 16 || block_size == 32 || block_size == 64))
     return PKV_ERR_UNSUPPORTED;
   if (group_shift_of(num_q_heads, num_kv_heads) < 0) return PKV_ERR_UNSUPPORTED;
-  if (num_blocks > INT32_MAX / block_size ||
-      static_cast<int64_t>(max_blocks_per_seq) * block_size > INT32_MAX - 2 * kTile)
+  if (num_tokens > INT32_MAX - 2 * kTile || num_blocks > INT32_MAX / block_size ||
+      static_cast<int64_t>(max_blocks_per_seq) * block_size > kMaxContext)
     return PKV_ERR_UNSUPPORTED;
   if (num_seqs > 0 && num_tokens > 0 && (!block_tables || !context_lens)) return PKV_ERR_INVALID_ARG;
   return run(out, q, k_cache, v_cache, block_tables, context_lens, query_start, num_tokens,
@@ -1196,7 +1199,7 @@ extern "C" int pkv_prompt_attention(void* out, const void* q, const void* k, con
     return PKV_ERR_INVALID_ARG;
   if (head_dim != kHeadDim || group_shift_of(num_q_heads, num_kv_heads) < 0)
     return PKV_ERR_UNSUPPORTED;
-  if (num_tokens > INT32_MAX - 2 * kTile) return PKV_ERR_UNSUPPORTED;
+  if (num_tokens > kMaxContext) return PKV_ERR_UNSUPPORTED;
   return run(out, q, k, v, nullptr, nullptr, query_start, num_tokens, num_seqs, num_q_heads,
              num_kv_heads, 0, 0, 0, scale, nullptr, 0, dev_err, stream);
 }

@@ -203,6 +203,35 @@ def test_paged_split_keys(ops, new, cached):
     check_paged(got, q, kc, vc, tables, lens, new)
 
 
+@pytest.mark.parametrize("tail", [127, 128, 129, 255, 256, 257, 384, 640, 1000])
+def test_paged_rows_in_one_tile(ops, tail):
+    """Chunks whose rows fill one query tile or less, over 1 to 8 KV tiles: both halves
+    of the kernel work on them, on every other KV tile each."""
+    for Hq, Hkv, n in ((2, 2, 100), (8, 1, 16), (8, 1, 3), (4, 1, 1)):
+        new, cached = [n, n + 1], [tail - n if tail > n else 0, tail]
+        q, kc, vc, tables, lens = paged_case(tail + Hq, new, cached, Hq, Hkv, 16)
+        got, err = run_paged(ops, q, kc, vc, tables, lens, starts(new))
+        assert err == 0
+        check_paged(got, q, kc, vc, tables, lens, new)
+
+
+@pytest.mark.parametrize("bs", [8, 16, 64])
+def test_many_units_of_every_kind(ops, bs):
+    """More units than the GPU has SMs, of one tile and of two, one KV tile and many, in
+    one launch: each SM goes through several, in the order they come."""
+    rng = np.random.default_rng(bs)
+    new = rng.choice([0, 1, 5, 31, 64, 65, 127, 128, 200, 256, 300], size=48)
+    cached = rng.choice([0, 0, 7, 100, 129, 640], size=48)
+    q, kc, vc, tables, lens = paged_case(19, new, cached, 16, 8, bs, behind=9)
+    assert ops.prefill_workspace_bytes(q.shape[0], 48, 16, 8, tables.shape[1], bs) == 0
+    got, err = run_paged(ops, q, kc, vc, tables, lens, starts(new))
+    assert err == 0
+    check_paged(got, q, kc, vc, tables, lens, new)
+    assert (got[int(new.sum()):] == 7).all()
+    again, _ = run_paged(ops, q, kc, vc, tables, lens, starts(new))
+    assert np.array_equal(got, again)
+
+
 def test_paged_split_bookkeeping(ops):
     """Maxima that lie hundreds of log2 units apart between the splits."""
     q, kc, vc, tables, lens = paged_case(12, [6], [6000], 4, 1, 16)
@@ -217,8 +246,8 @@ def test_paged_split_bookkeeping(ops):
         check_paged(got, q, kc, vc, tables, lens, [6])
 
 
-def test_same_bits_whatever_the_batch(ops):
-    """A prompt's rows do not depend on block ids, on neighbours or on a repeat."""
+def test_same_bits_whatever_the_placement(ops):
+    """Block ids and repeats leave the bits alone."""
     new, cached = [200, 33, 129], [100, 0, 500]
     q, kc, vc, tables, lens = paged_case(13, new, cached, 8, 2, 16, poison=False)
     a, _ = run_paged(ops, q, kc, vc, tables, lens, starts(new))
