@@ -460,6 +460,19 @@ def paged_attention_decode_grouped_fused(out, q, k_new, v_new, k_cache, v_cache,
 
 
 # ---- prompt attention ------------------------------------------------------------------
+# The checks of these entry points run once per call of a few microseconds: one
+# expression that holds for good arguments, and only where it does not the checks
+# that say what is wrong.
+
+_F16, _F32, _I32 = torch.float16, torch.float32, torch.int32
+
+
+def _explain(*specs):
+    """Raise for the first (tensor, name, dtype, ndim) that is not as it should be."""
+    for spec in specs:
+        _dev(*spec)
+    raise ValueError("arguments do not fit together")
+
 
 @functools.lru_cache(maxsize=256)
 def prefill_workspace_bytes(num_tokens, num_seqs, num_q_heads, num_kv_heads, max_blocks_per_seq,
@@ -476,51 +489,70 @@ def paged_attention_prefill(out, q, k_cache, v_cache, block_tables, context_lens
     query_start[s] .. query_start[s + 1] - 1 of q and out [T, Hq, 128], the last of its
     context_lens[s] tokens, all of whose K/V are in the cache.
     prepare=True returns a PreparedLaunch instead of launching."""
-    _dev(q, "q", torch.float16, 3)
-    _dev(out, "out", torch.float16, 3)
-    _dev(k_cache, "k_cache", torch.float16, 4)
-    _dev(v_cache, "v_cache", torch.float16, 4)
-    _dev(block_tables, "block_tables", torch.int32, 2)
-    _dev(context_lens, "context_lens", torch.int32, 1)
-    _dev(query_start, "query_start", torch.int32, 1)
-    T, Hq, D = q.shape
-    nb, bs, Hkv, D2 = k_cache.shape
+    try:
+        good = (q.dtype is _F16 and q.is_cuda and q.is_contiguous() and
+                out.dtype is _F16 and out.is_cuda and out.is_contiguous() and
+                k_cache.dtype is _F16 and k_cache.is_cuda and k_cache.is_contiguous() and
+                v_cache.dtype is _F16 and v_cache.is_cuda and v_cache.is_contiguous() and
+                block_tables.dtype is _I32 and block_tables.is_cuda and
+                block_tables.is_contiguous() and
+                context_lens.dtype is _I32 and context_lens.is_cuda and
+                context_lens.is_contiguous() and
+                query_start.dtype is _I32 and query_start.is_cuda and query_start.is_contiguous()
+                and q.dim() == 3 and k_cache.dim() == 4 and block_tables.dim() == 2)
+    except AttributeError:
+        good = False
+    if not good:
+        _explain((q, "q", _F16, 3), (out, "out", _F16, 3), (k_cache, "k_cache", _F16, 4),
+                 (v_cache, "v_cache", _F16, 4), (block_tables, "block_tables", _I32, 2),
+                 (context_lens, "context_lens", _I32, 1), (query_start, "query_start", _I32, 1))
+    T, Hq, D = shape = q.shape
+    nb, bs, Hkv, D2 = cache = k_cache.shape
     S, max_blocks = block_tables.shape
-    if out.shape != q.shape or v_cache.shape != k_cache.shape or D2 != D:
+    if out.shape != shape or v_cache.shape != cache or D2 != D:
         raise ValueError("shape mismatch")
-    if query_start.shape[0] != S + 1 or context_lens.shape[0] != S:
+    if query_start.shape != (S + 1,) or context_lens.shape != (S,):
         raise ValueError("query_start must have num_seqs + 1 entries, context_lens num_seqs")
     if workspace is None:
         need = prefill_workspace_bytes(T, S, Hq, Hkv, max_blocks, bs)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    args = (_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-            _ptr(context_lens), _ptr(query_start), T, S, Hq, Hkv, D, bs, nb, max_blocks,
-            float(scale), _ptr(workspace), ws_bytes, _ptr(dev_err), _stream_handle(stream))
+    args = (out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            block_tables.data_ptr(), context_lens.data_ptr(), query_start.data_ptr(), T, S, Hq,
+            Hkv, D, bs, nb, max_blocks, float(scale), _ptr(workspace), ws_bytes, _ptr(dev_err),
+            _stream_handle(stream))
     keep = (out, q, k_cache, v_cache, block_tables, context_lens, query_start, workspace, dev_err,
             stream) if prepare else None
-    return _run(lib().pkv_paged_attention_prefill, args, "paged_attention_prefill", prepare, keep, out)
+    return _run(lib().pkv_paged_attention_prefill, args, "paged_attention_prefill", prepare, keep,
+                out)
 
 
 def prompt_attention(out, q, k, v, query_start, scale, dev_err=None, stream=None, prepare=False):
     """Causal attention of whole packed prompts: q and out [T, Hq, 128], k and v [T, Hkv,
     128], sequence s owning rows query_start[s] .. query_start[s + 1] - 1 of each.
     prepare=True returns a PreparedLaunch instead of launching."""
-    _dev(q, "q", torch.float16, 3)
-    _dev(out, "out", torch.float16, 3)
-    _dev(k, "k", torch.float16, 3)
-    _dev(v, "v", torch.float16, 3)
-    _dev(query_start, "query_start", torch.int32, 1)
-    T, Hq, D = q.shape
-    Hkv = k.shape[1]
-    if out.shape != q.shape or k.shape != (T, Hkv, D) or v.shape != k.shape:
+    try:
+        good = (q.dtype is _F16 and q.is_cuda and q.is_contiguous() and
+                out.dtype is _F16 and out.is_cuda and out.is_contiguous() and
+                k.dtype is _F16 and k.is_cuda and k.is_contiguous() and
+                v.dtype is _F16 and v.is_cuda and v.is_contiguous() and
+                query_start.dtype is _I32 and query_start.is_cuda and query_start.is_contiguous()
+                and q.dim() == 3 and k.dim() == 3 and query_start.dim() == 1)
+    except AttributeError:
+        good = False
+    if not good:
+        _explain((q, "q", _F16, 3), (out, "out", _F16, 3), (k, "k", _F16, 3), (v, "v", _F16, 3),
+                 (query_start, "query_start", _I32, 1))
+    T, Hq, D = shape = q.shape
+    T2, Hkv, D2 = rows = k.shape
+    if out.shape != shape or T2 != T or D2 != D or v.shape != rows:
         raise ValueError("shape mismatch")
     S = query_start.shape[0] - 1
     if S < 0:
         raise ValueError("query_start must have num_seqs + 1 entries")
-    args = (_ptr(out), _ptr(q), _ptr(k), _ptr(v), _ptr(query_start), T, S, Hq, Hkv, D,
-            float(scale), _ptr(dev_err), _stream_handle(stream))
+    args = (out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), query_start.data_ptr(), T, S,
+            Hq, Hkv, D, float(scale), _ptr(dev_err), _stream_handle(stream))
     keep = (out, q, k, v, query_start, dev_err, stream) if prepare else None
     return _run(lib().pkv_prompt_attention, args, "prompt_attention", prepare, keep, out)
 
@@ -546,17 +578,26 @@ def q8_cache(num_blocks, num_kv_heads, block_size=BLOCK_SIZE, dtype=torch.int8, 
 
 
 def _q8_args(k_cache, v_cache, k_scale, v_scale):
-    code = _CODES.get(k_cache.dtype)
-    if code is None:
-        raise TypeError("k_cache must be torch.int8 or torch.float8_e4m3fn, got %s" % k_cache.dtype)
-    _dev(k_cache, "k_cache", k_cache.dtype, 4)
-    _dev(v_cache, "v_cache", k_cache.dtype, 4)
-    _dev(k_scale, "k_scale", torch.float32, 2)
-    _dev(v_scale, "v_scale", torch.float32, 2)
-    shape, (rows, stride) = k_cache.shape, k_scale.shape
-    if v_cache.shape != shape or v_scale.shape != (rows, stride):
+    """The cache's code and sizes: code, num_blocks, block_size, Hkv, head_dim, stride."""
+    try:
+        code = _CODES.get(k_cache.dtype)
+        good = (code is not None and k_cache.is_cuda and k_cache.is_contiguous() and
+                v_cache.dtype is k_cache.dtype and v_cache.is_cuda and v_cache.is_contiguous() and
+                k_scale.dtype is _F32 and k_scale.is_cuda and k_scale.is_contiguous() and
+                v_scale.dtype is _F32 and v_scale.is_cuda and v_scale.is_contiguous() and
+                k_cache.dim() == 4 and k_scale.dim() == 2)
+    except AttributeError:
+        good = False
+    if not good:
+        dtype = getattr(k_cache, "dtype", None)
+        if dtype not in _CODES:
+            raise TypeError("k_cache must be torch.int8 or torch.float8_e4m3fn, got %s" % dtype)
+        _explain((k_cache, "k_cache", dtype, 4), (v_cache, "v_cache", dtype, 4),
+                 (k_scale, "k_scale", _F32, 2), (v_scale, "v_scale", _F32, 2))
+    nb, bs, Hkv, D = shape = k_cache.shape
+    rows, stride = scales = k_scale.shape
+    if v_cache.shape != shape or v_scale.shape != scales:
         raise ValueError("K and V caches, and their scales, must share one shape")
-    nb, bs, Hkv, D = shape
     if rows != nb or stride < Hkv:
         raise ValueError("scales must be [num_blocks, >= num_kv_heads]")
     return code, nb, bs, Hkv, D, stride
@@ -569,21 +610,31 @@ def reshape_and_cache_q8(k, v, query_start, block_tables, context_lens, k_cache,
     tokens.  One scale per (block, KV head): the largest magnitude over 127 (int8) or
     448 (e4m3); rows a block already holds are coded anew when its scale grows.
     prepare=True returns a PreparedLaunch instead of launching."""
-    _dev(k, "k", torch.float16, 3)
-    _dev(v, "v", torch.float16, 3)
-    _dev(query_start, "query_start", torch.int32, 1)
-    _dev(block_tables, "block_tables", torch.int32, 2)
-    _dev(context_lens, "context_lens", torch.int32, 1)
+    try:
+        good = (k.dtype is _F16 and k.is_cuda and k.is_contiguous() and
+                v.dtype is _F16 and v.is_cuda and v.is_contiguous() and
+                query_start.dtype is _I32 and query_start.is_cuda and
+                query_start.is_contiguous() and
+                block_tables.dtype is _I32 and block_tables.is_cuda and
+                block_tables.is_contiguous() and
+                context_lens.dtype is _I32 and context_lens.is_cuda and
+                context_lens.is_contiguous() and k.dim() == 3 and block_tables.dim() == 2)
+    except AttributeError:
+        good = False
+    if not good:
+        _explain((k, "k", _F16, 3), (v, "v", _F16, 3), (query_start, "query_start", _I32, 1),
+                 (block_tables, "block_tables", _I32, 2), (context_lens, "context_lens", _I32, 1))
     code, nb, bs, Hkv, D, stride = _q8_args(k_cache, v_cache, k_scale, v_scale)
-    T = k.shape[0]
+    T, Hkv2, D2 = rows = k.shape
     S, max_blocks = block_tables.shape
-    if k.shape != (T, Hkv, D) or v.shape != (T, Hkv, D):
+    if Hkv2 != Hkv or D2 != D or v.shape != rows:
         raise ValueError("shape mismatch")
-    if query_start.shape[0] != S + 1 or context_lens.shape[0] != S:
+    if query_start.shape != (S + 1,) or context_lens.shape != (S,):
         raise ValueError("query_start must have num_seqs + 1 entries, context_lens num_seqs")
-    args = (_ptr(k), _ptr(v), _ptr(query_start), _ptr(block_tables), _ptr(context_lens),
-            _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), code, T, S, Hkv, D, bs, nb,
-            max_blocks, stride, _ptr(dev_err), _stream_handle(stream))
+    args = (k.data_ptr(), v.data_ptr(), query_start.data_ptr(), block_tables.data_ptr(),
+            context_lens.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), code, T, S, Hkv, D, bs, nb, max_blocks, stride, _ptr(dev_err),
+            _stream_handle(stream))
     keep = (k, v, query_start, block_tables, context_lens, k_cache, v_cache, k_scale, v_scale,
             dev_err, stream) if prepare else None
     return _run(lib().pkv_reshape_and_cache_q8, args, "reshape_and_cache_q8", prepare, keep, None)
@@ -594,25 +645,33 @@ def paged_attention_decode_q8(out, q, k_cache, v_cache, k_scale, v_scale, block_
                               prepare=False):
     """paged_attention_decode over an 8-bit cache (see q8_cache, reshape_and_cache_q8);
     same workspace.  prepare=True returns a PreparedLaunch instead of launching."""
-    _dev(q, "q", torch.float16, 3)
-    _dev(out, "out", torch.float16, 3)
-    _dev(block_tables, "block_tables", torch.int32, 2)
-    _dev(context_lens, "context_lens", torch.int32, 1)
+    try:
+        good = (q.dtype is _F16 and q.is_cuda and q.is_contiguous() and
+                out.dtype is _F16 and out.is_cuda and out.is_contiguous() and
+                block_tables.dtype is _I32 and block_tables.is_cuda and
+                block_tables.is_contiguous() and
+                context_lens.dtype is _I32 and context_lens.is_cuda and
+                context_lens.is_contiguous() and q.dim() == 3 and block_tables.dim() == 2)
+    except AttributeError:
+        good = False
+    if not good:
+        _explain((q, "q", _F16, 3), (out, "out", _F16, 3),
+                 (block_tables, "block_tables", _I32, 2), (context_lens, "context_lens", _I32, 1))
     code, nb, bs, Hkv, D, stride = _q8_args(k_cache, v_cache, k_scale, v_scale)
-    S, Hq, D2 = q.shape
-    if out.shape != (S, Hq, D) or D2 != D:
+    S, Hq, D2 = shape = q.shape
+    if out.shape != shape or D2 != D:
         raise ValueError("shape mismatch")
     rows, max_blocks = block_tables.shape
-    if rows != S or context_lens.shape[0] != S:
+    if rows != S or context_lens.shape != (S,):
         raise ValueError("block_tables / context_lens must have num_seqs rows")
-    need = workspace_bytes(S, Hq, max_blocks, bs, D)
-    if need and workspace is None:
+    if workspace is None:
         workspace = alloc_workspace(S, Hq, max_blocks, q.device, bs)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    args = (_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), code,
-            _ptr(block_tables), _ptr(context_lens), S, Hq, Hkv, D, bs, nb, max_blocks,
-            stride, float(scale), _ptr(workspace), ws_bytes, _ptr(dev_err),
-            _stream_handle(stream))
+    args = (out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scale.data_ptr(), v_scale.data_ptr(), code, block_tables.data_ptr(),
+            context_lens.data_ptr(), S, Hq, Hkv, D, bs, nb, max_blocks, stride, float(scale),
+            _ptr(workspace), ws_bytes, _ptr(dev_err), _stream_handle(stream))
     keep = (out, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, workspace,
             dev_err, stream) if prepare else None
-    return _run(lib().pkv_paged_attention_decode_q8, args, "paged_attention_decode_q8", prepare, keep, out)
+    return _run(lib().pkv_paged_attention_decode_q8, args, "paged_attention_decode_q8", prepare,
+                keep, out)
