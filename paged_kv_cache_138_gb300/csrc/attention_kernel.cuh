@@ -41,7 +41,6 @@
 #pragma once
 
 #include <cuda.h>
-#include <cudaTypedefs.h>
 
 #include <atomic>
 #include <climits>
@@ -1010,12 +1009,6 @@ int launch_grouped(const CUtensorMap& mk, const CUtensorMap& mv, const Params& p
              ? PKV_OK
              : PKV_ERR_CUDA;
 }
-
-// Host helpers (defined in paged_attention.cu).
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
-bool supported_block_size(int bs);
-int seq_stride_for(int num_seqs);
-int launch_merge(const Params& p, cudaStream_t st);
 
 // Host launchers for one block size (defined in attention_bs*.cu).
 template <int BS>

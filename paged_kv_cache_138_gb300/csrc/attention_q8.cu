@@ -24,6 +24,7 @@
 //    TMA ring each and 3 CTAs an SM: 192 KB in flight, as the fp16 kernel.
 //  * Splits, their fp32 partials and the merge are the fp16 kernel's.
 #include <cuda.h>
+#include <cudaTypedefs.h>
 
 #include <algorithm>
 
@@ -32,6 +33,12 @@
 
 namespace pkv {
 namespace attn {
+
+// the fp16 launches' host helpers and merge kernel (paged_attention.cu)
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
+bool supported_block_size(int bs);
+int seq_stride_for(int num_seqs);
+__global__ void paged_attention_merge_kernel(const Params p);
 
 constexpr int kQ8Tile = 32;                      // tokens per stage
 constexpr int kQ8HalfBytes = kQ8Tile * kHeadDim; // K or V of a stage
@@ -340,8 +347,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
   bool ok = true;
   for (int k = 0; k < issued; ++k) {
-    const bool landed = mbar_wait_bounded(&bars[k % kStages], (k / kStages) & 1, p.dev_err);
-    ok = __all_sync(kFull, ok && landed) != 0;
+    if (ok) ok = warp_wait(&bars[k % kStages], (k / kStages) & 1, p.dev_err);
     if (ok) {
       const uint8_t* st = ring + (k % kStages) * kStageBytes;
       float ks[kBoxes], lv[kBoxes];
@@ -595,9 +601,12 @@ extern "C" int pkv_paged_attention_decode_q8(void* out, const void* q, const voi
                      ? launch_q8_bs<Int8Half, false>(block_size, mk, mv, qp, splits, st)
                      : launch_q8_bs<E4m3Half, true>(block_size, mk, mv, qp, splits, st);
   if (rc != PKV_OK) return rc;
-  if (p.max_splits < kWideSplits) return p.max_splits > 1 ? launch_merge(p, st) : PKV_OK;
+  if (p.max_splits <= 1) return PKV_OK;
+  // one row a warp, eight a CTA, or a CTA for each row of many splits
+  const int64_t rows = static_cast<int64_t>(num_seqs) * num_q_heads;
+  const bool wide = p.max_splits >= kWideSplits;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(num_seqs) * num_q_heads));
+  cfg.gridDim = dim3(static_cast<unsigned>(wide ? rows : (rows + kWideWarps - 1) / kWideWarps));
   cfg.blockDim = dim3(kWideWarps * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -605,5 +614,8 @@ extern "C" int pkv_paged_attention_decode_q8(void* out, const void* q, const voi
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, q8_wide_merge_kernel, p) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, wide ? q8_wide_merge_kernel : paged_attention_merge_kernel, p) ==
+                 cudaSuccess
+             ? PKV_OK
+             : PKV_ERR_CUDA;
 }

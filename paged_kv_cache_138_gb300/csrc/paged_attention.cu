@@ -64,25 +64,6 @@ __global__ void __launch_bounds__(kMergeRows * 32) paged_attention_merge_kernel(
   store_out4(p.out + row * kHeadDim + 4 * lane, den, num);
 }
 
-// The merge of a launch's split partials, as a programmatic dependent launch:
-// the merge grid is scheduled while the attention kernel's last CTAs run and
-// starts the moment it completes.
-int launch_merge(const Params& p, cudaStream_t st) {
-  const int64_t rows = static_cast<int64_t>(p.num_seqs) * p.num_q_heads;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + kMergeRows - 1) / kMergeRows));
-  cfg.blockDim = dim3(kMergeRows * 32);
-  cfg.dynamicSmemBytes = 0;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_attention_merge_kernel, p) == cudaSuccess ? PKV_OK
-                                                                                  : PKV_ERR_CUDA;
-}
-
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -277,7 +258,22 @@ int decode(void* out, const void* q, const void* k_new, const void* v_new, const
     }
   }
   if (rc != PKV_OK) return rc;
-  if (p.max_splits > 1) return launch_merge(p, st);
+  if (p.max_splits > 1) {
+    // programmatic dependent launch: the merge grid is scheduled while the
+    // attention kernel's last CTAs run and starts the moment it completes
+    const int64_t rows = static_cast<int64_t>(p.num_seqs) * p.num_q_heads;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((rows + kMergeRows - 1) / kMergeRows));
+    cfg.blockDim = dim3(kMergeRows * 32);
+    cfg.dynamicSmemBytes = 0;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, paged_attention_merge_kernel, p) != cudaSuccess) return PKV_ERR_CUDA;
+  }
   return PKV_OK;
 }
 

@@ -66,19 +66,12 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
                                                   int32_t* dev_err,
                                                   uint64_t limit_ns = kWaitLimitNs) {
   if (mbar_try_wait(bar, parity)) return true;
-  // the timer is read once in 64 attempts: a read takes longer than the usual
-  // remaining wait
-  uint64_t t0 = 0;
-  for (uint32_t i = 1;; ++i) {
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 63) == 0) {
-      const uint64_t now = global_timer_ns();
-      if (t0 == 0) {
-        t0 = now;
-      } else if (now - t0 > limit_ns) {
-        report(dev_err, PKV_DEV_WAIT_TIMEOUT);
-        return false;
-      }
+    if (global_timer_ns() - t0 > limit_ns) {
+      report(dev_err, PKV_DEV_WAIT_TIMEOUT);
+      return false;
     }
   }
 }

@@ -191,22 +191,6 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
   return done != 0;
 }
 
-// mbar_wait_bounded of a whole warp: one vote decides, so that no lane branches by
-// itself (30 cycles when the barrier is through already, 90 lane by lane), and the
-// limit is counted in clock cycles (2^30, half a second), which are quick to read.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* dev_err) {
-  constexpr unsigned kAll = 0xffffffffu;
-  if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
-  const uint32_t t0 = clock();
-  while (!__all_sync(kAll, mbar_try_wait(bar, parity))) {
-    if (__any_sync(kAll, static_cast<uint32_t>(clock()) - t0 > 1u << 30)) {
-      report(dev_err, PKV_DEV_WAIT_TIMEOUT);
-      return false;
-    }
-  }
-  return true;
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));

@@ -62,6 +62,24 @@ __device__ __forceinline__ int find_unit_seq(const int32_t* query_start, int num
   return lo;
 }
 
+// ---- waits ------------------------------------------------------------------------
+// A bounded wait of a whole warp on an mbarrier: one vote decides, so that no lane
+// branches by itself, and the limit is counted in clock cycles (2^30, half a second),
+// which are quick to read.  A barrier that is through already costs 30 cycles so, 90
+// with each lane branching and a look at the global timer.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* dev_err) {
+  constexpr unsigned kAll = 0xffffffffu;
+  if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
+  const uint32_t t0 = clock();
+  while (!__all_sync(kAll, mbar_try_wait(bar, parity))) {
+    if (__any_sync(kAll, static_cast<uint32_t>(clock()) - t0 > 1u << 30)) {
+      report(dev_err, PKV_DEV_WAIT_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
 // ---- codes ------------------------------------------------------------------------
 // A code c of a block and KV head stands for c * scale.  int8: -127..127;
 // e4m3: the finite values, at most 448 in magnitude.
