@@ -4,6 +4,26 @@
 //   out[i, h] = sum_{t <= pos} softmax_t(scale <q[i, h], K[t, g]>) V[t, g]
 // with K and V either in the paged fp16 cache (context_lens[s] tokens, the
 // packed rows the last of them) or packed like q.
+//
+// How:
+//  * A unit of work is 256 rows of one KV head: 256 / group tokens with the
+//    group's query heads side by side, so that grouped heads share every K and V
+//    tile and the tiles along the diagonal are short.  Two query tiles of 128
+//    rows take turns: while one's 128 x 128 products run on the tensor core the
+//    other's softmax runs on the CUDA cores.
+//  * S = Q K^T (operands in shared memory) and O += P V (P in tensor memory, over
+//    the scores it came from) accumulate in fp32 in tensor memory: 2 x 128 columns
+//    of scores and 2 x 128 of outputs, all 512.
+//  * One softmax thread owns a row of scores.  Its running maximum moves only when
+//    a score passes it by more than 2^8, so O is rescaled in few tiles; the weights,
+//    at most 2^8, are rounded to fp16 for the product with V; their sum is fp32.
+//  * K and V come through a ring of four 32 KB tiles, by TMA: a box for each block
+//    (paged) or for 128 tokens (packed).
+//  * What bounds it: in steady state a turn (128 tokens for 256 rows) takes 2300
+//    cycles, of which the tensor core is busy 2048; a unit adds some 4000 at its
+//    ends.  16,384 tokens of 32/8 heads: 1197-1267 us, 1.74-1.84 PFLOP/s (the
+//    measured cuBLAS burst is 1.96; the chip runs at its power limit); 4 x 4096 of 32
+//    heads: 344 us, 1.60.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -58,6 +78,7 @@ struct Smem {
   static constexpr int answer = (drained + 16 + 15) / 16 * 16;
   static constexpr int unit = answer + 16;
   static constexpr int tmem = unit + 64;
+  static constexpr int gave_up = tmem + 4;               // a wait did
   static constexpr int total = tmem + 16;
   static constexpr int alloc = total + 1024;
   static_assert(alloc <= 227 * 1024, "shared memory of one CTA");
@@ -191,6 +212,24 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
   return done != 0;
 }
 
+// warp_wait with short code: a wait that gives up only raises a flag in shared memory,
+// which the CTA reports at its end.  There are some 45 waits, and code counts: what is
+// not in the instruction cache costs some 100 cycles for 8 instructions, and a unit's
+// first and last steps run code that the steps between have pushed out (the kernel
+// shrunk from 77 to 56 KB ran 5 % faster on prompts of 2048 tokens).
+__device__ __forceinline__ bool flag_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* gave_up) {
+  constexpr unsigned kAll = 0xffffffffu;
+  if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
+  const uint32_t t0 = clock();
+  while (!__all_sync(kAll, mbar_try_wait(bar, parity))) {
+    if (__any_sync(kAll, static_cast<uint32_t>(clock()) - t0 > 1u << 30)) {
+      *gave_up = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -219,7 +258,8 @@ constexpr uint32_t kNegateA = 1u << 13;
 // A unit with rows in one tile only (a short chunk, the rest of a prompt) is a
 // pair: both warpgroups work on tile 0's rows, on every other KV tile each, and
 // the first joins the two results.  Alone a tile waits for its own products and
-// weights in turn, 3100 cycles a KV tile instead of 1200.
+// weights in turn, 3100 cycles a KV tile; a pair takes 1200 to 2000 (copies of
+// 16-token blocks).
 struct alignas(16) Unit {
   int row0, n, ctx, s;   // the sequence (see PackedSeq) and its index
   int g, split;
@@ -305,7 +345,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int64_t max_context = BS ? static_cast<int64_t>(p.max_blocks) * BS : INT32_MAX;
   const auto bar = [&](int at, int i) { return reinterpret_cast<uint64_t*>(smem + at) + i; };
-  const auto wait = [&](uint64_t* b, uint32_t parity) { return warp_wait(b, parity, p.dev_err); };
+  volatile uint32_t* gave_up = reinterpret_cast<volatile uint32_t*>(smem + Smem::gave_up);
+  const auto wait = [&](uint64_t* b, uint32_t parity) { return flag_wait(b, parity, gave_up); };
   if (warp == kCopyWarp && lane == 0) {
     prefetch_tmap(&tmap_q);
     prefetch_tmap(&tmap_k);
@@ -329,6 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(Smem::unit_empty, 0), kReaders);
     mbar_init(bar(Smem::stolen, 0), 1);
     mbar_init(bar(Smem::drained, 0), 1);
+    *gave_up = 0;
     fence_barrier_init();
   }
   if (warp == kMmaWarp) {
@@ -362,31 +404,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       // a box of 16 rows every 73 cycles.
       const int mine = warp == kCopyVWarp;
       constexpr int kBoxes = BS ? kTile / (BS ? BS : 1) : 1;
-      int st = 0, round = 0, nraw = 0;   // ring position, cleaned tiles
-      int nq[2] = {0, 0};                // Q copies issued
+      static_assert((kStages & (kStages - 1)) == 0, "ring positions by shifts");
+      int base = 0, nraw = 0;                 // the unit's first place in the ring, cleaned tiles
+      uint32_t q_seen = 0, q_parity = 0;      // bit x: Q copies of tile x so far
+      uint32_t kv_seen = 0, kv_parity = 0;    // bit st: this warp's copies into a stage
       bool ok = true;
       Unit u;
       for (int k = 0; ok && next_unit(k, u); ++k) {
         const Tail<BS> tail(u);
-        const auto copy_q = [&] {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (!ok || u.end[x] == u.begin) continue;
-            if (nq[x] > 0) ok = wait(bar(Smem::q_empty, x), (nq[x] - 1) & 1);
-            if (!ok) continue;
-            ++nq[x];
-            if (lane == 0) {
-              uint64_t* b = bar(Smem::q_full, x);
-              uint8_t* dst = smem + Smem::q + x * kTileBytes;
-              mbar_arrive_expect_tx(b, kTileBytes);
-              for (int h = 0; h < 2; ++h)
-                tma_load_3d(dst + h * kHalfBytes, &tmap_q, 64 * h, u.g << p.group_shift,
-                            u.row0 + u.tok0[x], b);
-            }
-          }
-        };
-        // the block id of this lane's part of tile j (paged): loaded ahead, looked at when
-        // the tile's turn comes
+        const int n = u.last - u.begin;
+        // the block id of this lane's part of tile j (paged): loaded a tile ahead
         const auto id_of = [&](int j) {
           const int tok = j * kTile + lane * BS;
           return BS && lane < kBoxes && j >= u.begin && tok < u.ctx
@@ -394,93 +421,94 @@ __global__ void __launch_bounds__(kThreads, 1)
                              tok / (BS ? BS : 1))
                      : -1;
         };
-        const auto row_of = [&](int j, int32_t id) {
-          if (BS == 0) return u.row0 + j * kTile;
-          if (id >= 0 && id < p.num_blocks) return id * BS;
-          if (lane < kBoxes && j * kTile + lane * BS < u.ctx)
-            report(p.dev_err, PKV_DEV_BAD_BLOCK_ID);
-          return static_cast<int>(p.num_blocks * BS);   // past the last row: zeros
-        };
-        const auto load = [&](int kv, int j, int row) {
-          if (kv == mine && ok) {
-            if (round > 0) ok = wait(bar(Smem::kv_empty, st), (round - 1) & 1);
-            if (!ok) return;
-            const bool raw = kv == 1 && tail.clean && j == tail.tile;
-            uint64_t* b = raw ? bar(Smem::raw, 0) : bar(Smem::kv_full, st);
-            uint8_t* dst = smem + Smem::kv + st * kTileBytes;
-            if (lane == 0) mbar_arrive_expect_tx(b, kTileBytes);
-            __syncwarp();
-            if (lane < kBoxes) {
-              const CUtensorMap* m = kv ? &tmap_v : &tmap_k;
-              if (BS) {
-                tma_load_5d(dst + lane * (kTileBytes / kBoxes), m, 0, 0, 0, row >> 3, u.g, b);
-              } else {
-                tma_load_3d(dst, m, 0, u.g, row, b);
-                tma_load_3d(dst + kHalfBytes, m, 64, u.g, row, b);
-              }
-            }
-            if (kv == 0 && j == u.last - 1) copy_q();
-            if (raw) {   // zeros in the rows past the context, then the tile may be used
-              ok = wait(b, nraw & 1);
-              ++nraw;
-              const uint32_t at = smem_u32(dst);
-              for (int i = lane; ok && i < (tail.dirty_end - tail.valid) * 16; i += 32) {
-                const int r = tail.valid + (i >> 4);
-                st_shared_zero16(at + (i & 8 ? Kv::kHalf : 0) + (r >> 3) * Kv::kEight +
-                                 (r & 7) * 128 + (i & 7) * 16);
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar(Smem::kv_full, st));
-            }
-          }
-          if (++st == kStages) {
-            st = 0;
-            ++round;
-          }
-        };
-        // a tile's V follows its K, in a pair the next tile's K; K of tile j - ahead then
-        // comes with V of tile j
-        const int ahead = u.pair ? 2 : 1;
-        int32_t id0 = id_of(u.last - 1), id1 = id_of(u.last - 2);
-        int row0 = row_of(u.last - 1, id0), row1 = 0;
-        int32_t id2 = id_of(u.last - 3);
-        load(0, u.last - 1, row0);
-        if (u.pair) {
-          row1 = row_of(u.last - 2, id1);
-          load(0, u.last - 2, row1);
-        }
+        int32_t id = id_of(u.last - 1);
 #pragma unroll 1
-        for (int j = u.last - 1; j >= u.begin && ok; --j) {
-          const int32_t id3 = id_of(j - 3);
-          load(1, j, row0);
-          if (j - ahead >= u.begin) {
-            const int next = row_of(j - ahead, u.pair ? id2 : id1);
-            load(0, j - ahead, next);
-            row0 = u.pair ? row1 : next;
-            row1 = next;
-          } else {
-            row0 = row1;
+        for (int i = 0; i < n && ok; ++i) {
+          const int j = u.last - 1 - i;
+          const int32_t next_id = id_of(j - 1);
+          // where the tile's K or V comes in the ring: V after its K, in a pair after the
+          // next tile's K
+          const int at = !u.pair ? 2 * i + mine
+                         : mine  ? (i + 1 < n ? 2 * i + 2 : 2 * n - 1)
+                                 : max(0, 2 * i - 1);
+          const int st = (base + at) & (kStages - 1), round = (base + at) / kStages;
+          int row = u.row0 + j * kTile;
+          if (BS) {
+            row = static_cast<int>(p.num_blocks * BS);   // past the last row: zeros
+            if (id >= 0 && id < p.num_blocks)
+              row = id * BS;
+            else if (lane < kBoxes && j * kTile + lane * BS < u.ctx)
+              report(p.dev_err, PKV_DEV_BAD_BLOCK_ID);
           }
-          id1 = id2;
-          id2 = id3;
+          id = next_id;
+          if (round > 0) ok = wait(bar(Smem::kv_empty, st), (round - 1) & 1);
+          if (!ok) break;
+          kv_seen |= 1u << st;
+          kv_parity = (kv_parity & ~(1u << st)) | (round & 1) << st;
+          const bool raw = mine && tail.clean && j == tail.tile;
+          uint64_t* b = raw ? bar(Smem::raw, 0) : bar(Smem::kv_full, st);
+          uint8_t* dst = smem + Smem::kv + st * kTileBytes;
+          if (lane == 0) mbar_arrive_expect_tx(b, kTileBytes);
+          __syncwarp();
+          if (lane < kBoxes) {
+            const CUtensorMap* m = mine ? &tmap_v : &tmap_k;
+            if (BS) {
+              tma_load_5d(dst + lane * (kTileBytes / kBoxes), m, 0, 0, 0, row >> 3, u.g, b);
+            } else {
+              tma_load_3d(dst, m, 0, u.g, row, b);
+              tma_load_3d(dst + kHalfBytes, m, 64, u.g, row, b);
+            }
+          }
+          if (raw) {   // zeros in the rows past the context, then the tile may be used
+            ok = wait(b, nraw & 1);
+            ++nraw;
+            const uint32_t to = smem_u32(dst);
+            for (int c = lane; ok && c < (tail.dirty_end - tail.valid) * 16; c += 32) {
+              const int r = tail.valid + (c >> 4);
+              st_shared_zero16(to + (c & 8 ? Kv::kHalf : 0) + (r >> 3) * Kv::kEight + (r & 7) * 128 +
+                               (c & 7) * 16);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(Smem::kv_full, st));
+          }
+          if (i == 0 && !mine) {
+#pragma unroll 1
+            for (int x = 0; x < 2 && ok; ++x) {
+              if ((x ? u.end[1] : u.end[0]) == u.begin) continue;
+              if (q_seen >> x & 1)
+                ok = wait(bar(Smem::q_empty, x), (q_parity >> x & 1) ^ 1);
+              if (!ok) break;
+              q_seen |= 1u << x;
+              q_parity ^= 1u << x;
+              if (lane == 0) {
+                uint64_t* qb = bar(Smem::q_full, x);
+                uint8_t* to = smem + Smem::q + x * kTileBytes;
+                mbar_arrive_expect_tx(qb, kTileBytes);
+                for (int h = 0; h < 2; ++h)
+                  tma_load_3d(to + h * kHalfBytes, &tmap_q, 64 * h, u.g << p.group_shift,
+                              u.row0 + (x ? u.tok0[1] : u.tok0[0]), qb);
+              }
+            }
+          }
         }
+        base += 2 * n;
       }
-      if (!ok) {   // a wait gave up: let this CTA's copies land before it goes
-        for (int i = 0; i < kStages; ++i) {
-          const int done = round + (i < st);   // copies into stage i
-          if (done > 0) mbar_wait_bounded(bar(Smem::kv_full, i), (done - 1) & 1, p.dev_err);
-        }
+      if (!ok) {   // a wait gave up: let this warp's copies land before the CTA goes
+#pragma unroll 1
+        for (int i = 0; i < kStages; ++i)
+          if (kv_seen >> i & 1) wait(bar(Smem::kv_full, i), kv_parity >> i & 1);
+#pragma unroll 1
         for (int x = 0; x < 2; ++x)
-          if (nq[x] > 0) mbar_wait_bounded(bar(Smem::q_full, x), (nq[x] - 1) & 1, p.dev_err);
+          if (q_seen >> x & 1) wait(bar(Smem::q_full, x), (q_parity >> x & 1) ^ 1);
       }
     } else if (warp == kMmaWarp) {
       // ---- matrix products: the warp runs together, one elected lane issues ------------------
       // (operands stay in uniform registers that way; a loop of one diverged lane took 85
       // cycles to issue a product that runs for 64).  The tensor core holds some 7 products
-      // in its queue, and a wait takes about 100 cycles even when what it waits for is there:
-      // the waits for K and V are kept out of the stretch between one tile's products and
-      // the other's weights.  One warp issues for both tiles, a whole batch at a time: with a
+      // in its queue, and a wait takes 30 cycles even when what it waits for is there: the
+      // waits for K and V are kept out of the stretch between one tile's products and the
+      // other's weights.  One warp issues for both tiles, a whole batch at a time: with a
       // warp for each their products alternate, end together and the tiles fall into step
       // (3400 cycles a pair of tiles instead of 2800).
       struct Ring {
@@ -655,11 +683,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // every product has completed before the tensor memory is given back
       commit(bar(Smem::drained, 0));
-      mbar_wait_bounded(bar(Smem::drained, 0), 0, p.dev_err);
-      __syncwarp();
+      wait(bar(Smem::drained, 0), 0);
     } else if (warp == kWorkWarp) {
       // ---- work: the CTA's own unit, then those of CTAs that have not started -------------
       if (blockIdx.x == 0 && blockIdx.y == 0)   // every entry is looked at once, used or not
+#pragma unroll 1
         for (int s = lane; s < p.num_seqs; s += 32)
           packed_seq(p.query_start, p.context_lens, s, p.num_tokens, max_context, p.dev_err, true);
       int bx = blockIdx.x, by = blockIdx.y;
@@ -735,19 +763,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         ++ns;
         fence_after();
+        if (j * kTile + kTile - 1 > pos0) {
+          // some row of the tile does not see all of it: mask the scores in place, 32 columns
+          // at a time
+          const int see = pos - j * kTile;                    // columns 0 .. see
+          const int all = __shfl_sync(kFull, see, 0);         // lane 0 sees the fewest
+#pragma unroll 1
+          for (int q = max(0, all + 1) & ~31; q < kTile; q += 32) {
+            uint32_t v[32];
+            tmem_ld32(s_at + q, v);
+            wait_ld();
+            const int left = see - q;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) v[c] = c <= left ? v[c] : 0xff800000u;
+            tmem_st32(s_at + q, v);
+          }
+          wait_st();
+        }
         float s[kTile];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, reinterpret_cast<uint32_t*>(s + 32 * c));
         wait_ld();
-        if (j * kTile + kTile - 1 > pos0) {   // some row of the tile does not see all of it
-          const int see = pos - j * kTile;    // columns 0 .. see; lane 0 sees the fewest
-          const int all = __shfl_sync(kFull, see, 0);
-#pragma unroll
-          for (int q = 0; q < kTile; q += 32)
-            if (q + 31 > all)
-#pragma unroll
-              for (int c = q; c < q + 32; ++c) s[c] = c <= see ? s[c] : -INFINITY;
-        }
         float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
         for (int c = 4; c < kTile - 4; c += 8)
@@ -854,22 +890,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (mine32) {
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
-          uint32_t h[32];
-#pragma unroll
+          if (lane == 0) bulk_wait_read();   // the last rows have left the buffer
+          __syncwarp();
+#pragma unroll 1
           for (int d = 0; d < 2; ++d) {
             uint32_t o[32];
             take(64 * c + 32 * d, o);
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              h[16 * d + i] = pack_half2(__uint_as_float(o[2 * i]) * inv,
-                                         __uint_as_float(o[2 * i + 1]) * inv);
-          }
-          if (lane == 0) bulk_wait_read();   // the last rows have left the buffer
-          __syncwarp();
+            for (int i = 0; i < 4; ++i) {
+              uint32_t h[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            box[lane * 8 + (i ^ (lane & 7))] =
-                make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+              for (int e = 0; e < 4; ++e)
+                h[e] = pack_half2(__uint_as_float(o[8 * i + 2 * e]) * inv,
+                                  __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
+              box[lane * 8 + ((4 * d + i) ^ (lane & 7))] = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+          }
           fence_proxy_async_smem();
           __syncwarp();
           if (mine32 == kFull) {
@@ -877,6 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_store_3d(&tmap_o, box, 64 * c, u.g << p.group_shift,
                            u.row0 + u.tok0[x] + ((warp & 3) * 32 >> p.group_shift));
           } else {   // the sequence's last rows: only those
+#pragma unroll 1
             for (int i = 0; i < 8; ++i) {
               const int rr = 4 * i + (lane >> 3), ch = lane & 7;
               const int64_t to = __shfl_sync(kFull, row, rr);
@@ -913,6 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *gave_up) report(p.dev_err, PKV_DEV_WAIT_TIMEOUT);
   if (warp == kMmaWarp) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
