@@ -387,9 +387,8 @@ int pkv_copy_blocks(void* const* k_caches, void* const* v_caches, int num_layers
  *   out, q       fp16 [num_tokens, num_q_heads, 128], 16-byte aligned; rows of out
  *                that no sequence owns are left as they were
  *   k_cache, v_cache  fp16 [num_blocks, block_size, num_kv_heads, 128], 16-byte
- *                aligned; rows past a context may hold anything.  K and V of a
- *                context's own tokens must be finite: a V row that is not also
- *                spoils rows of q up to 127 positions before it
+ *                aligned; rows past a context may hold anything, and an infinity
+ *                or NaN of a context's own tokens reaches the rows that see it only
  *   block_tables int32 [num_seqs, max_blocks_per_seq] (device)
  *   context_lens int32 [num_seqs] (device)
  *   query_start  int32 [num_seqs + 1] (device), ascending, at most num_tokens

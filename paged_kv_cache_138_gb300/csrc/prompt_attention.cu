@@ -79,6 +79,8 @@ struct Smem {
   static constexpr int unit = answer + 16;
   static constexpr int tmem = unit + 64;
   static constexpr int gave_up = tmem + 4;               // a wait did
+  static constexpr int nonfinite = tmem + 8;             // [2] the last odd and even unit in whose
+                                                         // V some values were set to zero
   static constexpr int total = tmem + 16;
   static constexpr int alloc = total + 1024;
   static_assert(alloc <= 227 * 1024, "shared memory of one CTA");
@@ -100,6 +102,7 @@ constexpr uint32_t kColS = 0, kColO = 256;
 
 struct Params {
   __half* out;
+  const __half* v;
   const int32_t* query_start;
   const int32_t* context_lens;   // nullptr: K and V are packed like q
   const int32_t* block_tables;
@@ -236,6 +239,22 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+  uint4 w;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+               : "r"(addr)
+               : "memory");
+  return w;
+}
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint4 w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w.x), "r"(w.y), "r"(w.z),
+               "r"(w.w)
+               : "memory");
+}
+__device__ __forceinline__ __half2 u32_as_half2(uint32_t w) { return *reinterpret_cast<__half2*>(&w); }
+__device__ __forceinline__ uint32_t half2_as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+
 // Shared-memory operand descriptor, 128-byte swizzle.  K-major (Q, K): rows of
 // 128 bytes, 8-row groups `stride` apart.  MN-major (V): 64-dim chunks
 // `lead` apart, 8-token groups `stride` apart.
@@ -308,20 +327,81 @@ __device__ __forceinline__ bool make_unit(const Params& p, int bx, int by, int64
   return u.last > u.begin;
 }
 
-// Rows of the last KV tile past the context: whatever the copy brings there,
-// 0 * NaN must not reach a sum.  (A paged block wholly past the context is
-// read from past the cache's last row, where the copy engine fills zeros.)
+// Tokens of a KV tile that some row of the unit does not see have a weight of 0
+// there, and 0 * NaN must not reach a sum.  So before the product their V is made
+// finite in shared memory: tokens that no row of the unit sees, those past the
+// context among them (whatever the copy brings there; a paged block wholly past
+// the context is read from past the cache's last row, where the copy engine fills
+// zeros), become zeros; the others are searched for infinities and NaN, which
+// become zeros too and are added to the rows that see them at the end (add_nonfinite).
+// The search costs 1 % (4 x 4096 of 32 heads 356 us, 351 without; 16 x 512 of 32/8 47.2
+// and 45.9).  The warp that copies V does it: in the work warp, which has the time,
+// 64 prompts of 128 take 40.6 us instead of 36.6; one tile late, under the next
+// copy, 4 x 4096 takes 361.
 template <int BS>
-struct Tail {
-  int tile, valid, dirty_end;
-  bool clean;
-  __device__ __forceinline__ explicit Tail(const Unit& u) {
-    tile = (u.ctx - 1) / kTile;
-    valid = u.ctx - tile * kTile;
-    dirty_end = BS ? min(kTile, (valid + BS - 1) / (BS ? BS : 1) * BS) : kTile;
-    clean = tile < u.last && tile >= u.begin && dirty_end > valid;
+struct Masked {
+  int seen, unseen, end;   // tokens of the tile: [seen, unseen) by some rows, [unseen, end) by none
+  __device__ __forceinline__ Masked(const Unit& u, int group_shift, int j) {
+    const int at = u.ctx - u.n - j * kTile;   // the first packed row's place in the tile
+    unseen = min(kTile, at + min(u.n, u.tok0[0] + (kTile >> group_shift)));
+    seen = min(unseen, max(0, at + (j < u.end[1] ? u.tok0[1] : u.tok0[0]) + 1));
+    const int valid = u.ctx - j * kTile;
+    end = BS ? min(kTile, (valid + BS - 1) / (BS ? BS : 1) * BS) : kTile;
   }
+  __device__ __forceinline__ bool any() const { return seen < end; }
 };
+
+// infinities and NaN of a pair become zeros
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+  if ((w & 0x7c00u) == 0x7c00u) w &= 0xffff0000u;
+  if ((w & 0x7c000000u) == 0x7c000000u) w &= 0x0000ffffu;
+  return w;
+}
+
+// The infinities and NaN that Masked took out of the unit's V are added to the output in
+// tensor memory (a whole warp, a row each lane): the row that sees a token has a positive
+// weight for it.  Seldom run, so it is short and reads V again, token after token.
+template <int BS>
+__device__ __forceinline__ void add_nonfinite(const Params& p, const Unit& u, uint32_t o_at, int pos,
+                                           int end) {
+  const int per = kTile >> p.group_shift;
+  const int from = max(u.begin * kTile, u.ctx - u.n + u.tok0[1] + 1);
+  const int to = min(end * kTile, u.ctx - u.n + min(u.n, u.tok0[0] + per));
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t o[32];
+    tmem_ld32(o_at + 32 * c, o);
+    wait_ld();
+#pragma unroll 1
+    for (int t = from; t < to; ++t) {
+      int64_t row = static_cast<int64_t>(u.row0) + t;
+      if (BS) {
+        const int32_t id = __ldg(p.block_tables + static_cast<int64_t>(u.s) * p.max_blocks +
+                                 t / (BS ? BS : 1));
+        if (id < 0 || id >= p.num_blocks) continue;   // read as zeros
+        row = static_cast<int64_t>(id) * BS + t % (BS ? BS : 1);
+      }
+      const uint4* v = reinterpret_cast<const uint4*>(
+          p.v + (row * p.num_kv_heads + u.g) * kHeadDim + 32 * c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 w4 = __ldg(v + i);
+        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t rest = w[e] ^ finite2(w[e]);   // the bits that were taken out
+          const float2 f = half2_to_float2(rest);
+          if (t <= pos) {
+            o[8 * i + 2 * e] = __float_as_uint(__uint_as_float(o[8 * i + 2 * e]) + f.x);
+            o[8 * i + 2 * e + 1] = __float_as_uint(__uint_as_float(o[8 * i + 2 * e + 1]) + f.y);
+          }
+        }
+      }
+    }
+    tmem_st32(o_at + 32 * c, o);
+  }
+  wait_st();
+}
 
 // BS: block size of the paged cache, 0 for packed K and V.
 //
@@ -346,6 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t max_context = BS ? static_cast<int64_t>(p.max_blocks) * BS : INT32_MAX;
   const auto bar = [&](int at, int i) { return reinterpret_cast<uint64_t*>(smem + at) + i; };
   volatile uint32_t* gave_up = reinterpret_cast<volatile uint32_t*>(smem + Smem::gave_up);
+  volatile int* nonfinite = reinterpret_cast<volatile int*>(smem + Smem::nonfinite);
   const auto wait = [&](uint64_t* b, uint32_t parity) { return flag_wait(b, parity, gave_up); };
   if (warp == kCopyWarp && lane == 0) {
     prefetch_tmap(&tmap_q);
@@ -371,6 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(Smem::stolen, 0), 1);
     mbar_init(bar(Smem::drained, 0), 1);
     *gave_up = 0;
+    nonfinite[0] = nonfinite[1] = -1;
     fence_barrier_init();
   }
   if (warp == kMmaWarp) {
@@ -411,7 +493,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       Unit u;
       for (int k = 0; ok && next_unit(k, u); ++k) {
-        const Tail<BS> tail(u);
         const int n = u.last - u.begin;
         // the block id of this lane's part of tile j (paged): loaded a tile ahead
         const auto id_of = [&](int j) {
@@ -445,7 +526,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           kv_seen |= 1u << st;
           kv_parity = (kv_parity & ~(1u << st)) | (round & 1) << st;
-          const bool raw = mine && tail.clean && j == tail.tile;
+          const Masked<BS> masked(u, p.group_shift, j);
+          const bool raw = mine && masked.any();
           uint64_t* b = raw ? bar(Smem::raw, 0) : bar(Smem::kv_full, st);
           uint8_t* dst = smem + Smem::kv + st * kTileBytes;
           if (lane == 0) mbar_arrive_expect_tx(b, kTileBytes);
@@ -459,18 +541,40 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_3d(dst + kHalfBytes, m, 64, u.g, row, b);
             }
           }
-          if (raw) {   // zeros in the rows past the context, then the tile may be used
+          if (raw) {   // the tile may be used once its masked tokens are finite
             ok = wait(b, nraw & 1);
             ++nraw;
             const uint32_t to = smem_u32(dst);
-            for (int c = lane; ok && c < (tail.dirty_end - tail.valid) * 16; c += 32) {
-              const int r = tail.valid + (c >> 4);
-              st_shared_zero16(to + (c & 8 ? Kv::kHalf : 0) + (r >> 3) * Kv::kEight + (r & 7) * 128 +
-                               (c & 7) * 16);
+            const auto chunk = [&](int c) {   // 16 bytes: token c / 16, dims 8 (c % 16)
+              const int r = c >> 4;
+              return to + (c & 8 ? Kv::kHalf : 0) + (r >> 3) * Kv::kEight + (r & 7) * 128 +
+                     (c & 7) * 16;
+            };
+            // 0 * x adds a zero, and for an infinity or NaN a NaN
+            const __half2 zero = __floats2half2_rn(0.f, 0.f);
+            __half2 acc[4] = {zero, zero, zero, zero};
+#pragma unroll 4
+            for (int c = masked.seen * 16 + lane; c < masked.unseen * 16; c += 32) {
+              const uint4 w = ld_shared16(chunk(c));
+              acc[0] = __hfma2(u32_as_half2(w.x), zero, acc[0]);
+              acc[1] = __hfma2(u32_as_half2(w.y), zero, acc[1]);
+              acc[2] = __hfma2(u32_as_half2(w.z), zero, acc[2]);
+              acc[3] = __hfma2(u32_as_half2(w.w), zero, acc[3]);
             }
+            if (__any_sync(kFull, half2_as_u32(acc[0]) | half2_as_u32(acc[1]) | half2_as_u32(acc[2]) |
+                                      half2_as_u32(acc[3]))) {
+#pragma unroll 1
+              for (int c = masked.seen * 16 + lane; c < masked.unseen * 16; c += 32) {
+                const uint4 w = ld_shared16(chunk(c));
+                st_shared16(chunk(c), make_uint4(finite2(w.x), finite2(w.y), finite2(w.z), finite2(w.w)));
+              }
+              if (lane == 0) nonfinite[k & 1] = k;
+            }
+            for (int c = masked.unseen * 16 + lane; c < masked.end * 16; c += 32)
+              st_shared_zero16(chunk(c));
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(Smem::kv_full, st));
+            if (lane == 0 && ok) mbar_arrive(bar(Smem::kv_full, st));
           }
           if (i == 0 && !mine) {
 #pragma unroll 1
@@ -857,6 +961,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = wait(bar(Smem::o_full, x), o_turn[x] & 1);
       if (!ok) break;
       fence_after();
+      if (nonfinite[k & 1] == k)
+        add_nonfinite<BS>(p, u, o_at, pos, u.pair ? u.last : u.end[x]);
       const int head = (u.g << p.group_shift) + (r & ((1 << p.group_shift) - 1));
       const int64_t row = (static_cast<int64_t>(u.row0) + tok) * p.num_q_heads + head;
       const bool mine = tok < u.n;
@@ -1124,6 +1230,7 @@ int run(void* out, const void* q, const void* k, const void* v, const int32_t* b
     p.part_ml = p.part_o + rows * p.splits * kHeadDim;
   }
   p.out = static_cast<__half*>(out);
+  p.v = static_cast<const __half*>(v);
   p.query_start = query_start;
   p.context_lens = context_lens;
   p.block_tables = block_tables;

@@ -368,3 +368,84 @@ def test_wrappers_refuse(ops):
     from paged_kv_cache_138_gb300._lib import PagedKVError
     with pytest.raises(PagedKVError):
         ops.prompt_attention(q[:, :6].contiguous(), q[:, :6].contiguous(), k, k, qs, 1.0)
+
+
+# ---- infinities and NaN in a context's own V -----------------------------------------------
+
+def check_nonfinite(got, q, k, v, first):
+    """Values of V that are not finite reach the rows that see their token, in their
+    column, and no others: those match the definition with zeros in their place."""
+    bad = ~np.isfinite(v)                                            # [L, Hkv, D]
+    n, Hq = q.shape[:2]
+    L, Hkv = v.shape[:2]
+    see = np.arange(L)[None] <= (first + np.arange(n))[:, None]
+    hit = np.einsum("nl,lgd->ngd", see.astype(np.int64), bad.astype(np.int64)) > 0
+    hit = np.repeat(hit, Hq // Hkv, axis=1)
+    clean = np.where(bad, np.float16(0), v)
+    ref, spread, peak, mag, vmax = op.attend(q, k, clean, first, SCALE)
+    got = np.asarray(got, np.float64)
+    assert np.array_equal(~np.isfinite(got), hit)
+    over = np.abs(got - ref) - tolerance(ref, spread, peak, mag, vmax, L)
+    assert over[~hit].max(initial=-1) <= 0, over[~hit].max()
+    for sign in (1, -1):        # one infinity and nothing else in the column: its sign
+        inf = np.where(bad, np.where(v == sign * np.inf, 1, 10 ** 6), 0)
+        only = np.repeat(np.einsum("nl,lgd->ngd", see.astype(np.int64), inf), Hq // Hkv, axis=1) == 1
+        assert (got[only] == sign * np.inf).all()
+
+
+def plant(rng, v, tokens):
+    for t in tokens:
+        g, d = rng.integers(v.shape[1]), rng.choice(D, 3, replace=False)
+        v[t, g, d] = [np.inf, -np.inf, np.nan]
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (8, 2), (8, 1)])
+@pytest.mark.parametrize("n", [2, 40, 128, 129, 257, 600])
+def test_packed_nonfinite_values_reach_later_rows_only(ops, Hq, Hkv, n):
+    rng = np.random.default_rng(n + Hq)
+    new = [5, n, 30]
+    T = sum(new)
+    q = wl.host_normal_fp16(rng, (T, Hq, D))
+    k, v = (wl.host_normal_fp16(rng, (T, Hkv, D)) for _ in "kv")
+    qs = starts(new)
+    plant(rng, v, {int(qs[1]) + t for t in (n - 1, n // 2, min(n - 1, 127), min(n - 1, 130))})
+    got, err = run_packed(ops, q, k, v, qs)
+    assert err == 0
+    for s in range(len(new)):
+        a, b = qs[s], qs[s + 1]
+        check_nonfinite(got[a:b], q[a:b], k[a:b], v[a:b], 0)
+
+
+@pytest.mark.parametrize("bs", [8, 16, 32, 64])
+@pytest.mark.parametrize("Hq,Hkv,new,cached", [
+    (8, 8, [200, 3], [77, 500]),         # several tiles; a pair of warpgroups on one tile's rows
+    (8, 2, [70, 129], [0, 127]),
+    (8, 1, [9, 1, 2], [1000, 1500, 30]),
+    (8, 2, [6, 40], [4000, 2500]),       # a split key axis
+])
+def test_paged_nonfinite_values_reach_later_rows_only(ops, bs, Hq, Hkv, new, cached):
+    rng = np.random.default_rng(bs + sum(new))
+    q, kc, vc, tables, lens = paged_case(bs, new, cached, Hq, Hkv, bs)
+    for s, n in enumerate(new):
+        for t in {int(lens[s]) - 1, int(lens[s]) - 1 - n // 2, max(0, int(lens[s]) - n)}:
+            row = vc[tables[s][t // bs], t % bs][None]
+            plant(rng, row, [0])
+    got, err = run_paged(ops, q, kc, vc, tables, lens, starts(new))
+    assert err == 0
+    qs = starts(new)
+    for s, n in enumerate(new):
+        L = int(lens[s])
+        check_nonfinite(got[qs[s]:qs[s + 1]], q[qs[s]:qs[s + 1]], op.gather(kc, tables[s], L),
+                        op.gather(vc, tables[s], L), L - n)
+
+
+def test_all_values_nan_but_the_first_rows(ops):
+    """Every V row from token 37 on is NaN: rows 0 .. 36 are untouched by it."""
+    rng = np.random.default_rng(12)
+    n = 300
+    q = wl.host_normal_fp16(rng, (n, 4, D))
+    k, v = (wl.host_normal_fp16(rng, (n, 4, D)) for _ in "kv")
+    v[37:] = np.nan
+    got, err = run_packed(ops, q, k, v, [0, n])
+    assert err == 0
+    check_nonfinite(got, q, k, v, 0)
