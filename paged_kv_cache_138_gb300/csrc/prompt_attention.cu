@@ -1243,9 +1243,10 @@ int run(void* out, const void* q, const void* k, const void* v, const int32_t* b
   p.max_blocks = max_blocks;
   p.group_shift = shift;
   // a negative scale negates Q in the product, so that a row's maximum is the
-  // largest score either way; a scale of 0 keeps masked scores at -infinity
+  // largest score either way; a scale of 0 keeps masked scores at -infinity (and a
+  // NaN stays one: std::max returns its first argument then)
   p.idesc_qk = kIdescBase | (scale < 0.f ? kNegateA : 0u);
-  p.scale_log2 = std::max(1e-30f, (scale < 0.f ? -scale : scale) * 1.4426950408889634f);
+  p.scale_log2 = std::max((scale < 0.f ? -scale : scale) * 1.4426950408889634f, 1e-30f);
 
   CUtensorMap mq, mk, mv, mo;
   const int64_t rows = num_blocks * block_size;

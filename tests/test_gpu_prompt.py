@@ -449,3 +449,11 @@ def test_all_values_nan_but_the_first_rows(ops):
     got, err = run_packed(ops, q, k, v, [0, n])
     assert err == 0
     check_nonfinite(got, q, k, v, 0)
+
+
+def test_scale_that_is_nan(ops):
+    """A NaN for a scale gives NaN, not the result of some other scale."""
+    rng = np.random.default_rng(13)
+    q, k, v = (wl.host_normal_fp16(rng, (140, 2, D)) for _ in "qkv")
+    got, err = run_packed(ops, q, k, v, [0, 140], float("nan"))
+    assert err == 0 and np.isnan(got).all()
