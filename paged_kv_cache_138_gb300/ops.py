@@ -474,6 +474,18 @@ def _explain(*specs):
     raise ValueError("arguments do not fit together")
 
 
+def _new_workspace(nbytes, device, stream):
+    """A workspace for one launch on ``stream``, from that stream's memory: it is given
+    back when the call returns, for later work of the same stream."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else \
+            torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 @functools.lru_cache(maxsize=256)
 def prefill_workspace_bytes(num_tokens, num_seqs, num_q_heads, num_kv_heads, max_blocks_per_seq,
                             block_size=BLOCK_SIZE):
@@ -516,7 +528,7 @@ def paged_attention_prefill(out, q, k_cache, v_cache, block_tables, context_lens
     if workspace is None:
         need = prefill_workspace_bytes(T, S, Hq, Hkv, max_blocks, bs)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            workspace = _new_workspace(need, q.device, stream)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     args = (out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             block_tables.data_ptr(), context_lens.data_ptr(), query_start.data_ptr(), T, S, Hq,
@@ -665,7 +677,9 @@ def paged_attention_decode_q8(out, q, k_cache, v_cache, k_scale, v_scale, block_
     if rows != S or context_lens.shape != (S,):
         raise ValueError("block_tables / context_lens must have num_seqs rows")
     if workspace is None:
-        workspace = alloc_workspace(S, Hq, max_blocks, q.device, bs)
+        need = workspace_bytes(S, Hq, max_blocks, bs)
+        if need:
+            workspace = _new_workspace(need, q.device, stream)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     args = (out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             k_scale.data_ptr(), v_scale.data_ptr(), code, block_tables.data_ptr(),

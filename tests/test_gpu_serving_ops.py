@@ -132,3 +132,34 @@ def test_two_streams_at_once(ops):
         ops.paged_attention_decode_q8(douts[1], *dargs, SCALE, workspace=dws, stream=streams[1])
     torch.cuda.synchronize()
     assert torch.equal(outs[0], outs[1]) and torch.equal(douts[0], douts[1])
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_own_workspace_belongs_to_the_launch_stream(ops, raw):
+    """A workspace made by the call is of the stream it launches on: given back, it must not
+    go to work of the current stream while the launch still runs."""
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if raw else side
+    z = lambda *s, dtype=torch.float16: torch.zeros(s, dtype=dtype, device="cuda")
+    kc, tab = z(2048, 16, 2, 128), torch.arange(2048, dtype=torch.int32, device="cuda")[None]
+    lens = torch.full((1,), 32768, dtype=torch.int32, device="cuda")
+    q, qs = z(8, 8, 128), torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+    k8 = ops.q8_cache(2048, 2)
+    calls = [(ops.prefill_workspace_bytes(8, 1, 8, 2, 2048), lambda: ops.paged_attention_prefill(
+                  torch.empty_like(q), q, kc, kc, tab, lens, qs, 1.0, stream=stream, prepare=True)),
+             (ops.workspace_bytes(1, 8, 2048), lambda: ops.paged_attention_decode_q8(
+                  z(1, 8, 128), z(1, 8, 128), *k8, tab, lens, 1.0, stream=stream, prepare=True))]
+    for need, prepare in calls:
+        assert need > 0
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        launch = prepare()
+        used = [t.data_ptr() for t in launch._keep if isinstance(t, torch.Tensor) and
+                t.dtype is torch.uint8 and t.numel() == need]
+        assert len(used) == 1
+        del launch
+        mine = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(3)]
+        assert used[0] not in [t.data_ptr() for t in mine]
+        with torch.cuda.stream(torch.cuda.ExternalStream(side.cuda_stream)):
+            theirs = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(3)]
+        assert used[0] in [t.data_ptr() for t in theirs]
