@@ -470,7 +470,8 @@ _F16, _F32, _I32 = torch.float16, torch.float32, torch.int32
 def _explain(*specs):
     """Raise for the first (tensor, name, dtype, ndim) that is not as it should be."""
     for spec in specs:
-        _dev(*spec)
+        if _dev(*spec).get_device() != _get_device():
+            raise ValueError("%s must be on the current CUDA device" % spec[1])
     raise ValueError("arguments do not fit together")
 
 
@@ -502,17 +503,18 @@ def paged_attention_prefill(out, q, k_cache, v_cache, block_tables, context_lens
     context_lens[s] tokens, all of whose K/V are in the cache.
     prepare=True returns a PreparedLaunch instead of launching."""
     try:
-        good = (q.dtype is _F16 and q.is_cuda and q.is_contiguous() and
-                out.dtype is _F16 and out.is_cuda and out.is_contiguous() and
-                k_cache.dtype is _F16 and k_cache.is_cuda and k_cache.is_contiguous() and
-                v_cache.dtype is _F16 and v_cache.is_cuda and v_cache.is_contiguous() and
-                block_tables.dtype is _I32 and block_tables.is_cuda and
+        dev = _get_device()
+        good = (q.dtype is _F16 and q.get_device() == dev and q.is_contiguous() and
+                out.dtype is _F16 and out.get_device() == dev and out.is_contiguous() and
+                k_cache.dtype is _F16 and k_cache.get_device() == dev and k_cache.is_contiguous() and
+                v_cache.dtype is _F16 and v_cache.get_device() == dev and v_cache.is_contiguous() and
+                block_tables.dtype is _I32 and block_tables.get_device() == dev and
                 block_tables.is_contiguous() and
-                context_lens.dtype is _I32 and context_lens.is_cuda and
+                context_lens.dtype is _I32 and context_lens.get_device() == dev and
                 context_lens.is_contiguous() and
-                query_start.dtype is _I32 and query_start.is_cuda and query_start.is_contiguous()
+                query_start.dtype is _I32 and query_start.get_device() == dev and query_start.is_contiguous()
                 and q.dim() == 3 and k_cache.dim() == 4 and block_tables.dim() == 2)
-    except AttributeError:
+    except (AttributeError, RuntimeError):
         good = False
     if not good:
         _explain((q, "q", _F16, 3), (out, "out", _F16, 3), (k_cache, "k_cache", _F16, 4),
@@ -545,13 +547,14 @@ def prompt_attention(out, q, k, v, query_start, scale, dev_err=None, stream=None
     128], sequence s owning rows query_start[s] .. query_start[s + 1] - 1 of each.
     prepare=True returns a PreparedLaunch instead of launching."""
     try:
-        good = (q.dtype is _F16 and q.is_cuda and q.is_contiguous() and
-                out.dtype is _F16 and out.is_cuda and out.is_contiguous() and
-                k.dtype is _F16 and k.is_cuda and k.is_contiguous() and
-                v.dtype is _F16 and v.is_cuda and v.is_contiguous() and
-                query_start.dtype is _I32 and query_start.is_cuda and query_start.is_contiguous()
+        dev = _get_device()
+        good = (q.dtype is _F16 and q.get_device() == dev and q.is_contiguous() and
+                out.dtype is _F16 and out.get_device() == dev and out.is_contiguous() and
+                k.dtype is _F16 and k.get_device() == dev and k.is_contiguous() and
+                v.dtype is _F16 and v.get_device() == dev and v.is_contiguous() and
+                query_start.dtype is _I32 and query_start.get_device() == dev and query_start.is_contiguous()
                 and q.dim() == 3 and k.dim() == 3 and query_start.dim() == 1)
-    except AttributeError:
+    except (AttributeError, RuntimeError):
         good = False
     if not good:
         _explain((q, "q", _F16, 3), (out, "out", _F16, 3), (k, "k", _F16, 3), (v, "v", _F16, 3),
@@ -592,13 +595,14 @@ def q8_cache(num_blocks, num_kv_heads, block_size=BLOCK_SIZE, dtype=torch.int8, 
 def _q8_args(k_cache, v_cache, k_scale, v_scale):
     """The cache's code and sizes: code, num_blocks, block_size, Hkv, head_dim, stride."""
     try:
+        dev = _get_device()
         code = _CODES.get(k_cache.dtype)
-        good = (code is not None and k_cache.is_cuda and k_cache.is_contiguous() and
-                v_cache.dtype is k_cache.dtype and v_cache.is_cuda and v_cache.is_contiguous() and
-                k_scale.dtype is _F32 and k_scale.is_cuda and k_scale.is_contiguous() and
-                v_scale.dtype is _F32 and v_scale.is_cuda and v_scale.is_contiguous() and
+        good = (code is not None and k_cache.get_device() == dev and k_cache.is_contiguous() and
+                v_cache.dtype is k_cache.dtype and v_cache.get_device() == dev and v_cache.is_contiguous() and
+                k_scale.dtype is _F32 and k_scale.get_device() == dev and k_scale.is_contiguous() and
+                v_scale.dtype is _F32 and v_scale.get_device() == dev and v_scale.is_contiguous() and
                 k_cache.dim() == 4 and k_scale.dim() == 2)
-    except AttributeError:
+    except (AttributeError, RuntimeError):
         good = False
     if not good:
         dtype = getattr(k_cache, "dtype", None)
@@ -623,15 +627,16 @@ def reshape_and_cache_q8(k, v, query_start, block_tables, context_lens, k_cache,
     448 (e4m3); rows a block already holds are coded anew when its scale grows.
     prepare=True returns a PreparedLaunch instead of launching."""
     try:
-        good = (k.dtype is _F16 and k.is_cuda and k.is_contiguous() and
-                v.dtype is _F16 and v.is_cuda and v.is_contiguous() and
-                query_start.dtype is _I32 and query_start.is_cuda and
+        dev = _get_device()
+        good = (k.dtype is _F16 and k.get_device() == dev and k.is_contiguous() and
+                v.dtype is _F16 and v.get_device() == dev and v.is_contiguous() and
+                query_start.dtype is _I32 and query_start.get_device() == dev and
                 query_start.is_contiguous() and
-                block_tables.dtype is _I32 and block_tables.is_cuda and
+                block_tables.dtype is _I32 and block_tables.get_device() == dev and
                 block_tables.is_contiguous() and
-                context_lens.dtype is _I32 and context_lens.is_cuda and
+                context_lens.dtype is _I32 and context_lens.get_device() == dev and
                 context_lens.is_contiguous() and k.dim() == 3 and block_tables.dim() == 2)
-    except AttributeError:
+    except (AttributeError, RuntimeError):
         good = False
     if not good:
         _explain((k, "k", _F16, 3), (v, "v", _F16, 3), (query_start, "query_start", _I32, 1),
@@ -658,13 +663,14 @@ def paged_attention_decode_q8(out, q, k_cache, v_cache, k_scale, v_scale, block_
     """paged_attention_decode over an 8-bit cache (see q8_cache, reshape_and_cache_q8);
     same workspace.  prepare=True returns a PreparedLaunch instead of launching."""
     try:
-        good = (q.dtype is _F16 and q.is_cuda and q.is_contiguous() and
-                out.dtype is _F16 and out.is_cuda and out.is_contiguous() and
-                block_tables.dtype is _I32 and block_tables.is_cuda and
+        dev = _get_device()
+        good = (q.dtype is _F16 and q.get_device() == dev and q.is_contiguous() and
+                out.dtype is _F16 and out.get_device() == dev and out.is_contiguous() and
+                block_tables.dtype is _I32 and block_tables.get_device() == dev and
                 block_tables.is_contiguous() and
-                context_lens.dtype is _I32 and context_lens.is_cuda and
+                context_lens.dtype is _I32 and context_lens.get_device() == dev and
                 context_lens.is_contiguous() and q.dim() == 3 and block_tables.dim() == 2)
-    except AttributeError:
+    except (AttributeError, RuntimeError):
         good = False
     if not good:
         _explain((q, "q", _F16, 3), (out, "out", _F16, 3),

@@ -163,3 +163,23 @@ def test_own_workspace_belongs_to_the_launch_stream(ops, raw):
         with torch.cuda.stream(torch.cuda.ExternalStream(side.cuda_stream)):
             theirs = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(3)]
         assert used[0] in [t.data_ptr() for t in theirs]
+
+
+def test_tensors_of_another_device_are_refused(ops, monkeypatch):
+    """The kernels run on the current device; a tensor elsewhere is refused before a launch."""
+    z = lambda *s, dtype=torch.float16: torch.zeros(s, dtype=dtype, device="cuda")
+    q, kc = torch.full((2, 8, 128), 3.0, dtype=torch.float16, device="cuda"), z(4, 16, 2, 128)
+    tab, lens = z(1, 4, dtype=torch.int32), torch.full((1,), 2, dtype=torch.int32, device="cuda")
+    qs = torch.tensor([0, 2], dtype=torch.int32, device="cuda")
+    k, k8, out = z(2, 2, 128), ops.q8_cache(4, 2), z(2, 8, 128)
+    calls = [lambda: ops.prompt_attention(out, q, k, k, qs, 1.0),
+             lambda: ops.paged_attention_prefill(out, q, kc, kc, tab, lens, qs, 1.0),
+             lambda: ops.reshape_and_cache_q8(k, k, qs, tab, lens, *k8),
+             lambda: ops.paged_attention_decode_q8(out[:1], q[:1], *k8, tab, lens, 1.0)]
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    monkeypatch.setattr(ops, "_get_device", lambda: 1)
+    for call in calls:
+        with pytest.raises(ValueError, match="current CUDA device"):
+            call()
