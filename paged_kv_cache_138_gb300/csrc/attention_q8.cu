@@ -22,7 +22,11 @@
 //    up the result whatever the scales are, and l sums 2^(x - m) in fp32.
 //  * 32 tokens a stage (4 KB of K, 4 KB of V), 4 warps with a private 2-stage
 //    TMA ring each and 3 CTAs an SM: 192 KB in flight, as the fp16 kernel.
-//  * Splits, their fp32 partials and the merge are the fp16 kernel's.
+//  * Splits, their fp32 partials and the merge of few splits are the fp16 kernel's.
+//  * What bounds it: HBM.  64 x 4096 of 32 heads, int8 (2.15 GB): 317 us, 6.8 TB/s, the
+//    rate of a plain copy; the same copies without the arithmetic take 319.  256 x 4096 of
+//    32/8 heads, e4m3: 328-339 us (332 without the arithmetic).  Two contexts of 100k-131k tokens:
+//    92 us, 5.2 TB/s: 83-85 us of it here (3.6 rounds of CTAs), the rest the merge.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -415,10 +419,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 }
 
 // Log-sum-exp merge of a row of many splits: a CTA for the row, warp w takes
-// splits w, w + 8, ..., their sums join in warp order.  (One warp a row, as the fp16
-// launches have it, spent 48 us on the 118 splits of 64 rows.)
-constexpr int kWideSplits = 16;   // from here on
+// splits w, w + 8, ..., their sums join in warp order.  Against one warp a row, as the
+// fp16 launches have it (whole calls, int8, 32/8 heads unless said): 118 splits of 64
+// rows 92 us instead of 133, 16 splits (8 x 8000, e4m3) 32.3 and 36.1, 8 splits 33.9 and
+// 36.5 (16 x 4096), 16.3 and 18.3 (8 x 4096, 8/8); 4 splits 35.1 and 34.9 (32 x 2048),
+// 2 splits 38.0 and 35.1 (64 x 1024): a CTA for each of 2048 rows costs more than it reads.
+constexpr int kWideSplits = 8;   // from here on
 constexpr int kWideWarps = 8;
+constexpr int kNarrowRows = 8;   // rows (warps) of a CTA of paged_attention_merge_kernel
 __global__ void __launch_bounds__(kWideWarps * 32) q8_wide_merge_kernel(const Params p) {
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -602,12 +610,11 @@ extern "C" int pkv_paged_attention_decode_q8(void* out, const void* q, const voi
                      : launch_q8_bs<E4m3Half, true>(block_size, mk, mv, qp, splits, st);
   if (rc != PKV_OK) return rc;
   if (p.max_splits <= 1) return PKV_OK;
-  // one row a warp, eight a CTA, or a CTA for each row of many splits
   const int64_t rows = static_cast<int64_t>(num_seqs) * num_q_heads;
   const bool wide = p.max_splits >= kWideSplits;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(wide ? rows : (rows + kWideWarps - 1) / kWideWarps));
-  cfg.blockDim = dim3(kWideWarps * 32);
+  cfg.gridDim = dim3(static_cast<unsigned>(wide ? rows : (rows + kNarrowRows - 1) / kNarrowRows));
+  cfg.blockDim = dim3((wide ? kWideWarps : kNarrowRows) * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
