@@ -506,13 +506,16 @@ def paged_attention_prefill(out, q, k_cache, v_cache, block_tables, context_lens
         dev = _get_device()
         good = (q.dtype is _F16 and q.get_device() == dev and q.is_contiguous() and
                 out.dtype is _F16 and out.get_device() == dev and out.is_contiguous() and
-                k_cache.dtype is _F16 and k_cache.get_device() == dev and k_cache.is_contiguous() and
-                v_cache.dtype is _F16 and v_cache.get_device() == dev and v_cache.is_contiguous() and
+                k_cache.dtype is _F16 and k_cache.get_device() == dev and
+                k_cache.is_contiguous() and
+                v_cache.dtype is _F16 and v_cache.get_device() == dev and
+                v_cache.is_contiguous() and
                 block_tables.dtype is _I32 and block_tables.get_device() == dev and
                 block_tables.is_contiguous() and
                 context_lens.dtype is _I32 and context_lens.get_device() == dev and
                 context_lens.is_contiguous() and
-                query_start.dtype is _I32 and query_start.get_device() == dev and query_start.is_contiguous()
+                query_start.dtype is _I32 and query_start.get_device() == dev and
+                query_start.is_contiguous()
                 and q.dim() == 3 and k_cache.dim() == 4 and block_tables.dim() == 2)
     except (AttributeError, RuntimeError):
         good = False
@@ -552,7 +555,8 @@ def prompt_attention(out, q, k, v, query_start, scale, dev_err=None, stream=None
                 out.dtype is _F16 and out.get_device() == dev and out.is_contiguous() and
                 k.dtype is _F16 and k.get_device() == dev and k.is_contiguous() and
                 v.dtype is _F16 and v.get_device() == dev and v.is_contiguous() and
-                query_start.dtype is _I32 and query_start.get_device() == dev and query_start.is_contiguous()
+                query_start.dtype is _I32 and query_start.get_device() == dev and
+                query_start.is_contiguous()
                 and q.dim() == 3 and k.dim() == 3 and query_start.dim() == 1)
     except (AttributeError, RuntimeError):
         good = False
@@ -598,9 +602,12 @@ def _q8_args(k_cache, v_cache, k_scale, v_scale):
         dev = _get_device()
         code = _CODES.get(k_cache.dtype)
         good = (code is not None and k_cache.get_device() == dev and k_cache.is_contiguous() and
-                v_cache.dtype is k_cache.dtype and v_cache.get_device() == dev and v_cache.is_contiguous() and
-                k_scale.dtype is _F32 and k_scale.get_device() == dev and k_scale.is_contiguous() and
-                v_scale.dtype is _F32 and v_scale.get_device() == dev and v_scale.is_contiguous() and
+                v_cache.dtype is k_cache.dtype and v_cache.get_device() == dev and
+                v_cache.is_contiguous() and
+                k_scale.dtype is _F32 and k_scale.get_device() == dev and
+                k_scale.is_contiguous() and
+                v_scale.dtype is _F32 and v_scale.get_device() == dev and
+                v_scale.is_contiguous() and
                 k_cache.dim() == 4 and k_scale.dim() == 2)
     except (AttributeError, RuntimeError):
         good = False

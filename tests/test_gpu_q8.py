@@ -261,6 +261,17 @@ def test_decode_long_and_split(ops, code, bs):
     check_decode(got, q, codes, scales, tables, lens, bs)
 
 
+@pytest.mark.parametrize("longest", [1000, 3584, 3600, 4096, 8700, 40000])
+def test_decode_merges(ops, longest):
+    """2, 7, 8, 9, 17 and 79 splits beside sequences of fewer and of none: rows merged by
+    one warp and by a CTA."""
+    lens = [longest, 1, 513, 0, longest // 2, longest - 1]
+    q, codes, scales, tables, lens = decode_case(longest, lens, 8, 2, 16, "int8")
+    got, err = run_decode(ops, q, codes, scales, tables, lens, "int8", 16)
+    assert err == 0 and (got[3] == 0).all()
+    check_decode(got, q, codes, scales, tables, lens, 16)
+
+
 def test_decode_tiny_weights_on_large_scales(ops):
     """The tokens that carry the weight lie in blocks of tiny V scale; blocks of huge V
     scale have weights near 2^-60.  Zero scales among them."""
