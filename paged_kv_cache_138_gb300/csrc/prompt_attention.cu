@@ -21,9 +21,9 @@
 //    (paged) or for 128 tokens (packed).
 //  * What bounds it: in steady state a turn (128 tokens for 256 rows) takes 2300
 //    cycles, of which the tensor core is busy 2048; a unit adds some 4000 at its
-//    ends.  16,384 tokens of 32/8 heads: 1197-1267 us, 1.74-1.84 PFLOP/s (the
+//    ends.  16,384 tokens of 32/8 heads: 1192-1273 us, 1.73-1.84 PFLOP/s (the
 //    measured cuBLAS burst is 1.96; the chip runs at its power limit); 4 x 4096 of 32
-//    heads: 344 us, 1.60.
+//    heads: 351 us, 1.57.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
