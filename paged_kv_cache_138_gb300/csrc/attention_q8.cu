@@ -22,7 +22,7 @@
 //    up the result whatever the scales are, and l sums 2^(x - m) in fp32.
 //  * 32 tokens a stage (4 KB of K, 4 KB of V), 4 warps with a private 2-stage
 //    TMA ring each and 3 CTAs an SM: 192 KB in flight, as the fp16 kernel.
-//  * Splits, their fp32 partials and the merge of few splits are the fp16 kernel's.
+//  * Splits and their fp32 partials are the fp16 kernel's.
 //  * What bounds it: HBM.  64 x 4096 of 32 heads, int8 (2.15 GB): 317 us, 6.8 TB/s, the
 //    rate of a plain copy; the same copies without the arithmetic take 319.  256 x 4096 of
 //    32/8 heads, e4m3: 328-339 us (332 without the arithmetic).  Two contexts of 100k-131k tokens:
@@ -31,6 +31,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "attention_kernel.cuh"
 #include "q8_device.cuh"
@@ -38,11 +39,10 @@
 namespace pkv {
 namespace attn {
 
-// the fp16 launches' host helpers and merge kernel (paged_attention.cu)
+// the fp16 launches' host helpers (paged_attention.cu)
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 bool supported_block_size(int bs);
 int seq_stride_for(int num_seqs);
-__global__ void paged_attention_merge_kernel(const Params p);
 
 constexpr int kQ8Tile = 32;                      // tokens per stage
 constexpr int kQ8HalfBytes = kQ8Tile * kHeadDim; // K or V of a stage
@@ -213,6 +213,16 @@ __device__ __forceinline__ void q8_tile(const uint8_t* st, const uint32_t (&qb)[
   }
 }
 
+// fp16 output of dims d .. d + 3 of a row: 0 where every token was left out (a sum of 0),
+// NaN where the sum is NaN
+__device__ __forceinline__ void store_q8_out4(__half* o, float den, float4 num) {
+  const bool none = den == 0.f;
+  uint2 u;
+  u.x = pack_half2(none ? 0.f : num.x / den, none ? 0.f : num.y / den);
+  u.y = pack_half2(none ? 0.f : num.z / den, none ? 0.f : num.w / den);
+  *reinterpret_cast<uint2*>(o) = u;
+}
+
 // One CTA per (KV head, sequence, split); warp w streams tiles w, w + 4, ...
 template <class Half, int BS, bool CLEAR>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
@@ -327,9 +337,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
   }
 
-  // where the scores of the lane's two heads start
-  float s0[2] = {0.f, 0.f};
-  if (Half::kScoreBias != 0.f) {
+  // where the scores of the lane's two heads start (e4m3: 0, and NaN for a q that is not
+  // finite: its scores, were they all -inf, would else look like a head without tokens)
+  float s0[2];
+  {
     float sum = 0.f;   // of head lane / 4 over the lane's 32 dims, then over the four lanes
 #pragma unroll
     for (int k = 0; k < 8; ++k) sum += sum_half2(qb[k][0]) + sum_half2(qb[k][1]);
@@ -412,28 +423,29 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   merge_warps(ml, ob, G, [&](int gi, int d, float M, float den, float4 num) {
     const int64_t orow = static_cast<int64_t>(s) * p.num_q_heads + g * G + gi;
     if (nsplit == 1)
-      store_out4(p.out + orow * kHeadDim + d, den, num);
+      store_q8_out4(p.out + orow * kHeadDim + d, den, num);
     else
       store_partial(p, orow, split, d, M, den, num);
   });
 }
 
-// Log-sum-exp merge of a row of many splits: a CTA for the row, warp w takes
-// splits w, w + 8, ..., their sums join in warp order.  Against one warp a row, as the
-// fp16 launches have it (whole calls, int8, 32/8 heads unless said): 118 splits of 64
-// rows 92 us instead of 133, 16 splits (8 x 8000, e4m3) 32.3 and 36.1, 8 splits 33.9 and
-// 36.5 (16 x 4096), 16.3 and 18.3 (8 x 4096, 8/8); 4 splits 35.1 and 34.9 (32 x 2048),
-// 2 splits 38.0 and 35.1 (64 x 1024): a CTA for each of 2048 rows costs more than it reads.
-constexpr int kWideSplits = 8;   // from here on
-constexpr int kWideWarps = 8;
-constexpr int kNarrowRows = 8;   // rows (warps) of a CTA of paged_attention_merge_kernel
-__global__ void __launch_bounds__(kWideWarps * 32) q8_wide_merge_kernel(const Params p) {
+// Log-sum-exp merge of a row's splits by ROW_WARPS warps: warp w takes splits w,
+// w + ROW_WARPS, ..., their sums join in warp order.  A CTA (8 warps) a row against a warp
+// a row (whole calls, int8, 32/8 heads unless said): 118 splits of 64 rows 92 us instead
+// of 133, 16 splits (8 x 8000, e4m3) 32.3 and 36.1, 8 splits 33.9 and 36.5 (16 x 4096),
+// 16.3 and 18.3 (8 x 4096, 8/8); 4 splits 35.1 and 34.9 (32 x 2048), 2 splits 38.0 and 35.1
+// (64 x 1024): a CTA for each of 2048 rows costs more than it reads.
+constexpr int kWideSplits = 8;   // a CTA a row from here on
+constexpr int kMergeWarps = 8;
+template <int ROW_WARPS>
+__global__ void __launch_bounds__(kMergeWarps * 32) q8_merge_kernel(const Params p) {
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  __shared__ float4 part[kWideWarps][32];
-  __shared__ float dens[kWideWarps];
+  constexpr int kRows = kMergeWarps / ROW_WARPS;   // of a CTA
+  static_assert(ROW_WARPS == 1 || kRows == 1, "one row's sums meet in shared memory at most");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row = blockIdx.x;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + warp / ROW_WARPS;
+  if (row >= static_cast<int64_t>(p.num_seqs) * p.num_q_heads) return;
   const int s = static_cast<int>(row / p.num_q_heads);
   const int cap = p.max_blocks * p.block_size;
   const int L = max(0, min(__ldg(p.context_lens + s), cap));
@@ -447,8 +459,8 @@ __global__ void __launch_bounds__(kWideWarps * 32) q8_wide_merge_kernel(const Pa
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
   float den = 0.f;
-#pragma unroll 8
-  for (int i = warp; i < n; i += kWideWarps) {
+#pragma unroll (ROW_WARPS == 1 ? 4 : 8)
+  for (int i = warp % ROW_WARPS; i < n; i += ROW_WARPS) {
     const float2 w = ml[i];
     const float4 v = po[static_cast<int64_t>(i) * 32];
     const float c = exp2_approx(w.x - M);
@@ -458,20 +470,24 @@ __global__ void __launch_bounds__(kWideWarps * 32) q8_wide_merge_kernel(const Pa
     num.w += c * v.w;
     den += c * w.y;
   }
-  part[warp][lane] = num;
-  if (lane == 0) dens[warp] = den;
-  __syncthreads();
-  if (warp) return;
+  if (ROW_WARPS > 1) {
+    __shared__ float4 part[ROW_WARPS][32];
+    __shared__ float dens[ROW_WARPS];
+    part[warp][lane] = num;
+    if (lane == 0) dens[warp] = den;
+    __syncthreads();
+    if (warp) return;
 #pragma unroll
-  for (int w = 1; w < kWideWarps; ++w) {
-    const float4 v = part[w][lane];
-    num.x += v.x;
-    num.y += v.y;
-    num.z += v.z;
-    num.w += v.w;
-    den += dens[w];
+    for (int w = 1; w < ROW_WARPS; ++w) {
+      const float4 v = part[w][lane];
+      num.x += v.x;
+      num.y += v.y;
+      num.z += v.z;
+      num.w += v.w;
+      den += dens[w];
+    }
   }
-  store_out4(p.out + row * kHeadDim + 4 * lane, den, num);
+  store_q8_out4(p.out + row * kHeadDim + 4 * lane, den, num);
 }
 
 // The cache as [num_blocks * BS rows, Hkv, 128 bytes]; a box is min(BS, 32)
@@ -595,7 +611,9 @@ extern "C" int pkv_paged_attention_decode_q8(void* out, const void* q, const voi
     p.rank_by_length = num_seqs <= kMaxRankedSeqs && 2 * last_plane_tiles >= partition;
   }
   p.partition_tiles = partition;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  // an infinite scale makes every score infinite or NaN: NaN for all, as every score of
+  // -inf would look like a head without tokens
+  p.scale_log2 = std::isfinite(scale) ? scale * 1.4426950408889634f : NAN;
   qp.k_scale = k_scale;
   qp.v_scale = v_scale;
   qp.scale_stride = scale_stride;
@@ -613,15 +631,15 @@ extern "C" int pkv_paged_attention_decode_q8(void* out, const void* q, const voi
   const int64_t rows = static_cast<int64_t>(num_seqs) * num_q_heads;
   const bool wide = p.max_splits >= kWideSplits;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(wide ? rows : (rows + kNarrowRows - 1) / kNarrowRows));
-  cfg.blockDim = dim3((wide ? kWideWarps : kNarrowRows) * 32);
+  cfg.gridDim = dim3(static_cast<unsigned>(wide ? rows : (rows + kMergeWarps - 1) / kMergeWarps));
+  cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, wide ? q8_wide_merge_kernel : paged_attention_merge_kernel, p) ==
+  return cudaLaunchKernelEx(&cfg, wide ? q8_merge_kernel<kMergeWarps> : q8_merge_kernel<1>, p) ==
                  cudaSuccess
              ? PKV_OK
              : PKV_ERR_CUDA;
