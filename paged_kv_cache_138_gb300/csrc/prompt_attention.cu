@@ -970,7 +970,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = pos / kTile < p.split_tiles;
       const bool direct = mine && whole && u.split == 0;
       const bool part = mine && !whole && pos / kTile >= u.begin;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      // a row sees itself at least: its sum is 0 only if all its scores are -inf, and then the
+      // definition's NaN comes out (0 * inf)
+      const float inv = 1.f / l;
       const float mul = u.pair ? l2.x : 1.f;
       // 32 columns of the output, in units of 2^m
       const auto take = [&](int col, uint32_t* o) {
@@ -1098,7 +1100,7 @@ __global__ void __launch_bounds__(kMergeRows * 32)
     num.w += c * v.w;
     den += c * ml[2 * k + 1];
   }
-  const float inv = den > 0.f ? 1.f / den : 0.f;
+  const float inv = 1.f / den;   // 0 only if all scores are -inf: NaN, see above
   uint2 w;
   w.x = pack_half2(num.x * inv, num.y * inv);
   w.y = pack_half2(num.z * inv, num.w * inv);
