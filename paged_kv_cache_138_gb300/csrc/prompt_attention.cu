@@ -15,8 +15,11 @@
 //    the scores it came from) accumulate in fp32 in tensor memory: 2 x 128 columns
 //    of scores and 2 x 128 of outputs, all 512.
 //  * One softmax thread owns a row of scores.  Its running maximum moves only when
-//    a score passes it by more than 2^8, so O is rescaled in few tiles; the weights,
-//    at most 2^8, are rounded to fp16 for the product with V; their sum is fp32.
+//    a score passes it by more than 2^8, so O is rescaled in few tiles.  The weights
+//    are rounded to fp16 for the product with V, by half a step, 2^-11, or by 2^-32 of
+//    the largest (see kHeadroom).  Their sum is fp32 and takes them unrounded: the
+//    rounded ones would have to be widened again, 64 conversions more a thread and tile,
+//    and would spare only a row that one token dominates, which is now off by 2^-11.
 //  * K and V come through a ring of four 32 KB tiles, by TMA: a box for each block
 //    (paged) or for 128 tokens (packed).
 //  * What bounds it: in steady state a turn (128 tokens for 256 rows) takes 2300
@@ -52,6 +55,12 @@ static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "
 constexpr int kCopyWarp = 8, kMmaWarp = 9, kWorkWarp = 10, kCopyVWarp = 11;
 constexpr int kReaders = 11;                     // warps that read a unit's description
 constexpr float kRescale = 8.f;                  // log2 units
+// The weights' unit is 2^-7 of the running maximum, so that they fill fp16's range: at most
+// 2^(7 + kRescale), and what rounds to 0 is below 2^-32 of the maximum.  With the maximum
+// itself for a unit, 65,536 tokens 25 to 29 log2 units below one lost all their share of
+// the output, 2^-10, which their sum kept.
+constexpr float kHeadroom = 7.f;
+static_assert(kHeadroom + kRescale <= 15.f, "weights in fp16's range");
 constexpr float kNoMax = -1e30f;
 
 struct Smem {
@@ -859,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok = u.tok0[x] + (r >> p.group_shift);
       const int pos0 = u.ctx - u.n + u.tok0[x];             // of the tile's first row
       const int pos = min(u.ctx - u.n + tok, u.ctx - 1);
-      float m = kNoMax;
+      float m = kNoMax;   // log2 of the weights' unit
       float2 l2 = make_float2(0.f, 0.f);
       const int step = u.pair ? 2 : 1, top = u.pair ? u.last - 1 - x : u.end[x] - 1;
       for (int j = top; j >= u.begin; j -= step) {
@@ -897,9 +906,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], s[kTile - 4 + i]);
         const float bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
         // the maximum moves only when a score passes it by more than 2^8
-        const bool moves = bm > m + kRescale;
+        const bool moves = bm > m + (kHeadroom + kRescale);
         if (__any_sync(kFull, moves)) {
-          const float nm = moves ? bm : m;
+          const float nm = moves ? bm - kHeadroom : m;
           const float alpha = exp2_approx(m - nm);
           m = nm;
           l2 = fmul2(l2, make_float2(alpha, alpha));
