@@ -142,6 +142,18 @@ def alloc_workspace(num_seqs, num_q_heads, max_blocks_per_seq, device=None,
     return torch.empty(n, dtype=torch.uint8, device=device or torch.cuda.current_device())
 
 
+def _new_workspace(nbytes, device, stream):
+    """A workspace for one launch on ``stream``, from that stream's memory: it is given
+    back when the call returns, for later work of the same stream."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else \
+            torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def paged_attention_decode(out, q, k_cache, v_cache, block_tables, context_lens, scale,
                            workspace=None, dev_err=None, stream=None, prepare=False):
     """out[s,h] = softmax(scale * q[s,h] . K_s^T) V_s over context_lens[s] tokens.
@@ -161,7 +173,7 @@ def paged_attention_decode(out, q, k_cache, v_cache, block_tables, context_lens,
     max_blocks = block_tables.shape[1]
     need = workspace_bytes(S, Hq, max_blocks, bs, D)
     if need and workspace is None:
-        workspace = alloc_workspace(S, Hq, max_blocks, q.device, bs)
+        workspace = _new_workspace(need, q.device, stream)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     args = (_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
             _ptr(context_lens), S, Hq, Hkv, D, bs, nb, max_blocks, float(scale), _ptr(workspace),
@@ -196,7 +208,7 @@ def paged_attention_decode_fused(out, q, k_new, v_new, k_cache, v_cache, block_t
     max_blocks = block_tables.shape[1]
     need = workspace_bytes(S, Hq, max_blocks, bs, D)
     if need and workspace is None:
-        workspace = alloc_workspace(S, Hq, max_blocks, q.device, bs)
+        workspace = _new_workspace(need, q.device, stream)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     if cow is not None:
         cb, cs = _cow_args(cow, S)
@@ -393,7 +405,7 @@ def paged_attention_decode_grouped(out, q, k_cache, v_cache, block_tables, conte
     max_blocks = block_tables.shape[1]
     need = grouped_workspace_bytes(S, Hq, max_blocks, int(max_shared_tokens), bs, D)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _new_workspace(need, q.device, stream)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     args = (_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
             _ptr(context_lens), _ptr(group_first), _ptr(seq_group), _ptr(group_shared), G,
@@ -435,7 +447,7 @@ def paged_attention_decode_grouped_fused(out, q, k_new, v_new, k_cache, v_cache,
     max_blocks = block_tables.shape[1]
     need = grouped_workspace_bytes(S, Hq, max_blocks, int(max_shared_tokens), bs, D)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _new_workspace(need, q.device, stream)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     if cow is not None:
         cb, cs = _cow_args(cow, S)
@@ -473,18 +485,6 @@ def _explain(*specs):
         if _dev(*spec).get_device() != _get_device():
             raise ValueError("%s must be on the current CUDA device" % spec[1])
     raise ValueError("arguments do not fit together")
-
-
-def _new_workspace(nbytes, device, stream):
-    """A workspace for one launch on ``stream``, from that stream's memory: it is given
-    back when the call returns, for later work of the same stream."""
-    if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else \
-            torch.cuda.default_stream(device)
-    with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 @functools.lru_cache(maxsize=256)
