@@ -487,6 +487,27 @@ def _explain(*specs):
     raise ValueError("arguments do not fit together")
 
 
+def _check_side(workspace, dev_err):
+    """What the caller brings beside the data: a kernel writes it, so it is memory of the
+    current device, without gaps (a gap is another tensor's), and the error word is int32."""
+    dev = _get_device()
+    if dev_err is not None:
+        try:
+            good = (dev_err.dtype is _I32 and dev_err.get_device() == dev and
+                    dev_err.is_contiguous() and dev_err.numel() > 0)
+        except (AttributeError, RuntimeError):
+            good = False
+        if not good:
+            _explain((dev_err, "dev_err", _I32))
+    if workspace is not None:
+        try:
+            good = workspace.get_device() == dev and workspace.is_contiguous()
+        except (AttributeError, RuntimeError):
+            good = False
+        if not good:
+            _explain((workspace, "workspace", getattr(workspace, "dtype", None)))
+
+
 @functools.lru_cache(maxsize=256)
 def prefill_workspace_bytes(num_tokens, num_seqs, num_q_heads, num_kv_heads, max_blocks_per_seq,
                             block_size=BLOCK_SIZE):
@@ -530,6 +551,8 @@ def paged_attention_prefill(out, q, k_cache, v_cache, block_tables, context_lens
         raise ValueError("shape mismatch")
     if query_start.shape != (S + 1,) or context_lens.shape != (S,):
         raise ValueError("query_start must have num_seqs + 1 entries, context_lens num_seqs")
+    if workspace is not None or dev_err is not None:
+        _check_side(workspace, dev_err)
     if workspace is None:
         need = prefill_workspace_bytes(T, S, Hq, Hkv, max_blocks, bs)
         if need:
@@ -570,6 +593,8 @@ def prompt_attention(out, q, k, v, query_start, scale, dev_err=None, stream=None
     S = query_start.shape[0] - 1
     if S < 0:
         raise ValueError("query_start must have num_seqs + 1 entries")
+    if dev_err is not None:
+        _check_side(None, dev_err)
     args = (out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), query_start.data_ptr(), T, S,
             Hq, Hkv, D, float(scale), _ptr(dev_err), _stream_handle(stream))
     keep = (out, q, k, v, query_start, dev_err, stream) if prepare else None
@@ -655,6 +680,8 @@ def reshape_and_cache_q8(k, v, query_start, block_tables, context_lens, k_cache,
         raise ValueError("shape mismatch")
     if query_start.shape != (S + 1,) or context_lens.shape != (S,):
         raise ValueError("query_start must have num_seqs + 1 entries, context_lens num_seqs")
+    if dev_err is not None:
+        _check_side(None, dev_err)
     args = (k.data_ptr(), v.data_ptr(), query_start.data_ptr(), block_tables.data_ptr(),
             context_lens.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
             v_scale.data_ptr(), code, T, S, Hkv, D, bs, nb, max_blocks, stride, _ptr(dev_err),
@@ -689,6 +716,8 @@ def paged_attention_decode_q8(out, q, k_cache, v_cache, k_scale, v_scale, block_
     rows, max_blocks = block_tables.shape
     if rows != S or context_lens.shape != (S,):
         raise ValueError("block_tables / context_lens must have num_seqs rows")
+    if workspace is not None or dev_err is not None:
+        _check_side(workspace, dev_err)
     if workspace is None:
         need = workspace_bytes(S, Hq, max_blocks, bs)
         if need:
