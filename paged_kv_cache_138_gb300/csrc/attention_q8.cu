@@ -360,47 +360,53 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
   for (int i = 0; i < 8; ++i) a.o[i][0] = a.o[i][1] = a.o[i][2] = a.o[i][3] = 0.f;
 
+  const auto landed = [&](int k) {
+    return warp_wait(&bars[k % kStages], (k / kStages) & 1, p.dev_err);
+  };
   bool ok = true;
-  for (int k = 0; k < issued; ++k) {
-    if (ok) ok = warp_wait(&bars[k % kStages], (k / kStages) & 1, p.dev_err);
-    if (ok) {
-      const uint8_t* st = ring + (k % kStages) * kStageBytes;
-      float ks[kBoxes], lv[kBoxes];
+  int k = 0;
+  for (; k < issued; ++k) {
+    ok = landed(k);
+    if (!ok) break;
+    const uint8_t* st = ring + (k % kStages) * kStageBytes;
+    float ks[kBoxes], lv[kBoxes];
 #pragma unroll
-      for (int b = 0; b < kBoxes; ++b) {
-        const int box = k * kBoxes + b;
-        float vk = ksv[0], vl = lvv[0];
+    for (int b = 0; b < kBoxes; ++b) {
+      const int box = k * kBoxes + b;
+      float vk = ksv[0], vl = lvv[0];
 #pragma unroll
-        for (int i = 1; i < kSlots; ++i) {
-          vk = (box >> 5) == i ? ksv[i] : vk;
-          vl = (box >> 5) == i ? lvv[i] : vl;
-        }
-        ks[b] = __shfl_sync(kFull, vk, box & 31);
-        lv[b] = __shfl_sync(kFull, vl, box & 31);
+      for (int i = 1; i < kSlots; ++i) {
+        vk = (box >> 5) == i ? ksv[i] : vk;
+        vl = (box >> 5) == i ? lvv[i] : vl;
       }
-      const int valid = L - first - (k * kWarps + warp) * kQ8Tile;
-      if (CLEAR && valid < kQ8Tile) {
-        // rows past the context may hold any byte, and e4m3 has NaN codes: 0 * NaN
-        // would poison the sums
-        for (int i = lane; i < (kQ8Tile - valid) * 8; i += 32)
-          st_shared_zero16(smem_u32(st) + kQ8HalfBytes + valid * kHeadDim + i * 16);
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-      q8_tile<Half, kBoxes>(st, qb, s0, ks, lv, valid, lane, a);
+      ks[b] = __shfl_sync(kFull, vk, box & 31);
+      lv[b] = __shfl_sync(kFull, vl, box & 31);
     }
+    const int valid = L - first - (k * kWarps + warp) * kQ8Tile;
+    if (CLEAR && valid < kQ8Tile) {
+      // rows past the context may hold any byte, and e4m3 has NaN codes: 0 * NaN
+      // would poison the sums
+      for (int i = lane; i < (kQ8Tile - valid) * 8; i += 32)
+        st_shared_zero16(smem_u32(st) + kQ8HalfBytes + valid * kHeadDim + i * 16);
+      fence_proxy_async_smem();
+      __syncwarp();
+    }
+    q8_tile<Half, kBoxes>(st, qb, s0, ks, lv, valid, lane, a);
     __syncwarp();
-    if (ok && issued < mine) {
+    if (issued < mine) {
       issue(issued);
       ++issued;
     }
   }
+  // after a wait that gave up its copies and those behind them are still on their way into the
+  // ring: they get a bounded wait each before the shared memory goes to another CTA
+  for (; !ok && k < issued; ++k) landed(k);
 #pragma unroll
   for (int n = 0; n < 2; ++n)
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) a.l[n] += __shfl_xor_sync(kFull, a.l[n], o);
 
-  // after a wait that gave up boxes may still be in flight into the ring: no merge, no store
+  // after a wait that gave up: no merge (it reuses the rings), no store
   if (__syncthreads_or(!ok)) return;
   float* ml = reinterpret_cast<float*>(smem + Smem::ml);
   float* ob = reinterpret_cast<float*>(smem + Smem::stages);
