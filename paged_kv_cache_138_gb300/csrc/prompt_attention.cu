@@ -497,6 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int kBoxes = BS ? kTile / (BS ? BS : 1) : 1;
       static_assert((kStages & (kStages - 1)) == 0, "ring positions by shifts");
       int base = 0, nraw = 0;                 // the unit's first place in the ring, cleaned tiles
+      int raw_st = -1;                        // the stage of a tile that is to be cleaned
       uint32_t q_seen = 0, q_parity = 0;      // bit x: Q copies of tile x so far
       uint32_t kv_seen = 0, kv_parity = 0;    // bit st: this warp's copies into a stage
       bool ok = true;
@@ -539,6 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool raw = mine && masked.any();
           uint64_t* b = raw ? bar(Smem::raw, 0) : bar(Smem::kv_full, st);
           uint8_t* dst = smem + Smem::kv + st * kTileBytes;
+          if (raw) raw_st = st;
           if (lane == 0) mbar_arrive_expect_tx(b, kTileBytes);
           __syncwarp();
           if (lane < kBoxes) {
@@ -552,6 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (raw) {   // the tile may be used once its masked tokens are finite
             ok = wait(b, nraw & 1);
+            if (!ok) break;
             ++nraw;
             const uint32_t to = smem_u32(dst);
             const auto chunk = [&](int c) {   // 16 bytes: token c / 16, dims 8 (c % 16)
@@ -583,7 +586,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               st_shared_zero16(chunk(c));
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0 && ok) mbar_arrive(bar(Smem::kv_full, st));
+            if (lane == 0) mbar_arrive(bar(Smem::kv_full, st));
+            raw_st = -1;
           }
           if (i == 0 && !mine) {
 #pragma unroll 1
@@ -607,10 +611,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         base += 2 * n;
       }
-      if (!ok) {   // a wait gave up: let this warp's copies land before the CTA goes
+      if (*gave_up) {   // let this warp's copies land before the CTA goes (that of a tile to be
+                        // cleaned counts on a barrier of its own)
+        if (raw_st >= 0) wait(bar(Smem::raw, 0), nraw & 1);
 #pragma unroll 1
         for (int i = 0; i < kStages; ++i)
-          if (kv_seen >> i & 1) wait(bar(Smem::kv_full, i), kv_parity >> i & 1);
+          if ((kv_seen >> i & 1) && i != raw_st) wait(bar(Smem::kv_full, i), kv_parity >> i & 1);
 #pragma unroll 1
         for (int x = 0; x < 2; ++x)
           if (q_seen >> x & 1) wait(bar(Smem::q_full, x), (q_parity >> x & 1) ^ 1);
@@ -832,6 +838,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         ok = wait(bar(Smem::stolen, 0), tries & 1);
+        if (!ok) {   // the answer may still come: another wait before the CTA goes
+          wait(bar(Smem::stolen, 0), tries & 1);
+          break;
+        }
         uint32_t got, ax, ay;
         asm volatile(
             "{\n .reg .pred p;\n .reg .b128 h;\n .reg .b32 z, w;\n ld.shared.b128 h, [%3];\n"
