@@ -62,6 +62,8 @@ constexpr float kRescale = 8.f;                  // log2 units
 constexpr float kHeadroom = 7.f;
 static_assert(kHeadroom + kRescale <= 15.f, "weights in fp16's range");
 constexpr float kNoMax = -1e30f;
+constexpr uint32_t kWaitLimit = 1u << 31;        // cycles a wait may take, a second: some wait
+                                                 // for a whole unit (see kMaxContext)
 
 struct Smem {
   static constexpr int q = 0;                            // two query tiles
@@ -222,24 +224,6 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
       : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   return done != 0;
-}
-
-// warp_wait with short code: a wait that gives up only raises a flag in shared memory,
-// which the CTA reports at its end.  There are some 45 waits, and code counts: what is
-// not in the instruction cache costs some 100 cycles for 8 instructions, and a unit's
-// first and last steps run code that the steps between have pushed out (the kernel
-// shrunk from 77 to 56 KB ran 5 % faster on prompts of 2048 tokens).
-__device__ __forceinline__ bool flag_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* gave_up) {
-  constexpr unsigned kAll = 0xffffffffu;
-  if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
-  const uint32_t t0 = clock();
-  while (!__all_sync(kAll, mbar_try_wait(bar, parity))) {
-    if (__any_sync(kAll, static_cast<uint32_t>(clock()) - t0 > 1u << 30)) {
-      *gave_up = 1;
-      return false;
-    }
-  }
-  return true;
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -436,7 +420,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const auto bar = [&](int at, int i) { return reinterpret_cast<uint64_t*>(smem + at) + i; };
   volatile uint32_t* gave_up = reinterpret_cast<volatile uint32_t*>(smem + Smem::gave_up);
   volatile int* nonfinite = reinterpret_cast<volatile int*>(smem + Smem::nonfinite);
-  const auto wait = [&](uint64_t* b, uint32_t parity) { return flag_wait(b, parity, gave_up); };
+  const auto wait = [&](uint64_t* b, uint32_t parity) {
+    return flag_wait(b, parity, gave_up, kWaitLimit);
+  };
   if (warp == kCopyWarp && lane == 0) {
     prefetch_tmap(&tmap_q);
     prefetch_tmap(&tmap_k);
@@ -1207,9 +1193,10 @@ int group_shift_of(int num_q_heads, int num_kv_heads) {
 // for each SM, of at least 8 KV tiles.
 constexpr int kSms = 152;
 constexpr int kMinSplitTiles = 8;
-// The longest context: a warp that waits for a whole unit of it (2400 cycles for 128
-// tokens) stays within half the waits' limit.
+// The longest context: a warp that waits for a whole unit of it stays within half the waits'
+// limit.  128 tokens take 2300 cycles, 3100 in the slowest unit (one tile alone, see Unit).
 constexpr int64_t kMaxContext = 1 << 25;
+static_assert(kMaxContext / kTile * 3100 <= kWaitLimit / 2, "a unit of the longest context");
 int64_t units_for(int num_tokens, int num_seqs, int group_shift) {
   return num_tokens / (2 * kTile >> group_shift) + static_cast<int64_t>(num_seqs);
 }

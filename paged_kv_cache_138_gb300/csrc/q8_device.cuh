@@ -63,21 +63,40 @@ __device__ __forceinline__ int find_unit_seq(const int32_t* query_start, int num
 }
 
 // ---- waits ------------------------------------------------------------------------
-// A bounded wait of a whole warp on an mbarrier: one vote decides, so that no lane
-// branches by itself, and the limit is counted in clock cycles (2^30, half a second),
-// which are quick to read.  A barrier that is through already costs 30 cycles so, 90
-// with each lane branching and a look at the global timer.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* dev_err) {
+// Bounded waits of a whole warp on an mbarrier: one vote decides, so that no lane
+// branches by itself, and the limit is counted in clock cycles, which are quick to
+// read.  A barrier that is through already costs 30 cycles so, 90 with each lane
+// branching and a look at the global timer.
+constexpr uint32_t kCopyWaitLimit = 1u << 30;   // half a second
+
+// true: through; false: more than limit cycles have passed
+__device__ __forceinline__ bool vote_wait(uint64_t* bar, uint32_t parity, uint32_t limit) {
   constexpr unsigned kAll = 0xffffffffu;
   if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
   const uint32_t t0 = clock();
-  while (!__all_sync(kAll, mbar_try_wait(bar, parity))) {
-    if (__any_sync(kAll, static_cast<uint32_t>(clock()) - t0 > 1u << 30)) {
-      report(dev_err, PKV_DEV_WAIT_TIMEOUT);
-      return false;
-    }
-  }
+  while (!__all_sync(kAll, mbar_try_wait(bar, parity)))
+    if (__any_sync(kAll, static_cast<uint32_t>(clock()) - t0 > limit)) return false;
   return true;
+}
+
+// a wait that gives up is reported
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* dev_err,
+                                          uint32_t limit = kCopyWaitLimit) {
+  const bool through = vote_wait(bar, parity, limit);
+  if (!through) report(dev_err, PKV_DEV_WAIT_TIMEOUT);
+  return through;
+}
+
+// With short code: a wait that gives up only raises a flag in shared memory, which the
+// CTA reports at its end.  The prompt kernel has some 45 waits, and code counts: what is
+// not in the instruction cache costs some 100 cycles for 8 instructions, and a unit's
+// first and last steps run code that the steps between have pushed out (the kernel
+// shrunk from 77 to 56 KB ran 5 % faster on prompts of 2048 tokens).
+__device__ __forceinline__ bool flag_wait(uint64_t* bar, uint32_t parity,
+                                          volatile uint32_t* gave_up, uint32_t limit) {
+  const bool through = vote_wait(bar, parity, limit);
+  if (!through) *gave_up = 1;
+  return through;
 }
 
 // ---- codes ------------------------------------------------------------------------
