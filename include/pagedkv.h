@@ -533,6 +533,15 @@ int pkv_swap_blocks(const void* const* src_pools, void* const* dst_pools, int nu
 int pkv_selftest_bounded_wait(int32_t* dev_err, int32_t* landed, int limit_ms, void* stream);
 
 /*
+ * The same of the prompt and 8-bit kernels' waits, which a whole warp decides by one
+ * vote and which count clock cycles (limit_cycles 1 .. 2^31).  results (device int32 [5]):
+ * {1, 1, 0, 0, 1}: both kinds of wait pass a barrier that is through, both give up on one
+ * that nothing arrives on, the second kind having raised its flag; *dev_err becomes
+ * PKV_DEV_WAIT_TIMEOUT.
+ */
+int pkv_selftest_warp_waits(int32_t* dev_err, int32_t* results, int64_t limit_cycles, void* stream);
+
+/*
  * Synthetic inputs (benchmarks, the model-less serving driver; not part of the
  * paged-attention method).  Writes n standard-normal fp16 values to dst (device,
  * 16-byte aligned): element i is element offset + i of a stream keyed by seed,

@@ -5,7 +5,7 @@
 // recording it in dev_err.
 #include <algorithm>
 
-#include "pkv_device.cuh"
+#include "q8_device.cuh"
 
 namespace pkv {
 namespace cache {
@@ -279,5 +279,49 @@ extern "C" int pkv_selftest_bounded_wait(int32_t* dev_err, int32_t* landed, int 
   if (!dev_err || !landed || limit_ms <= 0 || limit_ms > 2000) return PKV_ERR_INVALID_ARG;
   pkv::cache::bounded_wait_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(
       dev_err, static_cast<uint64_t>(limit_ms) * 1000000ull, landed);
+  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+namespace pkv {
+namespace cache {
+
+// One warp and its two kinds of wait, each on a barrier that is through and on one that nothing
+// arrives on: the second must give up after limit cycles.
+__global__ void warp_waits_selftest_kernel(int32_t* dev_err, uint32_t limit, int32_t* results) {
+  __shared__ uint64_t bar[2];
+  __shared__ uint32_t flag;
+  if (threadIdx.x == 0) {
+    mbar_init(&bar[0], 1);
+    mbar_init(&bar[1], 1);
+    fence_barrier_init();
+    flag = 0;
+    mbar_arrive(&bar[0]);
+  }
+  __syncwarp();
+  const bool r0 = warp_wait(&bar[0], 0, dev_err, limit);
+  const bool r1 = flag_wait(&bar[0], 0, &flag, limit);
+  __syncwarp();
+  const bool raised = *static_cast<volatile uint32_t*>(&flag) != 0;
+  const bool r2 = flag_wait(&bar[1], 0, &flag, limit);
+  const bool r3 = warp_wait(&bar[1], 0, dev_err, limit);
+  __syncwarp();
+  if (threadIdx.x == 0) {
+    results[0] = r0;
+    results[1] = r1 && !raised;
+    results[2] = r2;
+    results[3] = r3;
+    results[4] = *static_cast<volatile uint32_t*>(&flag);
+  }
+}
+
+}  // namespace cache
+}  // namespace pkv
+
+extern "C" int pkv_selftest_warp_waits(int32_t* dev_err, int32_t* results, int64_t limit_cycles,
+                                       void* stream) {
+  if (!dev_err || !results || limit_cycles <= 0 || limit_cycles > int64_t(1) << 31)
+    return PKV_ERR_INVALID_ARG;
+  pkv::cache::warp_waits_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(
+      dev_err, static_cast<uint32_t>(limit_cycles), results);
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
