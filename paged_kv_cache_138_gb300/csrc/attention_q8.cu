@@ -17,9 +17,11 @@
 //  * Codes become fp16 exactly: int8 by placing the byte under the exponent of
 //    1024 and subtracting, e4m3 by its conversion.  The scales never touch the
 //    values: a block's K scale multiplies its scores, its V scale enters the
-//    weight's exponent, w = 2^(x + log2 v_scale - m2), under a running maximum
-//    m2 of its own.  So w keeps fp16's full precision for the tokens that make
-//    up the result whatever the scales are, and l sums 2^(x - m) in fp32.
+//    weight's exponent, w = 2^(x + log2 v_scale - m2), under a unit 2^m2 from a
+//    running maximum of its own.  So w keeps fp16's full precision for the tokens
+//    that make up the result whatever the scales are: it is off by half a step, 2^-11,
+//    or by 2^-32 of the largest.  l sums 2^(x - m) in fp32, without the V scales,
+//    so not the rounded weights: a row that one token dominates is off by 2^-11.
 //  * 32 tokens a stage (4 KB of K, 4 KB of V), 4 warps with a private 2-stage
 //    TMA ring each and 3 CTAs an SM: 192 KB in flight, as the fp16 kernel.
 //  * Splits and their fp32 partials are the fp16 kernel's.
@@ -67,8 +69,10 @@ struct Int8Half {
   static __device__ __forceinline__ uint32_t lo(uint32_t w) { return pair(w, 0x4140); }
   static __device__ __forceinline__ uint32_t hi(uint32_t w) { return pair(w, 0x4342); }
   // K keeps the bias: a byte alone in a half is the subnormal u 2^-24, and the scores start at
-  // -128 2^-24 sum q instead of 0.  Bias and codes are of one size, so the sum loses
-  // nothing by it (under V, where tokens average out, it would).
+  // -128 2^-24 sum q instead of 0.  The sums are then of the size of 255 sum |q| at most,
+  // whatever the codes are, and 8 steps round them by 2^-23 each: 2^-12 of a code for each
+  // product, where the code itself is off by up to a half.  So nothing is lost even in a
+  // block whose scale an outlier sets (under V, where tokens average out, it would count).
   static constexpr float kScoreUnit = 16777216.f, kScoreBias = -128.f / 16777216.f;
   static __device__ __forceinline__ uint32_t k_lo(uint32_t w) { return __byte_perm(w, 0u, 0x4140); }
   static __device__ __forceinline__ uint32_t k_hi(uint32_t w) { return __byte_perm(w, 0u, 0x4342); }
@@ -100,6 +104,11 @@ struct Q8State {
   float o[8][4];
 };
 
+// The unit of the fp16 weights and of O is 2^-7 of the running maximum, so that the weights
+// fill fp16's range: at most 2^(7 + kRescaleThreshold), and what rounds to 0 is below 2^-32
+// of the maximum (2^-25 with the maximum itself for a unit).
+constexpr float kHeadroom = 7.f;
+static_assert(kHeadroom + kRescaleThreshold <= 15.f, "weights in fp16's range");
 constexpr float kNoMax = -1e30f;    // below every exponent, and finite: x - m is never inf - inf
 constexpr int kLeftOut = 0x7fc0dead;  // in place of a K scale: the block has no valid id (a NaN
                                       // that no arithmetic makes)
@@ -151,7 +160,8 @@ __device__ __forceinline__ void q8_tile(const uint8_t* st, const uint32_t (&qb)[
                    fmaxf(x[1][n] + lv4[1][0], x[1][2 + n] + lv4[1][1]));
   }
   const bool moves = bm[0] > a.m[0] + kRescaleThreshold || bm[1] > a.m[1] + kRescaleThreshold ||
-                     bm2[0] > a.m2[0] + kRescaleThreshold || bm2[1] > a.m2[1] + kRescaleThreshold;
+                     bm2[0] > a.m2[0] + (kHeadroom + kRescaleThreshold) ||
+                     bm2[1] > a.m2[1] + (kHeadroom + kRescaleThreshold);
   if (__any_sync(kFull, moves)) {
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
@@ -164,14 +174,15 @@ __device__ __forceinline__ void q8_tile(const uint8_t* st, const uint32_t (&qb)[
         a.l[n] *= exp2_approx(a.m[n] - bm[n]);
         a.m[n] = bm[n];
       }
-      if (bm2[n] > a.m2[n] + kRescaleThreshold) {
-        const float alpha = exp2_approx(a.m2[n] - bm2[n]);
+      if (bm2[n] > a.m2[n] + (kHeadroom + kRescaleThreshold)) {
+        const float unit = bm2[n] - kHeadroom;
+        const float alpha = exp2_approx(a.m2[n] - unit);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           a.o[i][n] *= alpha;
           a.o[i][2 + n] *= alpha;
         }
-        a.m2[n] = bm2[n];
+        a.m2[n] = unit;
       }
     }
   }

@@ -2,8 +2,8 @@
 
 Derived, elementwise (u: half a step of the type's rounding):
 * A weight, V scale included, is rounded to fp16 for the product with V: 2^-11 of itself, or, below
-  fp16's normal range, 2^-25 of the unit.  The unit is at most the largest weight so far of the warp's own
-  tokens (32 of every 128 of a split): groups of tokens are off by 2^-25 n_g max_g (weight) |code|.
+  fp16's normal range, 2^-25 of the unit.  The unit is at most 2^-7 of the largest weight so far of the warp's
+  own tokens (32 of every 128 of a split): groups of tokens are off by 2^-32 n_g max_g (weight) |code|.
 * A score is 8 products of 16 dims accumulated in fp32, 2^-23 each of what has been added up: for int8 the
   codes carry a bias of 128, |code + 128| <= 255, which the start of the sum takes out: -128 sum q, itself off
   by 2^-24 for each of its 18 additions.  So off by (8 * 255 * 2 + 18 * 128) 2^-24 sum |q| k_scale scale for
@@ -31,7 +31,7 @@ def ops(native_lib):
     return o
 
 
-def check(got, q, codes, scales, tables, lens, bs, split, code, scale=tq.SCALE):
+def check(got, q, codes, scales, tables, lens, bs, split, code, scale=tq.SCALE, unit=2.0 ** -7):
     S, Hq, _ = q.shape
     Hkv = codes[0].shape[2]
     assert np.isfinite(got).all()
@@ -61,7 +61,7 @@ def check(got, q, codes, scales, tables, lens, bs, split, code, scale=tq.SCALE):
             n = np.bincount(group)
             top = np.zeros(len(n))
             np.maximum.at(top, group, w)
-            lost = 2.0 ** -25 * (n * top).sum() * np.abs(V).max()
+            lost = 2.0 ** -25 * unit * (n * top).sum() * np.abs(V).max()
             tol = 2.0 ** -11 * np.abs(ref) + 2.0 ** -25 + lost + \
                 1.01 * ((w * moved) @ np.abs(V) + (mean + sums + 2.0 ** -11) * spread)
             over = np.abs(got[s, h] - ref) - tol
@@ -110,3 +110,28 @@ def test_small_codes_beside_an_outlier(ops, code, sign):
     got, err = tq.run_decode(ops, q, codes, scales, tables, lens, code, 16)
     assert err == 0
     check(got, q, codes, scales, tables, lens, 16, ops.split_tokens(2, Hkv, tables.shape[1]), code)
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (8, 1)])
+def test_many_small_weights_beside_dominant_ones(ops, code, Hq, Hkv):
+    """2,000 tokens, one for each warp 25 to 29 log2 units above the others, its V 0 in half of the
+    dims: there the others make up the whole output."""
+    rng = np.random.default_rng(8)
+    q, codes, scales, tables, lens = tq.decode_case(9, [2000], Hq, Hkv, 16, code)
+    q[:] = 0
+    q[..., 0] = 1
+    top = tq.oq.QMAX[code]
+    codes[0][:] = 0
+    codes[0][..., 0] = tq.oq.nearest_code(-rng.uniform(0.87, 1, codes[0].shape[:3]) * top, code)
+    codes[1][:] = tq.oq.nearest_code(rng.uniform(0.5, 1, codes[1].shape) * top, code)
+    for warp in range(4):
+        b, r = tables[0, 2 * warp], 5
+        codes[0][b, r, :, 0] = 0
+        codes[1][b, r, :, ::2] = 0
+    scales[0][:] = 29 / top
+    scales[1][:] = 4000 / top
+    got, err = tq.run_decode(ops, q, codes, scales, tables, lens, code, 16, scale=np.log(2))
+    assert err == 0
+    check(got, q, codes, scales, tables, lens, 16, ops.split_tokens(1, Hkv, tables.shape[1]), code,
+          scale=np.log(2))
