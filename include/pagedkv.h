@@ -399,10 +399,12 @@ int pkv_copy_blocks(void* const* k_caches, void* const* v_caches, int num_layers
  * Reported, and left out: a sequence whose query_start entries are out of order
  * or past num_tokens (PKV_DEV_BAD_QUERY_RANGE; sequences beside it may be left out
  * too) or whose context is shorter than its rows or longer than its table
- * (PKV_DEV_BAD_CONTEXT_LEN); its rows of out stay as they were.  A block whose id is out of range (PKV_DEV_BAD_BLOCK_ID)
- * counts as zeros.
+ * (PKV_DEV_BAD_CONTEXT_LEN); its rows of out stay as they were.  A block whose id
+ * is out of range (PKV_DEV_BAD_BLOCK_ID) counts as zeros.
  * fp32 scores, maxima, sums and accumulators; the softmax weights are rounded
- * to fp16 for the product with V, the result once.
+ * to fp16 for the product with V (by half a step, or by 2^-32 of the largest), the
+ * result once.  A row with a score that is NaN or +infinity, or with none above
+ * -infinity, is NaN.
  */
 int pkv_paged_attention_prefill(void* out, const void* q, const void* k_cache,
                                 const void* v_cache, const int32_t* block_tables,
@@ -486,8 +488,11 @@ int pkv_reshape_and_cache_q8(const void* k, const void* v, const int32_t* query_
  * A token in a block whose id is out of range is left out.
  * fp32 accumulation; the softmax weights, with the V scale folded in and taken
  * relative to their running maximum, are rounded to fp16 once for the product
- * with V, the result once.  Scales must be finite and not negative (a zero
- * scale is a block of zeros); codes past the context may be any bytes.
+ * with V (by half a step, or by 2^-32 of the largest), the result once.  The
+ * blocks' scales must be finite and not negative (a zero scale is a block of
+ * zeros); codes past the context may be any bytes.  An infinity or NaN in a head's
+ * q makes that head's output NaN, a softmax scale that is not finite every output
+ * (contexts of no tokens give zeros).
  */
 int pkv_paged_attention_decode_q8(void* out, const void* q, const void* k_cache,
                                   const void* v_cache, const float* k_scale,

@@ -26,7 +26,7 @@
 //    TMA ring each and 3 CTAs an SM: 192 KB in flight, as the fp16 kernel.
 //  * Splits and their fp32 partials are the fp16 kernel's.
 //  * What bounds it: HBM.  64 x 4096 of 32 heads, int8 (2.15 GB): 317 us, 6.8 TB/s, the
-//    rate of a plain copy; the same copies without the arithmetic take 319.  256 x 4096 of
+//    rate of a plain copy (327 on another card); the same copies without the arithmetic take 319.  256 x 4096 of
 //    32/8 heads, e4m3: 328-339 us (332 without the arithmetic).  Two contexts of 100k-131k tokens:
 //    92 us, 5.2 TB/s: 83-85 us of it here (3.6 rounds of CTAs), the rest the merge.
 #include <cuda.h>
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 // w + ROW_WARPS, ..., their sums join in warp order.  A CTA (8 warps) a row against a warp
 // a row (whole calls, int8, 32/8 heads unless said): 118 splits of 64 rows 92 us instead
 // of 133, 16 splits (8 x 8000, e4m3) 32.3 and 36.1, 8 splits 33.9 and 36.5 (16 x 4096),
-// 16.3 and 18.3 (8 x 4096, 8/8); 4 splits 35.1 and 34.9 (32 x 2048), 2 splits 38.0 and 35.1
+// 16.3 and 18.3 (8 x 4096, 8/8, its 67 MB in L2); 4 splits 35.1 and 34.9 (32 x 2048), 2 splits 38.0 and 35.1
 // (64 x 1024): a CTA for each of 2048 rows costs more than it reads.
 constexpr int kWideSplits = 8;   // a CTA a row from here on
 constexpr int kMergeWarps = 8;

@@ -24,9 +24,9 @@
 //    (paged) or for 128 tokens (packed).
 //  * What bounds it: in steady state a turn (128 tokens for 256 rows) takes 2300
 //    cycles, of which the tensor core is busy 2048; a unit adds some 4000 at its
-//    ends.  16,384 tokens of 32/8 heads: 1192-1273 us, 1.73-1.84 PFLOP/s (the
-//    measured cuBLAS burst is 1.96; the chip runs at its power limit); 4 x 4096 of 32
-//    heads: 351 us, 1.57.
+//    ends.  16,384 tokens of 32/8 heads: 1180-1310 us in short runs, 1.68-1.86 PFLOP/s
+//    (the measured cuBLAS burst is 1.96), 1370-1460 us in loops of seconds, where the
+//    chip is at its power limit; 4 x 4096 of 32 heads: 345-371 us, 1.48-1.59, and 402-405.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -327,8 +327,8 @@ __device__ __forceinline__ bool make_unit(const Params& p, int bx, int by, int64
 // the context is read from past the cache's last row, where the copy engine fills
 // zeros), become zeros; the others are searched for infinities and NaN, which
 // become zeros too and are added to the rows that see them at the end (add_nonfinite).
-// The search costs 1 % (4 x 4096 of 32 heads 356 us, 351 without; 16 x 512 of 32/8 47.2
-// and 45.9).  The warp that copies V does it: in the work warp, which has the time,
+// The search costs 1 % (in one run, 4 x 4096 of 32 heads 356 us, 351 without; 16 x 512 of
+// 32/8 47.2 and 45.9).  The warp that copies V does it: in the work warp, which has the time,
 // 64 prompts of 128 take 40.6 us instead of 36.6; one tile late, under the next
 // copy, 4 x 4096 takes 361.
 template <int BS>
@@ -399,8 +399,8 @@ __device__ __forceinline__ void add_nonfinite(const Params& p, const Unit& u, ui
 // BS: block size of the paged cache, 0 for packed K and V.
 //
 // One CTA per SM.  Its warps: two softmax warpgroups (one per query tile, one
-// thread per row), a copy warp (TMA), a warp that issues the matrix products
-// and one that fetches work: the grid has a CTA for every unit, and a CTA that
+// thread per row), two copy warps (TMA; Q and K, and V), a warp that issues the matrix
+// products and one that fetches work: the grid has a CTA for every unit, and a CTA that
 // runs takes the place of CTAs that have not started (clusterlaunchcontrol), so
 // that the next unit's copies and first products run beside the last
 // unit's softmax and output, and units of any length balance themselves.
