@@ -470,8 +470,9 @@ int pkv_prompt_attention(void* out, const void* q, const void* k, const void* v,
  * too) or whose context is shorter than its rows or longer than its table
  * (PKV_DEV_BAD_CONTEXT_LEN); a block id out of range (PKV_DEV_BAD_BLOCK_ID).
  * Infinities and NaN are stored as 0 and reported (PKV_DEV_NONFINITE).  Two
- * sequences that write into one block race: give a shared block a private copy
- * first (pkv_copy_blocks on codes and scales).
+ * sequences that write into one block race (as does one whose table lists a
+ * written block twice): give a shared block a private copy first
+ * (pkv_copy_blocks on codes and scales).
  */
 int pkv_reshape_and_cache_q8(const void* k, const void* v, const int32_t* query_start,
                              const int32_t* block_tables, const int32_t* context_lens,
