@@ -597,8 +597,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         base += 2 * n;
       }
-      if (*gave_up) {   // let this warp's copies land before the CTA goes (that of a tile to be
-                        // cleaned counts on a barrier of its own)
+      // a wait gave up: let this warp's copies land before the CTA goes (that of a tile to be
+      // cleaned counts on a barrier of its own)
+      if (__any_sync(kFull, *gave_up)) {
         if (raw_st >= 0) wait(bar(Smem::raw, 0), nraw & 1);
 #pragma unroll 1
         for (int i = 0; i < kStages; ++i)
