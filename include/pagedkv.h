@@ -48,7 +48,7 @@ extern "C" {
 #define PKV_DEV_BAD_SLOT 3         /* slot >= num_blocks * block_size */
 #define PKV_DEV_WAIT_TIMEOUT 4     /* a bounded wait on a copy gave up; every
                                       output of that launch is then undefined */
-#define PKV_DEV_BAD_POSITION 5     /* position outside its block table */
+#define PKV_DEV_BAD_POSITION 5     /* position outside its block table or rotary table */
 #define PKV_DEV_BAD_QUERY_RANGE 7  /* query_start entries that are out of order or past
                                       num_tokens */
 #define PKV_DEV_NONFINITE 8        /* an infinity or NaN to be stored in 8 bits */
@@ -503,6 +503,88 @@ int pkv_paged_attention_decode_q8(void* out, const void* q, const void* k_cache,
                                   int64_t num_blocks, int max_blocks_per_seq, int scale_stride,
                                   float scale, void* workspace, size_t workspace_bytes,
                                   int32_t* dev_err, void* stream);
+
+/* ---- rotary positions -------------------------------------------------------- */
+/*
+ * Rotary positions of q and k, alone or on the way into the cache.  The first
+ * rot_dim = 2 n dims of a head are n pairs, pair j being dims (j, j + n) or, with
+ * `adjacent` not 0, (2 j, 2 j + 1).  A pair (x1, x2) of a token whose position on
+ * the pair's axis is p becomes, with (c, s) = table[p][j],
+ *   (x1 c - x2 s, x2 c + x1 s)
+ * every product and sum rounded to fp32.  fp16 results are rounded once from there.
+ * Dims from rot_dim on are copied.  (Negated sines turn back.)
+ *   table        fp32 [table_rows, n, 2]: cosine and sine of position p's angle p
+ *                inv_freq[j], times whatever magnitude the model gives them; 16-byte
+ *                aligned
+ *   positions    int32 [num_axes, num_tokens] (device): each token's position on
+ *                each axis (text has one; images and video time, height, width).  In
+ *                the calls that write a cache NULL stands for the place of the
+ *                token in its sequence, on every axis
+ *   axes         HOST array of n entries below num_axes: the axis of each pair.
+ *                Read before the call returns.  NULL: axis 0
+ *   num_axes     1 to 4
+ *   rot_dim      a multiple of 16, at most head_dim = 128
+ *   q, k, v, q_out, k_out  fp16, 16-byte aligned; the heads of a token are
+ *                contiguous ([num_heads, 128]) and *_stride halves lie between tokens (a
+ *                multiple of 8, so that slices of one projection's output do; an output's
+ *                at least its heads).  q_out may be q and k_out k with the same
+ *                stride (in place); they may not overlap otherwise.
+ * A token with a position outside [0, table_rows) on some axis is left out, its outputs
+ * as they were, and PKV_DEV_BAD_POSITION reported.
+ */
+
+/* q and k (num_kv_heads 0: q alone) rotated; `positions` is required. */
+int pkv_rotary_embedding(void* q_out, void* k_out, const void* q, const void* k,
+                         int64_t q_out_stride, int64_t k_out_stride, int64_t q_stride,
+                         int64_t k_stride, const int32_t* positions, int num_axes,
+                         const uint8_t* axes, const float* table, int64_t table_rows,
+                         int rot_dim, int adjacent, int num_tokens, int num_q_heads,
+                         int num_kv_heads, int head_dim, int32_t* dev_err, void* stream);
+
+/*
+ * q rotated into q_out, k rotated and v as it is written to the paged fp16 cache:
+ * pkv_rotary_embedding and pkv_reshape_and_cache in one launch.  The batch is
+ * packed: sequence s brings rows query_start[s] .. query_start[s + 1] - 1 of q, k
+ * and v, the last of its context_lens[s] tokens (prompts, chunks and single decoded
+ * tokens alike), which go to the slots their places have in the block table.
+ * block_size is any positive number.  Any number of heads.
+ * Reported, and left out: a sequence whose query_start entries are out of order
+ * or past num_tokens (PKV_DEV_BAD_QUERY_RANGE; sequences beside it may be left out
+ * too) or whose context is shorter than its rows or longer than its table
+ * (PKV_DEV_BAD_CONTEXT_LEN); rows of q_out that no sequence owns stay as they
+ * were.  A token in a block whose id is out of range (PKV_DEV_BAD_BLOCK_ID) is not
+ * cached; its q is rotated.  Two sequences that write one slot race.
+ */
+int pkv_rope_and_cache(void* q_out, const void* q, const void* k, const void* v,
+                       int64_t q_out_stride, int64_t q_stride, int64_t k_stride,
+                       int64_t v_stride, const int32_t* query_start,
+                       const int32_t* block_tables, const int32_t* context_lens, void* k_cache,
+                       void* v_cache, const int32_t* positions, int num_axes,
+                       const uint8_t* axes, const float* table, int64_t table_rows, int rot_dim,
+                       int adjacent, int num_tokens, int num_seqs, int num_q_heads,
+                       int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                       int max_blocks_per_seq, int32_t* dev_err, void* stream);
+
+/*
+ * The same into an 8-bit cache: pkv_reshape_and_cache_q8's rule (see there: one
+ * scale for each block and KV head, earlier codes coded anew when it grows, blocks
+ * that two sequences write) on the rotated k in fp32, with no rounding to fp16 before
+ * the code, and on v.  block_size 8, 16, 32 or 64.  Values of k that are not finite
+ * after the rotation, and such values of v, are stored as 0 and reported
+ * (PKV_DEV_NONFINITE); a token that is left out for its position takes no part in its
+ * block's scale.
+ */
+int pkv_rope_and_cache_q8(void* q_out, const void* q, const void* k, const void* v,
+                          int64_t q_out_stride, int64_t q_stride, int64_t k_stride,
+                          int64_t v_stride, const int32_t* query_start,
+                          const int32_t* block_tables, const int32_t* context_lens,
+                          void* k_cache, void* v_cache, float* k_scale, float* v_scale, int code,
+                          const int32_t* positions, int num_axes, const uint8_t* axes,
+                          const float* table, int64_t table_rows, int rot_dim, int adjacent,
+                          int num_tokens, int num_seqs, int num_q_heads, int num_kv_heads,
+                          int head_dim, int block_size, int64_t num_blocks,
+                          int max_blocks_per_seq, int scale_stride, int32_t* dev_err,
+                          void* stream);
 
 /* ---- swap between pools ---------------------------------------------------- */
 /*

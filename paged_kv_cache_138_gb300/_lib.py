@@ -62,6 +62,13 @@ SIGNATURES = {
                                       _I64, _I, _I, _P, _P]),
     "pkv_paged_attention_decode_q8": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I,
                                            _I64, _I, _I, _F, _P, _SZ, _P, _P]),
+    "pkv_rotary_embedding": (_I, [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _I, _P, _P, _I64, _I,
+                                  _I, _I, _I, _I, _I, _P, _P]),
+    "pkv_rope_and_cache": (_I, [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _I,
+                                _P, _P, _I64, _I, _I, _I, _I, _I, _I, _I, _I, _I64, _I, _P, _P]),
+    "pkv_rope_and_cache_q8": (_I, [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P,
+                                   _P, _I, _P, _I, _P, _P, _I64, _I, _I, _I, _I, _I, _I, _I, _I,
+                                   _I64, _I, _I, _P, _P]),
     "pkv_reshape_and_cache": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I64, _P, _P]),
     "pkv_slot_mapping": (_I, [_P, _P, _I, _I, _I, _I64, _P, _P, _P]),
     "pkv_copy_blocks": (_I, [_P, _P, _I, _P, _I, _I64, _I64, _P, _P]),

@@ -731,3 +731,227 @@ def paged_attention_decode_q8(out, q, k_cache, v_cache, k_scale, v_scale, block_
             dev_err, stream) if prepare else None
     return _run(lib().pkv_paged_attention_decode_q8, args, "paged_attention_decode_q8", prepare,
                 keep, out)
+
+
+# ---- rotary positions -------------------------------------------------------------------
+
+def rope_table(inv_freq, num_positions, magnitude=1.0, device=None):
+    """The table the rotary calls read: fp32 [num_positions, n, 2], magnitude times cosine
+    and sine of position * inv_freq[j], the angles in 64 bits (at a million positions
+    32 bits would be off by 0.03).  inv_freq: n radians a position, a sequence or a tensor."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    f = torch.as_tensor(inv_freq, dtype=torch.float64, device=dev)
+    if f.dim() != 1 or num_positions <= 0:
+        raise ValueError("need inv_freq [n] and a positive number of positions")
+    table = torch.empty((num_positions, f.shape[0], 2), dtype=torch.float32, device=dev)
+    for lo in range(0, num_positions, 1 << 16):   # a bounded amount of 64-bit intermediates
+        hi = min(num_positions, lo + (1 << 16))
+        angle = torch.arange(lo, hi, dtype=torch.float64, device=dev)[:, None] * f
+        table[lo:hi, :, 0] = angle.cos() * magnitude
+        table[lo:hi, :, 1] = angle.sin() * magnitude
+    return table
+
+
+def rope_sections(sizes, round_robin=False):
+    """The axis of each pair for the rotary calls' ``axes``: sizes[a] pairs of axis a, one
+    axis after the other, or dealt one to each axis in turn while it has some left."""
+    if not round_robin:
+        return tuple(a for a, m in enumerate(sizes) for _ in range(m))
+    return tuple(a for r in range(max(sizes)) for a, m in enumerate(sizes) if r < m)
+
+
+@functools.lru_cache(maxsize=256)
+def _pack_axes(axes, n, num_axes):
+    if len(axes) != n or not all(isinstance(a, int) and 0 <= a < num_axes for a in axes):
+        raise ValueError("axes must be %d axis numbers below %d, one for each pair" % (n, num_axes))
+    return bytes(axes)
+
+
+def _rows_of(t, name, dev):
+    """(tokens, heads, halves between tokens) of fp16 [T, H, 128] whose heads are contiguous;
+    the tokens may lie further apart, as in a slice of a projection's output."""
+    try:
+        good = t.dtype is _F16 and t.get_device() == dev and t.dim() == 3
+    except (AttributeError, RuntimeError):
+        good = False
+    if not good:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError("%s must be a CUDA tensor" % name)
+        if t.dtype != _F16:
+            raise TypeError("%s must be %s, got %s" % (name, _F16, t.dtype))
+        if t.dim() != 3:
+            raise ValueError("%s must have 3 dims, got %s" % (name, tuple(t.shape)))
+        raise ValueError("%s must be on the current CUDA device" % name)
+    T, H, D = t.shape
+    a, b, c = t.stride()
+    if D != HEAD_DIM or (c != 1 and T and H) or (b != HEAD_DIM and H > 1 and T):
+        raise ValueError("%s must be [T, heads, %d] with each token's heads contiguous" %
+                         (name, HEAD_DIM))
+    if T <= 1:
+        a = H * HEAD_DIM
+    elif a & 7:
+        raise ValueError("%s must have a multiple of 8 elements between tokens" % name)
+    return T, H, a
+
+
+def _rope_args(table, positions, axes, T, dev, required):
+    """(positions, num_axes, axes, table, table rows, rot_dim) as the C calls take them."""
+    try:
+        good = (table.dtype is _F32 and table.get_device() == dev and table.is_contiguous() and
+                table.dim() == 3)
+    except (AttributeError, RuntimeError):
+        good = False
+    if not good:
+        _explain((table, "table", _F32, 3))
+    rows, n, two = table.shape
+    if two != 2:
+        raise ValueError("table must be [positions, pairs, 2]")
+    num = 1
+    if positions is None:
+        if required:
+            raise TypeError("positions must be a CUDA tensor")
+        if axes is not None:
+            axes = _pack_axes(tuple(axes), n, 4)
+            num = 4
+    else:
+        try:
+            good = (positions.dtype is _I32 and positions.get_device() == dev and
+                    positions.is_contiguous() and 1 <= positions.dim() <= 2)
+        except (AttributeError, RuntimeError):
+            good = False
+        if not good:
+            _explain((positions, "positions", _I32, 2 if getattr(positions, "ndim", 1) > 1 else 1))
+        shape = positions.shape
+        if shape[-1] != T:
+            raise ValueError("positions must have one entry for each token")
+        num = shape[0] if len(shape) == 2 else 1
+        if not 1 <= num <= 4:
+            raise ValueError("positions must have 1 to 4 axes")
+        if axes is not None:
+            axes = _pack_axes(tuple(axes), n, num)
+        elif num > 1:
+            raise ValueError("axes must say which of the %d axes each pair follows" % num)
+    return _ptr(positions), num, axes, table.data_ptr(), rows, 2 * n
+
+
+def _check_out_stride(name, T, H, stride):
+    if T > 1 and stride < H * HEAD_DIM:
+        raise ValueError("tokens of %s overlap" % name)
+
+
+def rotary_embedding(q_out, k_out, q, k, positions, table, axes=None, adjacent=False, dev_err=None,
+                     stream=None, prepare=False):
+    """q_out = q and k_out = k [T, heads, 128] rotated by ``positions`` int32 [T], or [axes, T]
+    with ``axes`` the axis of each pair (rope_sections), through ``table`` (rope_table).
+    Pairs are dims (j, j + n), or (2j, 2j + 1) if ``adjacent``.  The tensors may be slices
+    of a projection's output, and q_out q, k_out k (in place); k and k_out may be None.
+    prepare=True returns a PreparedLaunch instead of launching."""
+    dev = _get_device()
+    T, Hq, sq = _rows_of(q, "q", dev)
+    To, Ho, so = _rows_of(q_out, "q_out", dev)
+    Hkv = sk = sko = 0
+    if (k is None) != (k_out is None):
+        raise TypeError("k and k_out go together")
+    if k is not None:
+        Tk, Hkv, sk = _rows_of(k, "k", dev)
+        Tko, Hko, sko = _rows_of(k_out, "k_out", dev)
+        if Tk != T or Tko != T or Hko != Hkv:
+            raise ValueError("shape mismatch")
+        _check_out_stride("k_out", T, Hkv, sko)
+    if To != T or Ho != Hq:
+        raise ValueError("shape mismatch")
+    _check_out_stride("q_out", T, Hq, so)
+    rot = _rope_args(table, positions, axes, T, dev, True)
+    if dev_err is not None:
+        _check_side(None, dev_err)
+    args = (q_out.data_ptr(), _ptr(k_out), q.data_ptr(), _ptr(k), so, sko, sq, sk, *rot,
+            int(bool(adjacent)), T, Hq, Hkv, HEAD_DIM, _ptr(dev_err), _stream_handle(stream))
+    keep = (q_out, k_out, q, k, positions, table, dev_err, stream) if prepare else None
+    return _run(lib().pkv_rotary_embedding, args, "rotary_embedding", prepare, keep, None)
+
+
+def _append_args(q_out, q, k, v, query_start, block_tables, context_lens, table, positions, axes):
+    """What both caches' calls share: sizes (T, S, Hq, Hkv, max_blocks), strides, rotation."""
+    dev = _get_device()
+    T, Hq, sq = _rows_of(q, "q", dev)
+    To, Ho, so = _rows_of(q_out, "q_out", dev)
+    Tk, Hkv, sk = _rows_of(k, "k", dev)
+    Tv, Hv, sv = _rows_of(v, "v", dev)
+    try:
+        good = (query_start.dtype is _I32 and query_start.get_device() == dev and
+                query_start.is_contiguous() and
+                block_tables.dtype is _I32 and block_tables.get_device() == dev and
+                block_tables.is_contiguous() and
+                context_lens.dtype is _I32 and context_lens.get_device() == dev and
+                context_lens.is_contiguous() and block_tables.dim() == 2)
+    except (AttributeError, RuntimeError):
+        good = False
+    if not good:
+        _explain((query_start, "query_start", _I32, 1), (block_tables, "block_tables", _I32, 2),
+                 (context_lens, "context_lens", _I32, 1))
+    S, max_blocks = block_tables.shape
+    if To != T or Tk != T or Tv != T or Ho != Hq or Hv != Hkv:
+        raise ValueError("shape mismatch")
+    if query_start.shape != (S + 1,) or context_lens.shape != (S,):
+        raise ValueError("query_start must have num_seqs + 1 entries, context_lens num_seqs")
+    _check_out_stride("q_out", T, Hq, so)
+    return (T, S, Hq, Hkv, max_blocks), (so, sq, sk, sv), \
+        _rope_args(table, positions, axes, T, dev, False)
+
+
+def rope_and_cache(q_out, q, k, v, query_start, block_tables, context_lens, k_cache, v_cache, table,
+                   positions=None, axes=None, adjacent=False, dev_err=None, stream=None,
+                   prepare=False):
+    """One launch: q [T, Hq, 128] rotated into q_out, k rotated and v as it is written to the
+    paged fp16 cache.  Sequence s brings rows query_start[s] .. query_start[s + 1] - 1, the
+    last of its context_lens[s] tokens; without ``positions`` a token's position is its place
+    in the sequence.  ``table``, ``positions``, ``axes``, ``adjacent`` and the layout of q, k,
+    v and q_out as in rotary_embedding.
+    prepare=True returns a PreparedLaunch instead of launching."""
+    (T, S, Hq, Hkv, max_blocks), strides, rot = _append_args(
+        q_out, q, k, v, query_start, block_tables, context_lens, table, positions, axes)
+    try:
+        dev = _get_device()
+        good = (k_cache.dtype is _F16 and k_cache.get_device() == dev and
+                k_cache.is_contiguous() and
+                v_cache.dtype is _F16 and v_cache.get_device() == dev and
+                v_cache.is_contiguous() and k_cache.dim() == 4)
+    except (AttributeError, RuntimeError):
+        good = False
+    if not good:
+        _explain((k_cache, "k_cache", _F16, 4), (v_cache, "v_cache", _F16, 4))
+    nb, bs, Hc, D = cache = k_cache.shape
+    if v_cache.shape != cache or Hc != Hkv or D != HEAD_DIM:
+        raise ValueError("shape mismatch")
+    if dev_err is not None:
+        _check_side(None, dev_err)
+    args = (q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides,
+            query_start.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), *rot, int(bool(adjacent)), T, S, Hq, Hkv, D,
+            bs, nb, max_blocks, _ptr(dev_err), _stream_handle(stream))
+    keep = (q_out, q, k, v, query_start, block_tables, context_lens, k_cache, v_cache, table,
+            positions, dev_err, stream) if prepare else None
+    return _run(lib().pkv_rope_and_cache, args, "rope_and_cache", prepare, keep, None)
+
+
+def rope_and_cache_q8(q_out, q, k, v, query_start, block_tables, context_lens, k_cache, v_cache,
+                      k_scale, v_scale, table, positions=None, axes=None, adjacent=False,
+                      dev_err=None, stream=None, prepare=False):
+    """rope_and_cache into an 8-bit cache (q8_cache): the rule of reshape_and_cache_q8 on the
+    rotated k in 32 bits and on v.
+    prepare=True returns a PreparedLaunch instead of launching."""
+    (T, S, Hq, Hkv, max_blocks), strides, rot = _append_args(
+        q_out, q, k, v, query_start, block_tables, context_lens, table, positions, axes)
+    code, nb, bs, Hc, D, stride = _q8_args(k_cache, v_cache, k_scale, v_scale)
+    if Hc != Hkv or D != HEAD_DIM:
+        raise ValueError("shape mismatch")
+    if dev_err is not None:
+        _check_side(None, dev_err)
+    args = (q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides,
+            query_start.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), code,
+            *rot, int(bool(adjacent)), T, S, Hq, Hkv, D, bs, nb, max_blocks, stride,
+            _ptr(dev_err), _stream_handle(stream))
+    keep = (q_out, q, k, v, query_start, block_tables, context_lens, k_cache, v_cache, k_scale,
+            v_scale, table, positions, dev_err, stream) if prepare else None
+    return _run(lib().pkv_rope_and_cache_q8, args, "rope_and_cache_q8", prepare, keep, None)
