@@ -504,6 +504,32 @@ int pkv_paged_attention_decode_q8(void* out, const void* q, const void* k_cache,
                                   float scale, void* workspace, size_t workspace_bytes,
                                   int32_t* dev_err, void* stream);
 
+/*
+ * Causal attention of prompt chunks over an 8-bit cache: pkv_paged_attention_prefill
+ * with K_s[t] = code * k_scale[block of t, g] and V_s[t] likewise.  Same packed batch,
+ * shapes, limits, workspace (pkv_paged_attention_prefill_workspace_bytes), errors and
+ * output: whole prompts, chunks behind earlier ones or behind a cached prefix, a few draft
+ * tokens.  All of the context's K and V must already be in the cache
+ * (pkv_reshape_and_cache_q8, pkv_rope_and_cache_q8).
+ *   k_cache, v_cache  codes, 16-byte aligned; k_scale, v_scale 4-byte aligned
+ * Scales must be finite and not negative (a zero scale is a block of zeros; a V scale
+ * below 2^-33 counts as 2^-33), and so must the e4m3 codes of a context; codes past the
+ * context may be any bytes, scales of blocks past it anything.  fp32 scores, sums and
+ * accumulators; the softmax weights, with the V scale folded in, are rounded to fp16 for
+ * the product with V (by half a step, or by 2^-32 of the largest), the result once.  A
+ * row with a score that is NaN or +infinity (an infinity or NaN in q, a softmax scale
+ * that is not finite) is NaN.
+ */
+int pkv_paged_attention_prefill_q8(void* out, const void* q, const void* k_cache,
+                                   const void* v_cache, const float* k_scale,
+                                   const float* v_scale, int code, const int32_t* block_tables,
+                                   const int32_t* context_lens, const int32_t* query_start,
+                                   int num_tokens, int num_seqs, int num_q_heads,
+                                   int num_kv_heads, int head_dim, int block_size,
+                                   int64_t num_blocks, int max_blocks_per_seq, int scale_stride,
+                                   float scale, void* workspace, size_t workspace_bytes,
+                                   int32_t* dev_err, void* stream);
+
 /* ---- rotary positions -------------------------------------------------------- */
 /*
  * Rotary positions of q and k, alone or on the way into the cache.  The first

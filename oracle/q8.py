@@ -85,3 +85,26 @@ def decode(q, k_codes, v_codes, k_scale, v_scale, tables, lens, scale, block_siz
             peak[s, h] = (p * vs).max()
             top[s, h] = np.abs(x).max()
     return out, spread, peak, top
+
+
+def chunk(q, k_codes, v_codes, k_scale, v_scale, first, scale):
+    """Causal attention of one sequence in fp64: q [n, Hq, D] at positions first .. first + n - 1,
+    codes [L, Hkv, D] with a scale for each token and head [L, Hkv].  Returns the output and,
+    for error bounds: the sum of weight * |V| (like out), the largest weight * v_scale and the
+    largest sum of |scale q_i k_i| [n, Hq]."""
+    n, Hq, D = q.shape
+    L, Hkv, _ = k_codes.shape
+    out, spread = np.zeros((n, Hq, D)), np.zeros((n, Hq, D))
+    peak, mag = np.zeros((n, Hq)), np.zeros((n, Hq))
+    see = np.arange(L)[None] <= (first + np.arange(n))[:, None]
+    for h in range(Hq):
+        g = h // (Hq // Hkv)
+        ks, vs = (np.asarray(a[:, g], np.float64)[:, None] for a in (k_scale, v_scale))
+        Q, K, V = np.asarray(q[:, h], np.float64), k_codes[:, g] * ks, v_codes[:, g] * vs
+        x = np.where(see, scale * (Q @ K.T), -np.inf)
+        p = np.exp(x - x.max(axis=1, keepdims=True))
+        p /= p.sum(axis=1, keepdims=True)
+        out[:, h], spread[:, h] = p @ V, p @ np.abs(V)
+        peak[:, h] = (p * vs[:, 0]).max(axis=1)
+        mag[:, h] = abs(scale) * np.where(see, np.abs(Q) @ np.abs(K).T, 0).max(axis=1)
+    return out, spread, peak, mag

@@ -733,6 +733,52 @@ def paged_attention_decode_q8(out, q, k_cache, v_cache, k_scale, v_scale, block_
                 keep, out)
 
 
+def paged_attention_prefill_q8(out, q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                               context_lens, query_start, scale, workspace=None, dev_err=None,
+                               stream=None, prepare=False):
+    """paged_attention_prefill over an 8-bit cache (see q8_cache, reshape_and_cache_q8,
+    rope_and_cache_q8); same workspace (prefill_workspace_bytes).
+    prepare=True returns a PreparedLaunch instead of launching."""
+    try:
+        dev = _get_device()
+        good = (q.dtype is _F16 and q.get_device() == dev and q.is_contiguous() and
+                out.dtype is _F16 and out.get_device() == dev and out.is_contiguous() and
+                block_tables.dtype is _I32 and block_tables.get_device() == dev and
+                block_tables.is_contiguous() and
+                context_lens.dtype is _I32 and context_lens.get_device() == dev and
+                context_lens.is_contiguous() and
+                query_start.dtype is _I32 and query_start.get_device() == dev and
+                query_start.is_contiguous() and q.dim() == 3 and block_tables.dim() == 2)
+    except (AttributeError, RuntimeError):
+        good = False
+    if not good:
+        _explain((q, "q", _F16, 3), (out, "out", _F16, 3),
+                 (block_tables, "block_tables", _I32, 2), (context_lens, "context_lens", _I32, 1),
+                 (query_start, "query_start", _I32, 1))
+    code, nb, bs, Hkv, D, stride = _q8_args(k_cache, v_cache, k_scale, v_scale)
+    T, Hq, D2 = shape = q.shape
+    S, max_blocks = block_tables.shape
+    if out.shape != shape or D2 != D:
+        raise ValueError("shape mismatch")
+    if query_start.shape != (S + 1,) or context_lens.shape != (S,):
+        raise ValueError("query_start must have num_seqs + 1 entries, context_lens num_seqs")
+    if workspace is not None or dev_err is not None:
+        _check_side(workspace, dev_err)
+    if workspace is None:
+        need = prefill_workspace_bytes(T, S, Hq, Hkv, max_blocks, bs)
+        if need:
+            workspace = _new_workspace(need, q.device, stream)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    args = (out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scale.data_ptr(), v_scale.data_ptr(), code, block_tables.data_ptr(),
+            context_lens.data_ptr(), query_start.data_ptr(), T, S, Hq, Hkv, D, bs, nb, max_blocks,
+            stride, float(scale), _ptr(workspace), ws_bytes, _ptr(dev_err), _stream_handle(stream))
+    keep = (out, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start,
+            workspace, dev_err, stream) if prepare else None
+    return _run(lib().pkv_paged_attention_prefill_q8, args, "paged_attention_prefill_q8", prepare,
+                keep, out)
+
+
 # ---- rotary positions -------------------------------------------------------------------
 
 def rope_table(inv_freq, num_positions, magnitude=1.0, device=None):
