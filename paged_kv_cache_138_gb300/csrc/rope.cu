@@ -15,7 +15,9 @@
 //
 // What bounds it: HBM for prompts; a step of single tokens is a chain of dependent loads
 // (sequence, position, table and block id, scale).
+#include <algorithm>
 #include <climits>
+#include <initializer_list>
 
 #include "q8_device.cuh"
 
@@ -33,6 +35,7 @@ struct Rotation {
   int num_axes;
   int n;                       // pairs, a multiple of 8
   uint32_t axis[4];            // two bits a pair
+  int in_twos;                 // pairs 2 i and 2 i + 1 always follow one axis
 };
 
 struct RowParams {
@@ -45,6 +48,7 @@ struct RowParams {
   int32_t* dev_err;
   int64_t num_blocks;
   int num_tokens, num_seqs, num_q_heads, num_kv_heads, block_size, max_blocks;
+  int part_rows;               // of a warp of rope_rows_kernel
 };
 
 // A row of a head is worked by 8 lanes, two 16-byte chunks each: a rotating lane c holds
@@ -61,41 +65,64 @@ struct Chunks {
   }
 };
 
-// a token's positions on the axes; false: one lies outside the table
-__device__ __forceinline__ bool load_positions(const Rotation& r, int64_t token, int place,
-                                               int32_t (&pos)[kMaxAxes]) {
+// a token's positions on the axes (AXES: 1, or kMaxAxes with num_axes of them in use)
+template <int AXES>
+__device__ __forceinline__ void load_positions(const Rotation& r, int64_t token, int place,
+                                               int32_t (&pos)[AXES]) {
+#pragma unroll
+  for (int a = 0; a < AXES; ++a) {
+    pos[a] = place;
+    if (r.positions && (a == 0 || a < r.num_axes)) pos[a] = __ldg(r.positions + a * r.num_tokens + token);
+  }
+}
+// false: one lies outside the table
+template <int AXES>
+__device__ __forceinline__ bool on_table(const Rotation& r, const int32_t (&pos)[AXES]) {
   bool ok = true;
 #pragma unroll
-  for (int a = 0; a < kMaxAxes; ++a) {
-    pos[a] = place;
-    if (r.positions && a < r.num_axes) pos[a] = __ldg(r.positions + a * r.num_tokens + token);
-    if (a < r.num_axes) ok = ok && pos[a] >= 0 && pos[a] < r.table_rows;
-  }
+  for (int a = 0; a < AXES; ++a)
+    if (a == 0 || a < r.num_axes) ok = ok && static_cast<uint32_t>(pos[a]) < static_cast<uint32_t>(r.table_rows);
   return ok;
 }
 
-// cosines and sines of the lane's 8 pairs (rotating lanes)
-template <bool ADJACENT>
+// Cosines and sines of the lane's 8 pairs (rotating lanes), as packed arithmetic takes them:
+// pairs 2 i and 2 i + 1 are (c, c', s, s').
+template <bool ADJACENT, int AXES>
 __device__ __forceinline__ void load_turn(const Rotation& r, const Chunks& ch,
-                                          const int32_t (&pos)[kMaxAxes], float2 (&cs)[8]) {
+                                          const int32_t (&pos)[AXES], float4 (&cs)[4]) {
   const int p0 = ADJACENT ? 4 * ch.a : 8 * ch.a, p1 = ADJACENT ? 4 * ch.b : p0 + 4;
-  if (r.num_axes == 1) {
-    const float* row = r.table + static_cast<int64_t>(pos[0]) * r.n * 2;
+  const float2* table = reinterpret_cast<const float2*>(r.table);
+  if (AXES == 1) {
+    const float4* row = reinterpret_cast<const float4*>(table + static_cast<int64_t>(pos[0]) * r.n);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 w = __ldg(reinterpret_cast<const float4*>(row + 2 * (i < 2 ? p0 : p1)) + (i & 1));
-      cs[2 * i] = make_float2(w.x, w.y);
-      cs[2 * i + 1] = make_float2(w.z, w.w);
+      const float4 w = __ldg(row + (i < 2 ? p0 : p1) / 2 + (i & 1));
+      cs[i] = make_float4(w.x, w.z, w.y, w.w);
+    }
+    return;
+  }
+  // the axes of the first and the last four pairs, two bits each
+  const auto word = [&](int p) {
+    const uint32_t lo = p & 16 ? r.axis[1] : r.axis[0], hi = p & 16 ? r.axis[3] : r.axis[2];
+    return (p & 32 ? hi : lo) >> (2 * (p & 15));
+  };
+  const uint32_t axes0 = word(p0), axes1 = ADJACENT ? word(p1) : axes0 >> 8;
+  const auto at = [&](int e) {   // the table's entry of the lane's pair e
+    const uint32_t a = (e < 4 ? axes0 : axes1) >> (2 * (e & 3));
+    const int32_t lo = a & 1 ? pos[1 % AXES] : pos[0], hi = a & 1 ? pos[3 % AXES] : pos[2 % AXES];
+    return table + static_cast<int64_t>(a & 2 ? hi : lo) * r.n + (e < 4 ? p0 : p1) + (e & 3);
+  };
+  if (r.in_twos) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 w = __ldg(reinterpret_cast<const float4*>(at(2 * i)));
+      cs[i] = make_float4(w.x, w.z, w.y, w.w);
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int p = (e < 4 ? p0 : p1) + (e & 3);
-      const int w = p >> 4;
-      const uint32_t word = w & 2 ? (w & 1 ? r.axis[3] : r.axis[2]) : (w & 1 ? r.axis[1] : r.axis[0]);
-      const uint32_t a = word >> (2 * (p & 15)) & 3;
-      const int32_t at = a & 2 ? (a & 1 ? pos[3] : pos[2]) : (a & 1 ? pos[1] : pos[0]);
-      cs[e] = __ldg(reinterpret_cast<const float2*>(r.table) + static_cast<int64_t>(at) * r.n + p);
+    for (int i = 0; i < 4; ++i) {
+      const float2 w = __ldg(at(2 * i)), v = __ldg(at(2 * i + 1));
+      cs[i] = make_float4(w.x, v.x, w.y, v.y);
     }
   }
 }
@@ -112,38 +139,40 @@ __device__ __forceinline__ uint4 narrow(const float (&f)[8]) {
                     pack_half2(f[6], f[7]));
 }
 
-__device__ __forceinline__ void turn(float& x1, float& x2, float2 cs) {
-  const float y1 = __fsub_rn(__fmul_rn(x1, cs.x), __fmul_rn(x2, cs.y));
-  x2 = __fadd_rn(__fmul_rn(x2, cs.x), __fmul_rn(x1, cs.y));
-  x1 = y1;
+// two pairs at a time: (x1 c - x2 s, x2 c + x1 s), each product and sum rounded by itself.
+// The sums stay scalar: packed ones were contracted with the packed products.
+__device__ __forceinline__ void turn2(float& x1, float& y1, float& x2, float& y2, float4 cs) {
+  const float2 a = make_float2(x1, y1), b = make_float2(x2, y2);
+  const float2 c = make_float2(cs.x, cs.y), s = make_float2(cs.z, cs.w);
+  const float2 ac = fmul2(a, c), bs = fmul2(b, s), bc = fmul2(b, c), as = fmul2(a, s);
+  x1 = __fsub_rn(ac.x, bs.x), y1 = __fsub_rn(ac.y, bs.y);
+  x2 = __fadd_rn(bc.x, as.x), y2 = __fadd_rn(bc.y, as.y);
 }
 
 // the lane's two chunks, widened and rotated
 template <bool ADJACENT>
-__device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const float2 (&cs)[8]) {
+__device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const float4 (&cs)[4]) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    if (!ADJACENT)
-      turn(a[e], b[e], cs[e]);
-    else if (e < 4)
-      turn(a[2 * e], a[2 * e + 1], cs[e]);
-    else
-      turn(b[2 * e - 8], b[2 * e - 7], cs[e]);
+  for (int i = 0; i < 4; ++i) {
+    if (!ADJACENT) {
+      turn2(a[2 * i], a[2 * i + 1], b[2 * i], b[2 * i + 1], cs[i]);
+    } else {
+      float* f = i < 2 ? a + 4 * i : b + 4 * i - 8;
+      turn2(f[0], f[2], f[1], f[3], cs[i]);
+    }
   }
 }
 
 // ---- rows: rotary alone, and the fp16 cache ----------------------------------------------
-// One warp per (token, 16 of its heads' rows), 4 rows a pass: the rows are loaded before
+// One warp per (token, up to 16 of its heads' rows), 4 rows a pass: the rows are loaded before
 // the warp knows the token's sequence, position, cosines and block, whose loads depend on
-// one another.  A prompt's warps are many enough to cover that chain, and a step's single
-// tokens are spread over many warps by their heads; a warp for a whole token would walk 3
-// to 8 times as many rows in turn.
+// one another.  A prompt's warps are many enough to cover that chain (24 on an SM), and a
+// step's single tokens are spread over many warps by their heads.
 constexpr int kRowWarps = 4;
-constexpr int kPasses = 4;             // of 4 rows each
-constexpr int kPartRows = 4 * kPasses;
+constexpr int kPasses = 4;             // of 4 rows each, at most
 
-template <bool CACHE, bool ADJACENT>
-__global__ void __launch_bounds__(kRowWarps * 32) rope_rows_kernel(const RowParams p) {
+template <bool CACHE, bool ADJACENT, int AXES>
+__global__ void __launch_bounds__(kRowWarps * 32, 7) rope_rows_kernel(const RowParams p) {
   // a programmatic dependent of the stream's previous kernel, and the next one may
   // place its CTAs while this grid runs: each reads after its wait
   asm volatile("griddepcontrol.launch_dependents;");
@@ -155,55 +184,61 @@ __global__ void __launch_bounds__(kRowWarps * 32) rope_rows_kernel(const RowPara
       packed_seq(p.query_start, p.context_lens, s, p.num_tokens, max_context, p.dev_err, true);
   const int i = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
   if (i >= p.num_tokens) return;
-  const int rows = p.num_q_heads + (CACHE ? 2 : 1) * p.num_kv_heads;
-  const int row0 = blockIdx.y * kPartRows + (lane >> 3);
+  const int row0 = blockIdx.y * p.part_rows + (lane >> 3);
+  const int rows = min(p.num_q_heads + (CACHE ? 2 : 1) * p.num_kv_heads, (blockIdx.y + 1) * p.part_rows);
   const Chunks ch(lane & 7, p.rot.n);
+  const int q_end = p.num_q_heads, k_end = q_end + p.num_kv_heads;
 
+  int32_t pos[AXES];
+  if (!CACHE) load_positions(p.rot, i, 0, pos);
   // plain loads: q and k may be rotated in place
   uint4 xa[kPasses], xb[kPasses];
+  const __half* from_q = p.q + i * p.q_stride;
+  const __half* from_k = p.k + i * p.k_stride;
+  const __half* from_v = CACHE ? p.v + i * p.v_stride : nullptr;
 #pragma unroll
   for (int u = 0; u < kPasses; ++u) {
     const int row = row0 + 4 * u;
     if (row >= rows) continue;
-    const int head = row < p.num_q_heads ? row : (row - p.num_q_heads) % p.num_kv_heads;
-    const __half* from = row < p.num_q_heads                      ? p.q + i * p.q_stride
-                         : row < p.num_q_heads + p.num_kv_heads ? p.k + i * p.k_stride
-                                                                : p.v + i * p.v_stride;
-    const uint4* at = reinterpret_cast<const uint4*>(from + head * kHeadDim);
+    const __half* from = row < q_end               ? from_q + row * kHeadDim
+                         : !CACHE || row < k_end ? from_k + (row - q_end) * kHeadDim
+                                                 : from_v + (row - k_end) * kHeadDim;
+    const uint4* at = reinterpret_cast<const uint4*>(from);
     xa[u] = at[ch.a];
     xb[u] = at[ch.b];
   }
 
-  int place = 0;
-  int64_t slot = -1;
+  int64_t slot = 0;
   if (CACHE) {
     const int s = find_unit_seq(p.query_start, p.num_seqs, i, 1, 0);
     const PackedSeq q = packed_seq(p.query_start, p.context_lens, s, p.num_tokens, max_context,
                                    p.dev_err, false);
     if (!q.ok || i < q.row0 || i >= q.row0 + q.n) return;
-    place = q.ctx - q.n + (i - q.row0);
+    const int place = q.ctx - q.n + (i - q.row0);
+    load_positions(p.rot, i, place, pos);
     const int lb = place / p.block_size;
     const int32_t blk = __ldg(p.block_tables + static_cast<int64_t>(s) * p.max_blocks + lb);
-    if (blk >= 0 && blk < p.num_blocks)
-      slot = static_cast<int64_t>(blk) * p.block_size + (place - lb * p.block_size);
-    else if (lane == 0)
-      report(p.dev_err, PKV_DEV_BAD_BLOCK_ID);
+    slot = blk >= 0 && blk < p.num_blocks
+               ? static_cast<int64_t>(blk) * p.block_size + (place - lb * p.block_size)
+               : -1;
   }
-  int32_t pos[kMaxAxes];
-  if (!load_positions(p.rot, i, place, pos)) {
+  if (!on_table(p.rot, pos)) {
     if (lane == 0) report(p.dev_err, PKV_DEV_BAD_POSITION);
     return;
   }
-  float2 cs[8];
+  float4 cs[4];
   if (ch.turns) load_turn<ADJACENT>(p.rot, ch, pos, cs);
+  if (slot < 0 && lane == 0) report(p.dev_err, PKV_DEV_BAD_BLOCK_ID);
 
+  const int64_t kv_row = slot * p.num_kv_heads * kHeadDim;
+  __half* to_q = p.q_out + i * p.q_out_stride;
+  __half* to_k = CACHE ? p.k_cache + kv_row : p.k_out + i * p.k_out_stride;
+  __half* to_v = p.v_cache + kv_row;
 #pragma unroll
   for (int u = 0; u < kPasses; ++u) {
     const int row = row0 + 4 * u;
     if (row >= rows) continue;
-    const bool is_q = row < p.num_q_heads, is_k = !is_q && row < p.num_q_heads + p.num_kv_heads;
-    const int head = is_q ? row : (row - p.num_q_heads) % p.num_kv_heads;
-    if (ch.turns && (is_q || is_k)) {
+    if (ch.turns && (!CACHE || row < k_end)) {
       float a[8], b[8];
       widen(xa[u], a);
       widen(xb[u], b);
@@ -211,15 +246,10 @@ __global__ void __launch_bounds__(kRowWarps * 32) rope_rows_kernel(const RowPara
       xa[u] = narrow(a);
       xb[u] = narrow(b);
     }
-    __half* to;
-    if (is_q) {
-      to = p.q_out + i * p.q_out_stride + head * kHeadDim;
-    } else if (!CACHE) {
-      to = p.k_out + i * p.k_out_stride + head * kHeadDim;
-    } else {
-      if (slot < 0) continue;
-      to = (is_k ? p.k_cache : p.v_cache) + (slot * p.num_kv_heads + head) * kHeadDim;
-    }
+    if (row >= q_end && slot < 0) continue;
+    __half* to = row < q_end               ? to_q + row * kHeadDim
+                 : !CACHE || row < k_end ? to_k + (row - q_end) * kHeadDim
+                                         : to_v + (row - k_end) * kHeadDim;
     reinterpret_cast<uint4*>(to)[ch.a] = xa[u];
     reinterpret_cast<uint4*>(to)[ch.b] = xb[u];
   }
@@ -232,6 +262,7 @@ struct Q8Params {
   float *k_scale, *v_scale;    // [num_blocks, scale_stride]
   int scale_stride;
   int by_token;                // units are tokens, see below
+  int heads_per_cta;           // a multiple of 4 kQ8Warps
 };
 
 // The new rows of one block of one sequence.
@@ -273,131 +304,295 @@ __device__ __forceinline__ bool find_piece(const Q8Params& qp, Piece& c) {
   return true;
 }
 
-// Heads are numbered q, k, v.  `lanes`: the lanes that share a block and head (32, or 8
-// when each group of 8 lanes has a head of its own and one row).  The rotated values are
-// computed twice, for the maximum and for the codes: held in 32 bits they would take
-// twice the registers of the fp16 rows, and the table's lines are in L1.
-template <class Code, int BS, bool ADJACENT, bool STEP>
-__device__ __forceinline__ void append_head(const Q8Params& qp, const Piece& c, int head,
-                                            bool valid) {
-  constexpr int kRows = STEP ? 1 : BS / 4;   // rows of a lane
-  const RowParams& p = qp.r;
-  const int lane = threadIdx.x & 31;
-  const Chunks ch(lane & 7, p.rot.n);
-  const bool is_q = head < p.num_q_heads, is_v = head >= p.num_q_heads + p.num_kv_heads;
-  const int g = is_q ? head : (head - p.num_q_heads) % p.num_kv_heads;
-  const int64_t in_stride = is_q ? p.q_stride : is_v ? p.v_stride : p.k_stride;
-  const __half* src = (is_q ? p.q : is_v ? p.v : p.k) + g * kHeadDim;
-  const auto row_of = [&](int u) { return STEP ? c.r0 : 4 * u + (lane >> 3); };
-  const auto in_range = [&](int u) { return valid && row_of(u) >= c.r0 && row_of(u) < c.r1; };
+// Where a head's rows come from and its codes go; heads are numbered q, k, v.
+struct HeadAt {
+  bool is_q, is_v;
+  int g;
+  const __half* src;     // its row of packed row 0
+  int64_t stride;
+  uint8_t* dst;          // its codes of the block's row 0
+  float* scale;
+  __device__ __forceinline__ HeadAt(const Q8Params& qp, const Piece& c, int block_size, int head) {
+    const RowParams& p = qp.r;
+    is_q = head < p.num_q_heads;
+    is_v = head >= p.num_q_heads + p.num_kv_heads;
+    g = is_q ? head : is_v ? head - p.num_q_heads - p.num_kv_heads : head - p.num_q_heads;
+    src = (is_q ? p.q : is_v ? p.v : p.k) + g * kHeadDim;
+    stride = is_q ? p.q_stride : is_v ? p.v_stride : p.k_stride;
+    dst = (is_v ? qp.v_codes : qp.k_codes) +
+          (c.blk * block_size * p.num_kv_heads + g) * kHeadDim;
+    scale = (is_v ? qp.v_scale : qp.k_scale) + c.blk * qp.scale_stride + g;
+  }
+};
 
-  uint4 xa[kRows], xb[kRows];
-#pragma unroll
-  for (int u = 0; u < kRows; ++u) {
-    if (!in_range(u)) continue;
-    const uint4* at = reinterpret_cast<const uint4*>(src + (c.row0 + row_of(u)) * in_stride);
-    xa[u] = at[ch.a];
-    xb[u] = at[ch.b];
-  }
-  const int64_t row_elems = static_cast<int64_t>(p.num_kv_heads) * kHeadDim;
-  uint8_t* dst = (is_v ? qp.v_codes : qp.k_codes) + c.blk * BS * row_elems + g * kHeadDim;
-  float* scale_at = (is_v ? qp.v_scale : qp.k_scale) + c.blk * qp.scale_stride + g;
-  const bool stores = valid && !is_q && c.blk >= 0;
-  const float before = stores && c.r0 > 0 ? *scale_at : 0.f;
+constexpr uint32_t kInf = 0x7f800000u;
 
-  // row u's values in 32 bits; false: it is left out
-  const auto values = [&](int u, float (&a)[8], float (&b)[8]) {
-    const int r = row_of(u);
-    int32_t pos[kMaxAxes];
-    if (!load_positions(p.rot, c.row0 + r, c.base + r, pos)) return false;
-    widen(xa[u], a);
-    widen(xb[u], b);
-    if (!is_v && ch.turns) {
-      float2 cs[8];
-      load_turn<ADJACENT>(p.rot, ch, pos, cs);
-      rotate<ADJACENT>(a, b, cs);
-    }
-    return true;
-  };
-
-  // the largest magnitude: as unsigned integers the bits of |y| order as |y| does, and
-  // those of infinities and NaN lie above
-  constexpr uint32_t kInf = 0x7f800000u;
-  uint32_t top = 0, all = 0;   // of the finite ones, of all
+// the largest magnitude of a chunk, NaN above all: as unsigned integers the bits of what is
+// not negative order as the numbers do
+__device__ __forceinline__ float top_of(float m, const float (&f)[8]) {
 #pragma unroll
-  for (int u = 0; u < kRows; ++u) {
-    if (!in_range(u)) continue;
-    float a[8], b[8];
-    if (!values(u, a, b)) {
-      if ((lane & 7) == 0) report(p.dev_err, PKV_DEV_BAD_POSITION);
-      continue;
-    }
-    if (is_q) {
-      uint4* to = reinterpret_cast<uint4*>(
-          p.q_out + (c.row0 + row_of(u)) * p.q_out_stride + g * kHeadDim);
-      to[ch.a] = narrow(a);
-      to[ch.b] = narrow(b);
-    } else {
+  for (int e = 0; e < 8; e += 2)
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(f[e]), "f"(f[e + 1]));
+  return m;
+}
+__device__ __forceinline__ void drop_nonfinite(float (&f)[8]) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t m = __float_as_uint(a[e]) & 0x7fffffffu, n = __float_as_uint(b[e]) & 0x7fffffffu;
-        all = max(all, max(m, n));
-        top = max(top, max(m < kInf ? m : 0u, n < kInf ? n : 0u));
-      }
-    }
-  }
-  if (all >= kInf && stores) report(p.dev_err, PKV_DEV_NONFINITE);
-  if (STEP) {
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-  } else {
-    top = __reduce_max_sync(0xffffffffu, top);
-  }
-  if (!is_q && valid && c.blk < 0 && (lane & 7) == 0) report(p.dev_err, PKV_DEV_BAD_BLOCK_ID);
-  const float scale = fmaxf(before, __fdiv_rn(__uint_as_float(top), Code::kMax));
-  const float inv = scale > 0.f ? __fdiv_rn(1.f, scale) : 0.f;
-  if (stores && scale > before && c.r0 > 0) {   // earlier rows of the block, under the grown scale
-    const float ratio = __fdiv_rn(before, scale);
-    for (int r = STEP ? 0 : lane >> 3; r < c.r0; r += STEP ? 1 : 4) {
-      uint4* at = reinterpret_cast<uint4*>(dst + r * row_elems) + (lane & 7);
-      const uint4 w = *at;
-      uint32_t in[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float f[4];
-        Code::decode4(in[e], f);
-        in[e] = Code::encode4(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
-      }
-      *at = make_uint4(in[0], in[1], in[2], in[3]);
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < kRows; ++u) {
-    if (!in_range(u) || !stores) continue;
-    float a[8], b[8];
-    if (!values(u, a, b)) continue;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {   // what is not finite is stored as 0
-      a[e] = fabsf(a[e]) < INFINITY ? a[e] * inv : 0.f;
-      b[e] = fabsf(b[e]) < INFINITY ? b[e] * inv : 0.f;
-    }
-    uint8_t* to = dst + row_of(u) * row_elems;
-    *reinterpret_cast<uint2*>(to + 8 * ch.a) =
-        make_uint2(Code::encode4(a[0], a[1], a[2], a[3]), Code::encode4(a[4], a[5], a[6], a[7]));
-    *reinterpret_cast<uint2*>(to + 8 * ch.b) =
-        make_uint2(Code::encode4(b[0], b[1], b[2], b[3]), Code::encode4(b[4], b[5], b[6], b[7]));
-  }
-  __syncwarp();   // every lane has read the earlier scale
-  if (stores && (STEP ? (lane & 7) == 0 : lane == 0)) *scale_at = scale;
+  for (int e = 0; e < 8; ++e) f[e] = fabsf(f[e]) < INFINITY ? f[e] : 0.f;
 }
 
-// One CTA per (unit, heads), a warp for 4 heads by tokens (side by side where the piece is
-// a single row, in turn otherwise), else for one.
-constexpr int kQ8Warps = 4;
+// codes of a chunk: no value times inv passes the largest code by more than a rounding
+template <class Code>
+__device__ __forceinline__ uint2 code8(const float (&f)[8], float inv) {
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float2 lo = fmul2(make_float2(f[4 * h], f[4 * h + 1]), make_float2(inv, inv));
+    const float2 hi = fmul2(make_float2(f[4 * h + 2], f[4 * h + 3]), make_float2(inv, inv));
+    w[h] = Code::near4(lo, hi);
+  }
+  return make_uint2(w[0], w[1]);
+}
+struct Int8Near : Int8Code {
+  // to the nearest integer, ties to even, by a sum whose last place is 1: its low byte is
+  // the code (9 instructions instead of 24 with conversions and limits)
+  static __device__ __forceinline__ uint32_t near4(float2 a, float2 b) {
+    const auto near = [](float y) { return __float_as_uint(__fadd_rn(y, 12582912.f)); };
+    return __byte_perm(__byte_perm(near(a.x), near(a.y), 0x0040),
+                       __byte_perm(near(b.x), near(b.y), 0x0040), 0x5410);
+  }
+};
+struct E4m3Near : E4m3Code {
+  static __device__ __forceinline__ uint32_t near4(float2 a, float2 b) {
+    return encode4(a.x, a.y, b.x, b.y);
+  }
+};
 
-template <class Code, int BS, bool ADJACENT>
+// 16 codes of a row under a scale that has grown
+template <class Code>
+__device__ __forceinline__ void recode16(uint8_t* at, float ratio) {
+  const uint4 w = *reinterpret_cast<uint4*>(at);
+  uint32_t in[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float f[4];
+    Code::decode4(in[e], f);
+    in[e] = Code::encode4(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
+  }
+  *reinterpret_cast<uint4*>(at) = make_uint4(in[0], in[1], in[2], in[3]);
+}
+
+// Pieces of a single row (a decoded token): each 8 lanes take a head of their own.
+template <class Code, int BS, bool ADJACENT, int AXES>
+__device__ __forceinline__ void append_row(const Q8Params& qp, const Piece& c, int first, int last) {
+  const RowParams& p = qp.r;
+  const int lane = threadIdx.x & 31, token = c.row0 + c.r0;
+  const Chunks ch(lane & 7, p.rot.n);
+  const int64_t row_elems = static_cast<int64_t>(p.num_kv_heads) * kHeadDim;
+  int32_t pos[AXES];
+  load_positions(p.rot, token, c.base + c.r0, pos);
+  const bool ok = on_table(p.rot, pos);
+  if (!ok && lane == 0) report(p.dev_err, PKV_DEV_BAD_POSITION);
+  float4 cs[4];
+  if (ok && ch.turns) load_turn<ADJACENT>(p.rot, ch, pos, cs);
+#pragma unroll 1
+  for (int h0 = first; h0 < last; h0 += 4) {
+    const bool valid = h0 + (lane >> 3) < last && ok;
+    const HeadAt at(qp, c, BS, min(h0 + (lane >> 3), last - 1));
+    const bool stores = valid && !at.is_q && c.blk >= 0;
+    uint4 xa = make_uint4(0u, 0u, 0u, 0u), xb = xa;
+    if (valid) {
+      const uint4* from = reinterpret_cast<const uint4*>(at.src + token * at.stride);
+      xa = from[ch.a];
+      xb = from[ch.b];
+    }
+    const float before = stores && c.r0 > 0 ? *at.scale : 0.f;
+    float a[8], b[8];
+    widen(xa, a);
+    widen(xb, b);
+    if (valid && !at.is_v && ch.turns) rotate<ADJACENT>(a, b, cs);
+    if (valid && at.is_q) {
+      uint4* to = reinterpret_cast<uint4*>(p.q_out + token * p.q_out_stride + at.g * kHeadDim);
+      to[ch.a] = narrow(a);
+      to[ch.b] = narrow(b);
+    }
+    uint32_t top = __float_as_uint(top_of(top_of(0.f, a), b));
+    if (__any_sync(0xffffffffu, stores && top >= kInf)) {
+      if (stores && top >= kInf) report(p.dev_err, PKV_DEV_NONFINITE);
+      drop_nonfinite(a);
+      drop_nonfinite(b);
+      top = __float_as_uint(top_of(top_of(0.f, a), b));
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float scale = fmaxf(before, __fdiv_rn(__uint_as_float(top), Code::kMax));
+    const float inv = scale > 0.f ? __fdiv_rn(1.f, scale) : 0.f;
+    if (stores) {
+      if (scale > before && c.r0 > 0) {   // earlier rows of the block
+        const float ratio = __fdiv_rn(before, scale);
+        for (int r = 0; r < c.r0; ++r) recode16<Code>(at.dst + r * row_elems + 16 * (lane & 7), ratio);
+      }
+      uint8_t* to = at.dst + c.r0 * row_elems;
+      *reinterpret_cast<uint2*>(to + 8 * ch.a) = code8<Code>(a, inv);
+      *reinterpret_cast<uint2*>(to + 8 * ch.b) = code8<Code>(b, inv);
+    }
+    __syncwarp();   // every lane has read the earlier scale
+    if (stores && (lane & 7) == 0) *at.scale = scale;
+  }
+}
+
+// Pieces of several rows: a warp holds 16 rows of the block (8 of 8-row blocks), 4 a
+// pass, and walks the heads, the CTA's rows' cosines and sines in shared memory.  A block of
+// 32 or 64 rows is a team of 2 or 4 warps, which join their maxima.  The rotated values stay
+// in 32 bits from the maximum to the codes, while the next head's rows are under way.
+constexpr int kQ8Warps = 4;
+constexpr int kWarpRows = 16;
+
+// The rows' cosines and sines in shared memory: 8 lanes of a row read a 16-byte chunk each at
+// a time, chunk i of the 4 of lane c lying at i XOR (c / 2), in 8 different banks.
+__device__ __forceinline__ int turn_at(int row, int c, int i) { return (row * 8 + c) * 4 + (i ^ (c >> 1)); }
+
+template <class Code, int BS, bool ADJACENT, int AXES>
+__device__ __forceinline__ void append_rows(const Q8Params& qp, const Piece& c, int first, int last,
+                                            uint32_t (&tops)[2][kQ8Warps], float4 (&table)[BS * 32]) {
+  constexpr int kRows = BS < kWarpRows ? BS : kWarpRows, kPass = kRows / 4;
+  constexpr int kTeam = BS / kRows, kTeams = kQ8Warps / kTeam;
+  const RowParams& p = qp.r;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int team = warp / kTeam, own = kRows * (warp % kTeam) + (lane >> 3);
+  const Chunks ch(lane & 7, p.rot.n);
+  const int64_t row_elems = static_cast<int64_t>(p.num_kv_heads) * kHeadDim;
+
+  uint4 xa[kPass], xb[kPass];
+  const auto load = [&](int head) {
+    const HeadAt at(qp, c, BS, head);
+#pragma unroll
+    for (int u = 0; u < kPass; ++u) {
+      const int r = own + 4 * u;
+      xa[u] = xb[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (r >= c.r0 && r < c.r1) {
+        const uint4* from = reinterpret_cast<const uint4*>(at.src + (c.row0 + r) * at.stride);
+        xa[u] = from[ch.a];
+        xb[u] = from[ch.b];
+      }
+    }
+  };
+  int head = first + team;
+  if (head < last) load(head);
+  // bit u: the pass's row is one of the piece and has a place in the table
+  uint32_t in = 0;
+#pragma unroll 1
+  for (int r = threadIdx.x >> 3; r < BS; r += kQ8Warps * 4) {
+    int32_t pos[AXES];
+    bool ok = false;
+    if (r >= c.r0 && r < c.r1) {
+      load_positions(p.rot, c.row0 + r, c.base + r, pos);
+      ok = on_table(p.rot, pos);
+    }
+    if (r >= c.r0 && r < c.r1 && !ok) report(p.dev_err, PKV_DEV_BAD_POSITION);
+    if (ok && ch.turns) {
+      float4 cs[4];
+      load_turn<ADJACENT>(p.rot, ch, pos, cs);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) table[turn_at(r, lane & 7, i)] = cs[i];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kPass; ++u) {
+    const int r = own + 4 * u;
+    if (r >= c.r0 && r < c.r1) {
+      int32_t pos[AXES];
+      load_positions(p.rot, c.row0 + r, c.base + r, pos);
+      if (on_table(p.rot, pos)) in |= 1u << u;
+    }
+  }
+  __syncthreads();
+  int turns = 0;               // of the team's exchange
+  const auto join = [&](uint32_t top) {
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (kTeam > 1) {
+      if (lane == 0) tops[turns & 1][warp] = top;
+      asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(kTeam * 32) : "memory");
+#pragma unroll
+      for (int w = 0; w < kTeam; ++w) top = max(top, tops[turns & 1][team * kTeam + w]);
+      ++turns;
+    }
+    return top;
+  };
+#pragma unroll 1
+  for (; head < last; head += kTeams) {
+    const HeadAt at(qp, c, BS, head);
+    const bool stores = !at.is_q && c.blk >= 0;
+    const float before = stores && c.r0 > 0 ? *at.scale : 0.f;
+    float a[kPass][8], b[kPass][8];
+#pragma unroll
+    for (int u = 0; u < kPass; ++u) {
+      widen(xa[u], a[u]);
+      widen(xb[u], b[u]);
+    }
+    if (head + kTeams < last) load(head + kTeams);
+    if (!at.is_v && ch.turns)
+#pragma unroll
+      for (int u = 0; u < kPass; ++u) {
+        if (!(in >> u & 1)) continue;
+        float4 cs[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cs[i] = table[turn_at(own + 4 * u, lane & 7, i)];
+        rotate<ADJACENT>(a[u], b[u], cs);
+      }
+    if (at.is_q) {
+#pragma unroll
+      for (int u = 0; u < kPass; ++u) {
+        if (!(in >> u & 1)) continue;
+        uint4* to = reinterpret_cast<uint4*>(p.q_out + (c.row0 + own + 4 * u) * p.q_out_stride +
+                                             at.g * kHeadDim);
+        to[ch.a] = narrow(a[u]);
+        to[ch.b] = narrow(b[u]);
+      }
+      continue;
+    }
+    if (!stores) continue;
+    const auto largest = [&]() {
+      float m = 0.f;
+#pragma unroll
+      for (int u = 0; u < kPass; ++u)
+        if (in >> u & 1) m = top_of(top_of(m, a[u]), b[u]);
+      return join(__float_as_uint(m));
+    };
+    uint32_t top = largest();
+    if (top >= kInf) {
+      if (lane == 0) report(p.dev_err, PKV_DEV_NONFINITE);
+#pragma unroll
+      for (int u = 0; u < kPass; ++u) {
+        drop_nonfinite(a[u]);
+        drop_nonfinite(b[u]);
+      }
+      top = largest();
+    }
+    const float scale = fmaxf(before, __fdiv_rn(__uint_as_float(top), Code::kMax));
+    const float inv = scale > 0.f ? __fdiv_rn(1.f, scale) : 0.f;
+    if (scale > before && c.r0 > 0) {   // earlier rows of the block, under the grown scale
+      const float ratio = __fdiv_rn(before, scale);
+      for (int r = own; r < min(c.r0, kRows * (warp % kTeam) + kRows); r += 4)
+        recode16<Code>(at.dst + r * row_elems + 16 * (lane & 7), ratio);
+    }
+#pragma unroll
+    for (int u = 0; u < kPass; ++u) {
+      if (!(in >> u & 1)) continue;
+      uint8_t* to = at.dst + (own + 4 * u) * row_elems;
+      *reinterpret_cast<uint2*>(to + 8 * ch.a) = code8<Code>(a[u], inv);
+      *reinterpret_cast<uint2*>(to + 8 * ch.b) = code8<Code>(b[u], inv);
+    }
+    __syncwarp();   // every lane has read the earlier scale (every warp, before they joined)
+    if (lane == 0 && warp % kTeam == 0) *at.scale = scale;
+  }
+}
+
+// One CTA per (unit, range of heads).
+template <class Code, int BS, bool ADJACENT, int AXES>
 __global__ void __launch_bounds__(kQ8Warps * 32) rope_q8_kernel(const Q8Params qp) {
   const RowParams& p = qp.r;
+  __shared__ uint32_t tops[2][kQ8Warps];
+  __shared__ float4 table[BS * 32];
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (blockIdx.x == 0 && blockIdx.y == 0)   // every entry is looked at once, used or not
@@ -406,21 +601,14 @@ __global__ void __launch_bounds__(kQ8Warps * 32) rope_q8_kernel(const Q8Params q
                  static_cast<int64_t>(p.max_blocks) * BS, p.dev_err, true);
   Piece c;
   if (!find_piece<BS>(qp, c)) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int heads = p.num_q_heads + 2 * p.num_kv_heads;
-  if (!qp.by_token) {
-    const int head = blockIdx.y * kQ8Warps + warp;
-    if (head < heads) append_head<Code, BS, ADJACENT, false>(qp, c, head, true);
-    return;
-  }
-  const int first = (blockIdx.y * kQ8Warps + warp) * 4;
+  if (c.blk < 0 && threadIdx.x == 0) report(p.dev_err, PKV_DEV_BAD_BLOCK_ID);
+  const int first = blockIdx.y * qp.heads_per_cta;
+  const int last = min(first + qp.heads_per_cta, p.num_q_heads + 2 * p.num_kv_heads);
   if (c.r1 - c.r0 == 1) {
-    const int head = first + (lane >> 3);
-    append_head<Code, BS, ADJACENT, true>(qp, c, min(head, heads - 1), head < heads);
+    const int per = qp.heads_per_cta / kQ8Warps, warp = threadIdx.x >> 5;
+    append_row<Code, BS, ADJACENT, AXES>(qp, c, first + warp * per, min(last, first + (warp + 1) * per));
   } else {
-#pragma unroll 1
-    for (int h = first; h < min(first + 4, heads); ++h)
-      append_head<Code, BS, ADJACENT, false>(qp, c, h, true);
+    append_rows<Code, BS, ADJACENT, AXES>(qp, c, first, last, tops, table);
   }
 }
 
@@ -446,19 +634,23 @@ int make_rotation(Rotation* r, const int32_t* positions, int num_axes, const uin
       if (axes[j] >= num_axes) return PKV_ERR_INVALID_ARG;
       r->axis[j >> 4] |= static_cast<uint32_t>(axes[j]) << 2 * (j & 15);
     }
+  r->in_twos = 1;
+  for (int j = 0; axes && j < r->n; j += 2) r->in_twos &= axes[j] == axes[j + 1];
   r->table = table;
   r->positions = positions;
   r->table_rows = table_rows;
   r->num_tokens = num_tokens;
-  // on every axis the place in the sequence: one axis
-  if (!positions) r->num_axes = 1;
+  if (!positions) {   // on every axis the place in the sequence: one axis
+    r->num_axes = r->in_twos = 1;
+    for (uint32_t& w : r->axis) w = 0;
+  }
   return PKV_OK;
 }
 
 bool bad_stride(int64_t stride) { return stride < 0 || stride % 8; }
 
 template <class... P>
-int launch(void (*kernel)(const P...), dim3 grid, int threads, void* stream, const P&... p) {
+int launch(void (*kernel)(P...), dim3 grid, int threads, void* stream, const P&... p) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
@@ -472,25 +664,41 @@ int launch(void (*kernel)(const P...), dim3 grid, int threads, void* stream, con
 }
 
 template <bool CACHE>
-int launch_rows(const RowParams& p, bool adjacent, void* stream) {
-  const int rows = p.num_q_heads + (CACHE ? 2 : 1) * p.num_kv_heads;
-  const int64_t parts = (static_cast<int64_t>(rows) + kPartRows - 1) / kPartRows;
+int launch_rows(RowParams& p, bool adjacent, void* stream) {
+  const int64_t rows = p.num_q_heads + (CACHE ? 2ll : 1ll) * p.num_kv_heads;
+  // parts of even length; shorter ones where they leave SMs with less than 16 warps
+  int64_t parts = (rows + 4 * kPasses - 1) / (4 * kPasses);
+  if (p.num_tokens * parts < 152 * 16) parts = (rows + 7) / 8;
+  p.part_rows = static_cast<int>((rows + 4 * parts - 1) / (4 * parts) * 4);
+  parts = (rows + p.part_rows - 1) / p.part_rows;
   if (parts > 65535) return PKV_ERR_UNSUPPORTED;
   const dim3 grid((static_cast<unsigned>(p.num_tokens) + kRowWarps - 1) / kRowWarps,
                   static_cast<unsigned>(parts));
-  return adjacent ? launch(rope_rows_kernel<CACHE, true>, grid, kRowWarps * 32, stream, p)
-                  : launch(rope_rows_kernel<CACHE, false>, grid, kRowWarps * 32, stream, p);
+  const auto go = [&](auto kernel) { return launch(kernel, grid, kRowWarps * 32, stream, p); };
+  if (p.rot.num_axes == 1)
+    return adjacent ? go(rope_rows_kernel<CACHE, true, 1>) : go(rope_rows_kernel<CACHE, false, 1>);
+  return adjacent ? go(rope_rows_kernel<CACHE, true, kMaxAxes>)
+                  : go(rope_rows_kernel<CACHE, false, kMaxAxes>);
 }
 
-template <class Code, bool ADJACENT>
+template <class Code, bool ADJACENT, int AXES>
 int launch_q8(const Q8Params& p, int block_size, dim3 grid, void* stream) {
-  constexpr int kThreads = kQ8Warps * 32;
+  const auto go = [&](auto kernel) { return launch(kernel, grid, kQ8Warps * 32, stream, p); };
   switch (block_size) {
-    case 8: return launch(rope_q8_kernel<Code, 8, ADJACENT>, grid, kThreads, stream, p);
-    case 16: return launch(rope_q8_kernel<Code, 16, ADJACENT>, grid, kThreads, stream, p);
-    case 32: return launch(rope_q8_kernel<Code, 32, ADJACENT>, grid, kThreads, stream, p);
-    default: return launch(rope_q8_kernel<Code, 64, ADJACENT>, grid, kThreads, stream, p);
+    case 8: return go(rope_q8_kernel<Code, 8, ADJACENT, AXES>);
+    case 16: return go(rope_q8_kernel<Code, 16, ADJACENT, AXES>);
+    case 32: return go(rope_q8_kernel<Code, 32, ADJACENT, AXES>);
+    default: return go(rope_q8_kernel<Code, 64, ADJACENT, AXES>);
   }
+}
+
+template <class Code>
+int launch_q8(const Q8Params& p, bool adjacent, int block_size, dim3 grid, void* stream) {
+  if (p.r.rot.num_axes == 1)
+    return adjacent ? launch_q8<Code, true, 1>(p, block_size, grid, stream)
+                    : launch_q8<Code, false, 1>(p, block_size, grid, stream);
+  return adjacent ? launch_q8<Code, true, kMaxAxes>(p, block_size, grid, stream)
+                  : launch_q8<Code, false, kMaxAxes>(p, block_size, grid, stream);
 }
 
 }  // namespace rope
@@ -653,12 +861,15 @@ extern "C" int pkv_rope_and_cache_q8(void* q_out, const void* q, const void* k, 
   const int64_t heads = num_q_heads + 2ll * num_kv_heads;
   const int64_t units = p.by_token ? num_tokens
                                    : static_cast<int64_t>(num_tokens) / block_size + 2ll * num_seqs;
-  const int64_t per = p.by_token ? 4 * kQ8Warps : kQ8Warps;
+  // a step's heads are spread over as many warps as there are; a prompt's stay together, as
+  // they share cosines and sines, while there are some rounds of CTAs
+  constexpr int64_t kLeast = 4 * kQ8Warps, kRounds = 152 * 3 * 4;
+  int64_t per = kLeast;
+  if (!p.by_token) per = std::max(per, heads * units / kRounds / kLeast * kLeast);
+  per = std::min(per, (heads + kLeast - 1) / kLeast * kLeast);
+  p.heads_per_cta = static_cast<int>(per);
   if (units > INT32_MAX || (heads + per - 1) / per > 65535) return PKV_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(units), static_cast<unsigned>((heads + per - 1) / per));
-  if (code == PKV_CODE_INT8)
-    return adjacent ? launch_q8<pkv::Int8Code, true>(p, block_size, grid, stream)
-                    : launch_q8<pkv::Int8Code, false>(p, block_size, grid, stream);
-  return adjacent ? launch_q8<pkv::E4m3Code, true>(p, block_size, grid, stream)
-                  : launch_q8<pkv::E4m3Code, false>(p, block_size, grid, stream);
+  return code == PKV_CODE_INT8 ? launch_q8<Int8Near>(p, adjacent != 0, block_size, grid, stream)
+                               : launch_q8<E4m3Near>(p, adjacent != 0, block_size, grid, stream);
 }
