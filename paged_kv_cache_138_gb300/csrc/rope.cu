@@ -335,6 +335,10 @@ __device__ __forceinline__ float top_of(float m, const float (&f)[8]) {
     asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(f[e]), "f"(f[e + 1]));
   return m;
 }
+__device__ __forceinline__ float top2(float a, float b) {
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(a), "f"(b));
+  return a;
+}
 __device__ __forceinline__ void drop_nonfinite(float (&f)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) f[e] = fabsf(f[e]) < INFINITY ? f[e] : 0.f;
@@ -441,15 +445,28 @@ __device__ __forceinline__ void append_row(const Q8Params& qp, const Piece& c, i
 }
 
 // Pieces of several rows: a warp holds 16 rows of the block (8 of 8-row blocks), 4 a
-// pass, and walks the heads, the CTA's rows' cosines and sines in shared memory.  A block of
-// 32 or 64 rows is a team of 2 or 4 warps, which join their maxima.  The rotated values stay
-// in 32 bits from the maximum to the codes, while the next head's rows are under way.
+// pass, and walks the heads, the CTA's rows' cosines and sines in shared memory (read again
+// for every head from L1, strided, they bounded the kernel: prompts 203 us instead of 110).  A
+// block of 32 or 64 rows is a team of 2 or 4 warps, which join their maxima.  The rotated
+// values stay in 32 bits from the maximum to the codes, while the next head's rows are under
+// way; computed twice instead, at 96 registers, they took 10 to 20 % longer.  Four CTAs an SM
+// (128 registers) for teams, three (0: left to the compiler) where a warp is alone and keeps its cosines in
+// registers: 32-token blocks 48 us (three CTAs: 54), 16-token blocks 110 us (four: 113).
 constexpr int kQ8Warps = 4;
 constexpr int kWarpRows = 16;
 
 // The rows' cosines and sines in shared memory: 8 lanes of a row read a 16-byte chunk each at
 // a time, chunk i of the 4 of lane c lying at i XOR (c / 2), in 8 different banks.
 __device__ __forceinline__ int turn_at(int row, int c, int i) { return (row * 8 + c) * 4 + (i ^ (c >> 1)); }
+
+// read where it is used: as a loop invariant it would take 64 registers
+__device__ __forceinline__ float4 read_turn(const float4* at) {
+  float4 w;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(w.x), "=f"(w.y), "=f"(w.z), "=f"(w.w)
+               : "r"(smem_u32(at)));
+  return w;
+}
 
 template <class Code, int BS, bool ADJACENT, int AXES>
 __device__ __forceinline__ void append_rows(const Q8Params& qp, const Piece& c, int first, int last,
@@ -462,40 +479,8 @@ __device__ __forceinline__ void append_rows(const Q8Params& qp, const Piece& c, 
   const Chunks ch(lane & 7, p.rot.n);
   const int64_t row_elems = static_cast<int64_t>(p.num_kv_heads) * kHeadDim;
 
-  uint4 xa[kPass], xb[kPass];
-  const auto load = [&](int head) {
-    const HeadAt at(qp, c, BS, head);
-#pragma unroll
-    for (int u = 0; u < kPass; ++u) {
-      const int r = own + 4 * u;
-      xa[u] = xb[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (r >= c.r0 && r < c.r1) {
-        const uint4* from = reinterpret_cast<const uint4*>(at.src + (c.row0 + r) * at.stride);
-        xa[u] = from[ch.a];
-        xb[u] = from[ch.b];
-      }
-    }
-  };
-  int head = first + team;
-  if (head < last) load(head);
-  // bit u: the pass's row is one of the piece and has a place in the table
+  // bit u: the pass's row is one of the piece and has a place in the table; the others are zeros
   uint32_t in = 0;
-#pragma unroll 1
-  for (int r = threadIdx.x >> 3; r < BS; r += kQ8Warps * 4) {
-    int32_t pos[AXES];
-    bool ok = false;
-    if (r >= c.r0 && r < c.r1) {
-      load_positions(p.rot, c.row0 + r, c.base + r, pos);
-      ok = on_table(p.rot, pos);
-    }
-    if (r >= c.r0 && r < c.r1 && !ok) report(p.dev_err, PKV_DEV_BAD_POSITION);
-    if (ok && ch.turns) {
-      float4 cs[4];
-      load_turn<ADJACENT>(p.rot, ch, pos, cs);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) table[turn_at(r, lane & 7, i)] = cs[i];
-    }
-  }
 #pragma unroll
   for (int u = 0; u < kPass; ++u) {
     const int r = own + 4 * u;
@@ -503,6 +488,35 @@ __device__ __forceinline__ void append_rows(const Q8Params& qp, const Piece& c, 
       int32_t pos[AXES];
       load_positions(p.rot, c.row0 + r, c.base + r, pos);
       if (on_table(p.rot, pos)) in |= 1u << u;
+    }
+  }
+  uint4 xa[kPass], xb[kPass];
+  const auto load = [&](const HeadAt& at) {
+    const __half* row = at.src + (c.row0 + own) * at.stride;
+#pragma unroll
+    for (int u = 0; u < kPass; ++u, row += 4 * at.stride) {
+      xa[u] = xb[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (in >> u & 1) {
+        xa[u] = reinterpret_cast<const uint4*>(row)[ch.a];
+        xb[u] = reinterpret_cast<const uint4*>(row)[ch.b];
+      }
+    }
+  };
+  int head = first + team;
+  HeadAt next(qp, c, BS, min(head, last - 1));
+  if (head < last) load(next);
+#pragma unroll 1
+  for (int r = threadIdx.x >> 3; r < BS; r += kQ8Warps * 4) {
+    if (r < c.r0 || r >= c.r1) continue;
+    int32_t pos[AXES];
+    load_positions(p.rot, c.row0 + r, c.base + r, pos);
+    if (!on_table(p.rot, pos)) {
+      report(p.dev_err, PKV_DEV_BAD_POSITION);
+    } else if (ch.turns) {
+      float4 cs[4];
+      load_turn<ADJACENT>(p.rot, ch, pos, cs);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) table[turn_at(r, lane & 7, i)] = cs[i];
     }
   }
   __syncthreads();
@@ -520,7 +534,7 @@ __device__ __forceinline__ void append_rows(const Q8Params& qp, const Piece& c, 
   };
 #pragma unroll 1
   for (; head < last; head += kTeams) {
-    const HeadAt at(qp, c, BS, head);
+    const HeadAt at = next;
     const bool stores = !at.is_q && c.blk >= 0;
     const float before = stores && c.r0 > 0 ? *at.scale : 0.f;
     float a[kPass][8], b[kPass][8];
@@ -529,24 +543,30 @@ __device__ __forceinline__ void append_rows(const Q8Params& qp, const Piece& c, 
       widen(xa[u], a[u]);
       widen(xb[u], b[u]);
     }
-    if (head + kTeams < last) load(head + kTeams);
+    if (head + kTeams < last) {
+      next = HeadAt(qp, c, BS, head + kTeams);
+      load(next);
+    }
     if (!at.is_v && ch.turns)
 #pragma unroll
-      for (int u = 0; u < kPass; ++u) {
-        if (!(in >> u & 1)) continue;
+      for (int u = 0; u < kPass; ++u) {   // rows that are not in hold zeros, whatever turns them
         float4 cs[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) cs[i] = table[turn_at(own + 4 * u, lane & 7, i)];
+        for (int i = 0; i < 4; ++i) {
+          const float4* from = table + turn_at(own + 4 * u, lane & 7, i);
+          cs[i] = kTeam > 1 ? read_turn(from) : *from;
+        }
         rotate<ADJACENT>(a[u], b[u], cs);
       }
     if (at.is_q) {
+      __half* out = p.q_out + (c.row0 + own) * p.q_out_stride + at.g * kHeadDim;
 #pragma unroll
-      for (int u = 0; u < kPass; ++u) {
-        if (!(in >> u & 1)) continue;
-        uint4* to = reinterpret_cast<uint4*>(p.q_out + (c.row0 + own + 4 * u) * p.q_out_stride +
-                                             at.g * kHeadDim);
-        to[ch.a] = narrow(a[u]);
-        to[ch.b] = narrow(b[u]);
+      for (int u = 0; u < kPass; ++u, out += 4 * p.q_out_stride) {
+        const uint4 ya = narrow(a[u]), yb = narrow(b[u]);
+        if (in >> u & 1) {
+          reinterpret_cast<uint4*>(out)[ch.a] = ya;
+          reinterpret_cast<uint4*>(out)[ch.b] = yb;
+        }
       }
       continue;
     }
@@ -554,8 +574,10 @@ __device__ __forceinline__ void append_rows(const Q8Params& qp, const Piece& c, 
     const auto largest = [&]() {
       float m = 0.f;
 #pragma unroll
-      for (int u = 0; u < kPass; ++u)
-        if (in >> u & 1) m = top_of(top_of(m, a[u]), b[u]);
+      for (int u = 0; u < kPass; ++u) {
+        const float t = top_of(top_of(0.f, a[u]), b[u]);
+        if (in >> u & 1) m = top2(m, t);
+      }
       return join(__float_as_uint(m));
     };
     uint32_t top = largest();
@@ -575,12 +597,14 @@ __device__ __forceinline__ void append_rows(const Q8Params& qp, const Piece& c, 
       for (int r = own; r < min(c.r0, kRows * (warp % kTeam) + kRows); r += 4)
         recode16<Code>(at.dst + r * row_elems + 16 * (lane & 7), ratio);
     }
+    uint8_t* to = at.dst + own * row_elems;
 #pragma unroll
-    for (int u = 0; u < kPass; ++u) {
-      if (!(in >> u & 1)) continue;
-      uint8_t* to = at.dst + (own + 4 * u) * row_elems;
-      *reinterpret_cast<uint2*>(to + 8 * ch.a) = code8<Code>(a[u], inv);
-      *reinterpret_cast<uint2*>(to + 8 * ch.b) = code8<Code>(b[u], inv);
+    for (int u = 0; u < kPass; ++u, to += 4 * row_elems) {
+      const uint2 ya = code8<Code>(a[u], inv), yb = code8<Code>(b[u], inv);
+      if (in >> u & 1) {
+        *reinterpret_cast<uint2*>(to + 8 * ch.a) = ya;
+        *reinterpret_cast<uint2*>(to + 8 * ch.b) = yb;
+      }
     }
     __syncwarp();   // every lane has read the earlier scale (every warp, before they joined)
     if (lane == 0 && warp % kTeam == 0) *at.scale = scale;
@@ -589,7 +613,7 @@ __device__ __forceinline__ void append_rows(const Q8Params& qp, const Piece& c, 
 
 // One CTA per (unit, range of heads).
 template <class Code, int BS, bool ADJACENT, int AXES>
-__global__ void __launch_bounds__(kQ8Warps * 32) rope_q8_kernel(const Q8Params qp) {
+__global__ void __launch_bounds__(kQ8Warps * 32, BS > 16 ? 4 : 0) rope_q8_kernel(const Q8Params qp) {
   const RowParams& p = qp.r;
   __shared__ uint32_t tops[2][kQ8Warps];
   __shared__ float4 table[BS * 32];
@@ -862,11 +886,11 @@ extern "C" int pkv_rope_and_cache_q8(void* q_out, const void* q, const void* k, 
   const int64_t units = p.by_token ? num_tokens
                                    : static_cast<int64_t>(num_tokens) / block_size + 2ll * num_seqs;
   // a step's heads are spread over as many warps as there are; a prompt's stay together, as
-  // they share cosines and sines, while there are some rounds of CTAs
-  constexpr int64_t kLeast = 4 * kQ8Warps, kRounds = 152 * 3 * 4;
-  int64_t per = kLeast;
-  if (!p.by_token) per = std::max(per, heads * units / kRounds / kLeast * kLeast);
-  per = std::min(per, (heads + kLeast - 1) / kLeast * kLeast);
+  // they share cosines and sines, as long as there are two rounds of CTAs (four are 3 to 6 %
+  // slower on prompts of 32/8 and 32/32 heads)
+  constexpr int64_t kLeast = 4 * kQ8Warps, kRounds = 152 * 4 * 2;
+  const int64_t parts = p.by_token ? heads : (kRounds + units - 1) / units;
+  const int64_t per = std::max(kLeast, (heads + parts * kLeast - 1) / (parts * kLeast) * kLeast);
   p.heads_per_cta = static_cast<int>(per);
   if (units > INT32_MAX || (heads + per - 1) / per > 65535) return PKV_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(units), static_cast<unsigned>((heads + per - 1) / per));
