@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // One warp brings Q, K and the scales of both, one V: both count through the whole
       // sequence.
       const int mine = warp == kCopyVWarp;
-      constexpr int kBoxes = kTile / BS;
+      constexpr int kBoxes = kTile / BS, kBatch = 32 / kBoxes;
       uint32_t base = 0, tiles = 0;           // the unit's first place in the ring, its first tile
       uint32_t q_seen = 0, q_parity = 0;      // bit x: Q copies of tile x so far
       uint32_t raw_seen = 0, raw_parity = 0;  // bit st: this warp's copies into a stage
@@ -231,11 +231,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       Unit u;
       for (int k = 0; ok && next_unit(k, u); ++k) {
         const int n = u.last - u.begin;
-        // the block id of this lane's part of tile j, loaded two tiles ahead, and its scales,
-        // loaded one ahead; -1 past the context
-        const auto id_of = [&](int j) {
-          const int tok = j * kTile + lane * BS;
-          return lane < kBoxes && j >= u.begin && tok < u.ctx
+        // Block ids and scales come a batch of 32 boxes at a time (a box a lane), ids two
+        // batches ahead and scales one: loaded tile by tile, one ahead, their latency was the
+        // time of a tile (3100 cycles with few rows).
+        const auto ids_of = [&](int b) {   // -1 past the context
+          const int i = b * kBatch + lane / kBoxes;
+          const int tok = (u.last - 1 - i) * kTile + lane % kBoxes * BS;
+          return i < n && tok < u.ctx
                      ? __ldg(p.block_tables + static_cast<int64_t>(u.s) * p.max_blocks + tok / BS)
                      : -1;
         };
@@ -244,13 +246,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int64_t at = static_cast<int64_t>(id) * qp.scale_stride + u.g;
           return make_float2(__ldg(qp.k_scale + at), __ldg(qp.v_scale + at));
         };
-        int32_t id = id_of(u.last - 1), id1 = id_of(u.last - 2);
-        float2 sc = scales_of(id);
+        int32_t ids = ids_of(0), ids1 = ids_of(1), ids2 = -1;
+        float2 scs = scales_of(ids), scs1 = make_float2(0.f, 0.f);
 #pragma unroll 1
         for (int i = 0; i < n && ok; ++i) {
-          const int j = u.last - 1 - i;
-          const int32_t id2 = id_of(j - 2);
-          const float2 sc1 = scales_of(id1);
+          const int j = u.last - 1 - i, in_batch = i % kBatch;
+          if (in_batch == 0) {
+            if (i > 0) {
+              ids = ids1;
+              ids1 = ids2;
+              scs = scs1;
+            }
+            ids2 = ids_of(i / kBatch + 2);
+            scs1 = scales_of(ids1);
+          }
+          // this lane's box of the tile
+          const int32_t id = __shfl_sync(kFull, ids, in_batch * kBoxes + lane % kBoxes);
           // where the tile's K or V comes in the ring (see CopyAt)
           const int at = !u.pair ? 2 * i + mine
                          : mine  ? (i + 1 < n ? 2 * i + 2 : 2 * n - 1)
@@ -272,12 +283,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane < kBoxes)
             tma_load_3d(dst + lane * (kRawBytes / kBoxes), mine ? &tmap_v : &tmap_k, 0, u.g, row, b);
           if (!mine) {
+            const float k_sc = __shfl_sync(kFull, scs.x, in_batch * kBoxes + lane % kBoxes);
+            const float v_sc = __shfl_sync(kFull, scs.y, in_batch * kBoxes + lane % kBoxes);
             if (lane < kBoxes) {
               // a factor of 0 would turn a masked -infinity into a NaN (a scale that is
               // not a number stays one)
-              const float f = sc.x * p.scale_log2, v = fmaxf(sc.y, kLeastScale);
+              const float f = k_sc * p.scale_log2, v = fmaxf(v_sc, kLeastScale);
               const float kf = f < 1e-30f ? 1e-30f : f;
-              const float lv = sc.y <= kLeastScale ? kLeastLog : __log2f(v), inv = __frcp_rn(v);
+              const float lv = v_sc <= kLeastScale ? kLeastLog : __log2f(v), inv = __frcp_rn(v);
               float* to = scales_at(tiles + i);
 #pragma unroll
               for (int e = 0; e < BS / Sc::gran; ++e) {
@@ -290,9 +303,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(Smem::sc_full, (tiles + i) & (kSlots - 1)));
           }
-          id = id1;
-          id1 = id2;
-          sc = sc1;
           if (i == 0 && !mine) {
 #pragma unroll 1
             for (int x = 0; x < 2 && ok; ++x) {

@@ -843,41 +843,38 @@ def _rows_of(t, name, dev):
 def _rope_args(table, positions, axes, T, dev, required):
     """(positions, num_axes, axes, table, table rows, rot_dim) as the C calls take them."""
     try:
-        good = (table.dtype is _F32 and table.get_device() == dev and table.is_contiguous() and
-                table.dim() == 3)
-    except (AttributeError, RuntimeError):
+        rows, n, two = table.shape
+        good = (table.dtype is _F32 and table.get_device() == dev and table.is_contiguous())
+    except (AttributeError, RuntimeError, ValueError):
         good = False
     if not good:
         _explain((table, "table", _F32, 3))
-    rows, n, two = table.shape
     if two != 2:
         raise ValueError("table must be [positions, pairs, 2]")
-    num = 1
     if positions is None:
         if required:
             raise TypeError("positions must be a CUDA tensor")
-        if axes is not None:
-            axes = _pack_axes(tuple(axes), n, 4)
-            num = 4
-    else:
-        try:
-            good = (positions.dtype is _I32 and positions.get_device() == dev and
-                    positions.is_contiguous() and 1 <= positions.dim() <= 2)
-        except (AttributeError, RuntimeError):
-            good = False
-        if not good:
-            _explain((positions, "positions", _I32, 2 if getattr(positions, "ndim", 1) > 1 else 1))
+        if axes is None:
+            return None, 1, None, table.data_ptr(), rows, 2 * n
+        return None, 4, _pack_axes(tuple(axes), n, 4), table.data_ptr(), rows, 2 * n
+    try:
+        good = (positions.dtype is _I32 and positions.get_device() == dev and
+                positions.is_contiguous())
         shape = positions.shape
-        if shape[-1] != T:
-            raise ValueError("positions must have one entry for each token")
-        num = shape[0] if len(shape) == 2 else 1
-        if not 1 <= num <= 4:
-            raise ValueError("positions must have 1 to 4 axes")
-        if axes is not None:
-            axes = _pack_axes(tuple(axes), n, num)
-        elif num > 1:
-            raise ValueError("axes must say which of the %d axes each pair follows" % num)
-    return _ptr(positions), num, axes, table.data_ptr(), rows, 2 * n
+    except (AttributeError, RuntimeError):
+        good = False
+    if not good or not 1 <= len(shape) <= 2:
+        _explain((positions, "positions", _I32, 2 if getattr(positions, "ndim", 1) > 1 else 1))
+    if shape[-1] != T:
+        raise ValueError("positions must have one entry for each token")
+    num = shape[0] if len(shape) == 2 else 1
+    if not 1 <= num <= 4:
+        raise ValueError("positions must have 1 to 4 axes")
+    if axes is not None:
+        axes = _pack_axes(tuple(axes), n, num)
+    elif num > 1:
+        raise ValueError("axes must say which of the %d axes each pair follows" % num)
+    return positions.data_ptr(), num, axes, table.data_ptr(), rows, 2 * n
 
 
 def _check_out_stride(name, T, H, stride):
@@ -893,25 +890,39 @@ def rotary_embedding(q_out, k_out, q, k, positions, table, axes=None, adjacent=F
     of a projection's output, and q_out q, k_out k (in place); k and k_out may be None.
     prepare=True returns a PreparedLaunch instead of launching."""
     dev = _get_device()
-    T, Hq, sq = _rows_of(q, "q", dev)
-    To, Ho, so = _rows_of(q_out, "q_out", dev)
-    Hkv = sk = sko = 0
-    if (k is None) != (k_out is None):
-        raise TypeError("k and k_out go together")
-    if k is not None:
-        Tk, Hkv, sk = _rows_of(k, "k", dev)
-        Tko, Hko, sko = _rows_of(k_out, "k_out", dev)
-        if Tk != T or Tko != T or Hko != Hkv:
+    try:
+        T, Hq, D = shape = q.shape
+        Tk, Hkv, Dk = shape_k = k.shape
+        (so, a, b), (sq, c, d) = q_out.stride(), q.stride()
+        (sko, e, f), (sk, g, h) = k_out.stride(), k.stride()
+        good = (q.dtype is _F16 and q_out.dtype is _F16 and k.dtype is _F16 and
+                k_out.dtype is _F16 and q.get_device() == dev and q_out.get_device() == dev and
+                k.get_device() == dev and k_out.get_device() == dev and
+                q_out.shape == shape and k_out.shape == shape_k and Tk == T and
+                D == Dk == a == c == e == g == 128 and b == d == f == h == 1 and
+                not (so | sq | sko | sk) & 7)
+    except (AttributeError, RuntimeError, ValueError):
+        good = False
+    if not good:      # what is wrong, or a shape of one token or head with other strides
+        T, Hq, sq = _rows_of(q, "q", dev)
+        To, Ho, so = _rows_of(q_out, "q_out", dev)
+        Hkv = sk = sko = 0
+        if (k is None) != (k_out is None):
+            raise TypeError("k and k_out go together")
+        if k is not None:
+            Tk, Hkv, sk = _rows_of(k, "k", dev)
+            Tko, Hko, sko = _rows_of(k_out, "k_out", dev)
+            if Tk != T or Tko != T or Hko != Hkv:
+                raise ValueError("shape mismatch")
+        if To != T or Ho != Hq:
             raise ValueError("shape mismatch")
-        _check_out_stride("k_out", T, Hkv, sko)
-    if To != T or Ho != Hq:
-        raise ValueError("shape mismatch")
     _check_out_stride("q_out", T, Hq, so)
+    _check_out_stride("k_out", T, Hkv, sko)
     rot = _rope_args(table, positions, axes, T, dev, True)
     if dev_err is not None:
         _check_side(None, dev_err)
     args = (q_out.data_ptr(), _ptr(k_out), q.data_ptr(), _ptr(k), so, sko, sq, sk, *rot,
-            int(bool(adjacent)), T, Hq, Hkv, HEAD_DIM, _ptr(dev_err), _stream_handle(stream))
+            1 if adjacent else 0, T, Hq, Hkv, HEAD_DIM, _ptr(dev_err), _stream_handle(stream))
     keep = (q_out, k_out, q, k, positions, table, dev_err, stream) if prepare else None
     return _run(lib().pkv_rotary_embedding, args, "rotary_embedding", prepare, keep, None)
 
@@ -919,25 +930,37 @@ def rotary_embedding(q_out, k_out, q, k, positions, table, axes=None, adjacent=F
 def _append_args(q_out, q, k, v, query_start, block_tables, context_lens, table, positions, axes):
     """What both caches' calls share: sizes (T, S, Hq, Hkv, max_blocks), strides, rotation."""
     dev = _get_device()
-    T, Hq, sq = _rows_of(q, "q", dev)
-    To, Ho, so = _rows_of(q_out, "q_out", dev)
-    Tk, Hkv, sk = _rows_of(k, "k", dev)
-    Tv, Hv, sv = _rows_of(v, "v", dev)
     try:
-        good = (query_start.dtype is _I32 and query_start.get_device() == dev and
+        T, Hq, D = shape = q.shape
+        Tk, Hkv, Dk = shape_k = k.shape
+        S, max_blocks = block_tables.shape
+        (so, a, b), (sq, c, d) = q_out.stride(), q.stride()
+        (sk, e, f), (sv, g, h) = k.stride(), v.stride()
+        good = (q.dtype is _F16 and q_out.dtype is _F16 and k.dtype is _F16 and v.dtype is _F16 and
+                q.get_device() == dev and q_out.get_device() == dev and k.get_device() == dev and
+                v.get_device() == dev and q_out.shape == shape and v.shape == shape_k and
+                Tk == T and D == Dk == a == c == e == g == 128 and b == d == f == h == 1 and
+                not (so | sq | sk | sv) & 7 and
+                query_start.dtype is _I32 and query_start.get_device() == dev and
                 query_start.is_contiguous() and
                 block_tables.dtype is _I32 and block_tables.get_device() == dev and
                 block_tables.is_contiguous() and
                 context_lens.dtype is _I32 and context_lens.get_device() == dev and
-                context_lens.is_contiguous() and block_tables.dim() == 2)
-    except (AttributeError, RuntimeError):
+                context_lens.is_contiguous())
+    except (AttributeError, RuntimeError, ValueError, TypeError):
         good = False
-    if not good:
-        _explain((query_start, "query_start", _I32, 1), (block_tables, "block_tables", _I32, 2),
-                 (context_lens, "context_lens", _I32, 1))
-    S, max_blocks = block_tables.shape
-    if To != T or Tk != T or Tv != T or Ho != Hq or Hv != Hkv:
-        raise ValueError("shape mismatch")
+    if not good:      # what is wrong, or a shape of one token or head with other strides
+        T, Hq, sq = _rows_of(q, "q", dev)
+        To, Ho, so = _rows_of(q_out, "q_out", dev)
+        Tk, Hkv, sk = _rows_of(k, "k", dev)
+        Tv, Hv, sv = _rows_of(v, "v", dev)
+        for t, name, dim in ((query_start, "query_start", 1), (block_tables, "block_tables", 2),
+                             (context_lens, "context_lens", 1)):
+            if _dev(t, name, _I32, dim).get_device() != dev:
+                raise ValueError("%s must be on the current CUDA device" % name)
+        if To != T or Tk != T or Tv != T or Ho != Hq or Hv != Hkv:
+            raise ValueError("shape mismatch")
+        S, max_blocks = block_tables.shape
     if query_start.shape != (S + 1,) or context_lens.shape != (S,):
         raise ValueError("query_start must have num_seqs + 1 entries, context_lens num_seqs")
     _check_out_stride("q_out", T, Hq, so)
@@ -973,7 +996,7 @@ def rope_and_cache(q_out, q, k, v, query_start, block_tables, context_lens, k_ca
         _check_side(None, dev_err)
     args = (q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides,
             query_start.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
-            k_cache.data_ptr(), v_cache.data_ptr(), *rot, int(bool(adjacent)), T, S, Hq, Hkv, D,
+            k_cache.data_ptr(), v_cache.data_ptr(), *rot, 1 if adjacent else 0, T, S, Hq, Hkv, D,
             bs, nb, max_blocks, _ptr(dev_err), _stream_handle(stream))
     keep = (q_out, q, k, v, query_start, block_tables, context_lens, k_cache, v_cache, table,
             positions, dev_err, stream) if prepare else None
@@ -996,7 +1019,7 @@ def rope_and_cache_q8(q_out, q, k, v, query_start, block_tables, context_lens, k
     args = (q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides,
             query_start.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
             k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), code,
-            *rot, int(bool(adjacent)), T, S, Hq, Hkv, D, bs, nb, max_blocks, stride,
+            *rot, 1 if adjacent else 0, T, S, Hq, Hkv, D, bs, nb, max_blocks, stride,
             _ptr(dev_err), _stream_handle(stream))
     keep = (q_out, q, k, v, query_start, block_tables, context_lens, k_cache, v_cache, k_scale,
             v_scale, table, positions, dev_err, stream) if prepare else None
