@@ -207,9 +207,11 @@ struct alignas(16) Unit {
 };
 static_assert(sizeof(Unit) <= 64 && sizeof(Unit) % 16 == 0, "a unit's place in shared memory");
 
+// TILES: query tiles of a unit, 2, or 1 where units have rows in one tile only
+template <int TILES = 2>
 __device__ __forceinline__ bool make_unit(const Params& p, int bx, int by, int64_t max_context,
                                           Unit& u) {
-  const int per = 2 * kTile >> p.group_shift;   // tokens of a unit
+  const int per = TILES * kTile >> p.group_shift;   // tokens of a unit
   const int units = gridDim.x / p.num_kv_heads;
   // later rows of a prompt see more tokens: start with them
   const int unit = units - 1 - bx / p.num_kv_heads;
@@ -226,10 +228,10 @@ __device__ __forceinline__ bool make_unit(const Params& p, int bx, int by, int64
   if (!q.ok || nth < 0 || static_cast<int64_t>(nth) * per >= q.n) return false;
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
-    u.tok0[x] = nth * per + (1 - x) * (kTile >> p.group_shift);
+    u.tok0[x] = nth * per + (TILES - 1 - x) * (kTile >> p.group_shift);
     const int tok_end = min(q.n, u.tok0[x] + (kTile >> p.group_shift));
     u.end[x] = u.begin;
-    if (tok_end > u.tok0[x]) {
+    if (tok_end > u.tok0[x] && x < TILES) {
       const int last_pos = q.ctx - q.n + tok_end - 1;
       u.end[x] = max(u.begin, min(u.begin + p.split_tiles, last_pos / kTile + 1));
     }
@@ -296,8 +298,8 @@ constexpr int kMinSplitTiles = 8;
 // limit.  128 tokens take 2300 cycles, 3100 in the slowest unit (one tile alone, see Unit).
 constexpr int64_t kMaxContext = 1 << 25;
 static_assert(kMaxContext / kTile * 3100 <= kWaitLimit / 2, "a unit of the longest context");
-inline int64_t units_for(int num_tokens, int num_seqs, int group_shift) {
-  return num_tokens / (2 * kTile >> group_shift) + static_cast<int64_t>(num_seqs);
+inline int64_t units_for(int num_tokens, int num_seqs, int group_shift, int tiles = 2) {
+  return num_tokens / (tiles * kTile >> group_shift) + static_cast<int64_t>(num_seqs);
 }
 inline int splits_for(int64_t ctas, int64_t max_context, int* split_tiles) {
   const int64_t tiles = (max_context + kTile - 1) / kTile;

@@ -28,7 +28,6 @@ namespace prompt_q8 {
 using namespace prompt;
 
 constexpr int kStages = 3;                       // fp16 tiles in shared memory
-constexpr int kRaw = 3;                          // tiles of codes
 constexpr int kRawBytes = kTile * kHeadDim;
 constexpr int kThreads = 512;                    // 2 softmax warpgroups; 2 copy, MMA and work
                                                  // warps; a widening warpgroup
@@ -40,8 +39,8 @@ constexpr int kCopyWarp = 8, kMmaWarp = 9, kWorkWarp = 10, kCopyVWarp = 11, kWid
 constexpr int kReaders = 15;                     // warps that read a unit's description
 // Scale entries of a tile, one for each `gran` tokens, in a ring: a tile's are written
 // before its K is waited for and read until its weights are done.  K of the tile kSlots
-// further on cannot be under way by then: at most kRaw + kStages copies of K and V lie
-// between, fewer than 4 tiles.
+// further on cannot be under way by then: the copies that are not yet read number kRaw at
+// most, the widened tiles that are not yet used kStages, 8 copies of K and V or 4 tiles in all.
 constexpr int kSlots = 8;
 template <int BS>
 struct Scales {
@@ -50,9 +49,14 @@ struct Scales {
   static constexpr int bytes = 3 * n * 4;          // K factors, log2 of V scales, their inverses
 };
 
+// TILES: query tiles of a unit.  Units of one tile (few rows a sequence) have two more places
+// for codes where the second tile would be: what bounds them is how much is under way.
+template <int TILES>
 struct Layout {
-  static constexpr int q = 0;                            // two query tiles
-  static constexpr int kv = q + 2 * kTileBytes;
+  static constexpr int kRaw = TILES == 2 ? 3 : 5;        // tiles of codes
+  static_assert(kRaw + kStages <= 8 && kSlots >= 8, "see kSlots");
+  static constexpr int q = 0;                            // query tiles
+  static constexpr int kv = q + TILES * kTileBytes;
   static constexpr int raw = kv + kStages * kTileBytes;
   static constexpr int stage = raw + kRaw * kRawBytes;   // output rows, 2 KB a softmax warp
   static constexpr int lm = stage + 8 * 2048;            // float2 [128]: sums and maxima of a
@@ -129,23 +133,25 @@ __device__ __forceinline__ CopyAt copy_at(int at, int n, bool pair) {
   return at ? CopyAt{(at - 2) >> 1, true} : CopyAt{0, false};
 }
 
-struct Ring {
+template <int N>
+struct RingOf {
   int st;
   uint32_t round;
-  __device__ __forceinline__ Ring after() const {
-    return st + 1 == kStages ? Ring{0, round + 1} : Ring{st + 1, round};
+  __device__ __forceinline__ RingOf after() const {
+    return st + 1 == N ? RingOf{0, round + 1} : RingOf{st + 1, round};
   }
 };
-static_assert(kRaw == kStages, "both rings in one count");
+using Ring = RingOf<kStages>;
 
-template <class Wide, int BS>
+template <class Wide, int BS, int TILES>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_q8_kernel(const __grid_constant__ CUtensorMap tmap_q,
                      const __grid_constant__ CUtensorMap tmap_k,
                      const __grid_constant__ CUtensorMap tmap_v,
                      const __grid_constant__ CUtensorMap tmap_o, const Q8Params qp) {
   using Sc = Scales<BS>;
-  using Smem = Layout;
+  using Smem = Layout<TILES>;
+  constexpr int kRaw = Smem::kRaw;
   constexpr unsigned kFull = 0xffffffffu;
   const Params& p = qp.p;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -177,9 +183,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(Smem::p_full, 2 * i + 1), 4);
       mbar_init(bar(Smem::o_full, i), 1);
     }
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kRaw; ++i) {
       mbar_init(bar(Smem::raw_full, i), 1);
       mbar_init(bar(Smem::raw_empty, i), 4);
+    }
+    for (int i = 0; i < kStages; ++i) {
       mbar_init(bar(Smem::kv_full, i), 4);
       mbar_init(bar(Smem::kv_empty, i), 1);
     }
@@ -344,20 +352,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t to = smem_u32(smem + Smem::kv) + (token >> 3) * kEight + (token & 7) * 128;
       const uint32_t x7 = (token & 7) << 4;
       Ring ring = {0, 0};
+      RingOf<kRaw> raw = {0, 0};
       bool ok = true;
       Unit u;
       for (int k = 0; ok && next_unit(k, u); ++k) {
         const int n = u.last - u.begin;
 #pragma unroll 1
-        for (int at = 0; at < 2 * n; ++at, ring = ring.after()) {
-          ok = wait(bar(Smem::raw_full, ring.st), ring.round & 1);
+        for (int at = 0; at < 2 * n; ++at, ring = ring.after(), raw = raw.after()) {
+          ok = wait(bar(Smem::raw_full, raw.st), raw.round & 1);
           if (!ok) break;
           uint4 w[8];
 #pragma unroll
           for (int c = 0; c < 8; ++c)
-            w[c] = ld_shared16(from + ring.st * kRawBytes + ((c << 4) ^ x7));
+            w[c] = ld_shared16(from + raw.st * kRawBytes + ((c << 4) ^ x7));
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(Smem::raw_empty, ring.st));
+          if (lane == 0) mbar_arrive(bar(Smem::raw_empty, raw.st));
           // a weight of 0 must not meet a NaN: codes past the context are any bytes
           const int tile = u.last - 1 - copy_at(at, n, u.pair).tile;
           if (tile * kTile + token >= u.ctx)
@@ -560,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int published = 0;
       for (int tries = 0; ok; ++tries) {
         Unit u;
-        const bool work = bx >= 0 && make_unit(p, bx, by, max_context, u);
+        const bool work = bx >= 0 && make_unit<TILES>(p, bx, by, max_context, u);
         if (bx < 0) u.begin = u.last = 0;   // tells the readers to stop
         if (work || bx < 0) {
           if (lane == 0) {
@@ -626,6 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok = u.tok0[x] + (r >> p.group_shift);
       const int pos0 = u.ctx - u.n + u.tok0[x];             // of the tile's first row
       const int pos = min(u.ctx - u.n + tok, u.ctx - 1);
+      const bool rows = u.tok0[x] + ((warp & 3) * 32 >> p.group_shift) < u.n;
       float m = kNoMax;   // log2 of the weights' unit
       float2 l2 = make_float2(0.f, 0.f);
       const int step = u.pair ? 2 : 1, top = u.pair ? u.last - 1 - x : u.end[x] - 1;
@@ -635,6 +645,14 @@ __global__ void __launch_bounds__(kThreads, 1)
              wait(bar(Smem::s_full, x), ns & 1);
         if (!ok) break;
         ++ns;
+        if (!rows) {   // none of the warp's rows is a token's: whatever the weights are, nobody reads
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(Smem::p_full, 2 * x));
+            mbar_arrive(bar(Smem::p_full, 2 * x + 1));
+          }
+          continue;
+        }
         fence_after();
         if (j * kTile + kTile - 1 > pos0) {
           // some row of the tile does not see all of it: mask the scores in place, 32 columns
@@ -883,30 +901,33 @@ bool make_out_map(CUtensorMap* map, void* base, int heads, int64_t rows, int gro
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class Wide, int BS>
-int launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-           const CUtensorMap& mo, const Q8Params& qp, dim3 grid, cudaStream_t st) {
+struct Maps {
+  CUtensorMap q, k, v, out;
+};
+
+template <class Wide, int BS, int TILES>
+int launch(const Maps& m, const Q8Params& qp, dim3 grid, cudaStream_t st) {
   static std::atomic<uint8_t> opted_in[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
   if (dev < 0 || dev >= 64 || !opted_in[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(prompt_q8_kernel<Wide, BS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Layout::alloc) != cudaSuccess)
+    if (cudaFuncSetAttribute(prompt_q8_kernel<Wide, BS, TILES>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Layout<TILES>::alloc) != cudaSuccess)
       return PKV_ERR_CUDA;
     if (dev >= 0 && dev < 64) opted_in[dev].store(1, std::memory_order_release);
   }
-  return launch_dependent(prompt_q8_kernel<Wide, BS>, grid, kThreads, Layout::alloc, st, mq, mk, mv,
-                          mo, qp);
+  return launch_dependent(prompt_q8_kernel<Wide, BS, TILES>, grid, kThreads, Layout<TILES>::alloc,
+                          st, m.q, m.k, m.v, m.out, qp);
 }
 
-template <class Wide>
-int launch_any(int block_size, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-               const CUtensorMap& mo, const Q8Params& qp, dim3 grid, cudaStream_t st) {
+template <class Wide, int TILES>
+int launch_any(int block_size, const Maps& m, const Q8Params& qp, dim3 grid, cudaStream_t st) {
   switch (block_size) {
-    case 8: return launch<Wide, 8>(mq, mk, mv, mo, qp, grid, st);
-    case 16: return launch<Wide, 16>(mq, mk, mv, mo, qp, grid, st);
-    case 32: return launch<Wide, 32>(mq, mk, mv, mo, qp, grid, st);
-    default: return launch<Wide, 64>(mq, mk, mv, mo, qp, grid, st);
+    case 8: return launch<Wide, 8, TILES>(m, qp, grid, st);
+    case 16: return launch<Wide, 16, TILES>(m, qp, grid, st);
+    case 32: return launch<Wide, 32, TILES>(m, qp, grid, st);
+    default: return launch<Wide, 64, TILES>(m, qp, grid, st);
   }
 }
 
@@ -943,7 +964,12 @@ extern "C" int pkv_paged_attention_prefill_q8(
           15 ||
       (reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale)) & 3)
     return PKV_ERR_INVALID_ARG;
-  const int64_t units = units_for(num_tokens, num_seqs, shift);
+  // one query tile a unit where a sequence brings, on average, no more rows than that (any
+  // batch works either way)
+  const int tiles = (static_cast<int64_t>(num_tokens) << shift) <= static_cast<int64_t>(num_seqs) * kTile
+                        ? 1
+                        : 2;
+  const int64_t units = units_for(num_tokens, num_seqs, shift, tiles);
   if (units * num_kv_heads > INT32_MAX || num_q_heads > 65535) return PKV_ERR_UNSUPPORTED;
   Q8Params qp = {};
   Params& p = qp.p;
@@ -975,18 +1001,21 @@ extern "C" int pkv_paged_attention_prefill_q8(
   qp.v_scale = v_scale;
   qp.scale_stride = scale_stride;
 
-  CUtensorMap mq, mk, mv, mo;
+  Maps m;
   const int64_t rows = num_blocks * block_size;
-  if (!make_map(&mq, q, num_q_heads, num_tokens, 1 << shift, kTile >> shift) ||
-      !make_out_map(&mo, out, num_q_heads, num_tokens, 1 << shift) ||
-      !make_code_map(&mk, k_cache, num_kv_heads, rows, block_size) ||
-      !make_code_map(&mv, v_cache, num_kv_heads, rows, block_size))
+  if (!make_map(&m.q, q, num_q_heads, num_tokens, 1 << shift, kTile >> shift) ||
+      !make_out_map(&m.out, out, num_q_heads, num_tokens, 1 << shift) ||
+      !make_code_map(&m.k, k_cache, num_kv_heads, rows, block_size) ||
+      !make_code_map(&m.v, v_cache, num_kv_heads, rows, block_size))
     return PKV_ERR_CUDA;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const dim3 grid(static_cast<unsigned>(units * num_kv_heads), p.splits);
-  const int rc = code == PKV_CODE_INT8
-                     ? launch_any<Int8Wide>(block_size, mq, mk, mv, mo, qp, grid, st)
-                     : launch_any<E4m3Wide>(block_size, mq, mk, mv, mo, qp, grid, st);
+  const auto go = [&](auto wide) {
+    using Wide = decltype(wide);
+    return tiles == 1 ? launch_any<Wide, 1>(block_size, m, qp, grid, st)
+                      : launch_any<Wide, 2>(block_size, m, qp, grid, st);
+  };
+  const int rc = code == PKV_CODE_INT8 ? go(Int8Wide()) : go(E4m3Wide());
   if (rc != PKV_OK || p.splits == 1) return rc;
   return launch_merge(p, max_context, st);
 }
