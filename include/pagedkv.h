@@ -507,9 +507,9 @@ int pkv_paged_attention_decode_q8(void* out, const void* q, const void* k_cache,
 /*
  * Causal attention of prompt chunks over an 8-bit cache: pkv_paged_attention_prefill
  * with K_s[t] = code * k_scale[block of t, g] and V_s[t] likewise.  Same packed batch,
- * shapes, limits, workspace (pkv_paged_attention_prefill_workspace_bytes), errors and
- * output: whole prompts, chunks behind earlier ones or behind a cached prefix, a few draft
- * tokens.  All of the context's K and V must already be in the cache
+ * shapes, limits, errors and output: whole prompts, chunks behind earlier ones or behind a
+ * cached prefix, a few draft tokens (a kernel of its own where the sequences bring 16 rows
+ * of a KV head or fewer on average).  All of the context's K and V must already be in the cache
  * (pkv_reshape_and_cache_q8, pkv_rope_and_cache_q8).
  *   k_cache, v_cache  codes, 16-byte aligned; k_scale, v_scale 4-byte aligned
  * Scales must be finite and not negative (a zero scale is a block of zeros; a V scale
@@ -529,6 +529,11 @@ int pkv_paged_attention_prefill_q8(void* out, const void* q, const void* k_cache
                                    int64_t num_blocks, int max_blocks_per_seq, int scale_stride,
                                    float scale, void* workspace, size_t workspace_bytes,
                                    int32_t* dev_err, void* stream);
+
+/* Workspace bytes of pkv_paged_attention_prefill_q8 for these sizes (host only). */
+size_t pkv_paged_attention_prefill_q8_workspace_bytes(int num_tokens, int num_seqs,
+                                                      int num_q_heads, int num_kv_heads,
+                                                      int max_blocks_per_seq, int block_size);
 
 /* ---- rotary positions -------------------------------------------------------- */
 /*

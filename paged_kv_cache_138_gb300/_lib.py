@@ -64,6 +64,7 @@ SIGNATURES = {
                                            _I64, _I, _I, _F, _P, _SZ, _P, _P]),
     "pkv_paged_attention_prefill_q8": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I,
                                             _I, _I, _I64, _I, _I, _F, _P, _SZ, _P, _P]),
+    "pkv_paged_attention_prefill_q8_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "pkv_rotary_embedding": (_I, [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _I, _P, _P, _I64, _I,
                                   _I, _I, _I, _I, _I, _P, _P]),
     "pkv_rope_and_cache": (_I, [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _I,

@@ -20,12 +20,10 @@
 //    again, a block's sum at a time.
 //  * Output rows leave through 2 KB a warp (the fp16 kernel: 4), which makes room for the
 //    third ring stage of each kind.
-#include "prompt_device.cuh"
+#include "prompt_q8.cuh"
 
 namespace pkv {
 namespace prompt_q8 {
-
-using namespace prompt;
 
 constexpr int kStages = 3;                       // fp16 tiles in shared memory
 constexpr int kRawBytes = kTile * kHeadDim;
@@ -90,35 +88,6 @@ struct Layout {
 // an fp16 tile: both halves of the dims one after the other, 1 KB atoms of 8 tokens x 64
 // dims (128-byte swizzle)
 constexpr uint32_t kHalf = kHalfBytes, kEight = 1024;
-
-struct Q8Params {
-  Params p;                // v unused
-  const float* k_scale;    // [num_blocks, scale_stride]
-  const float* v_scale;
-  int scale_stride;
-};
-
-// V scales from here down count as this one: fp16 values give none as small but 0 (2^-24 /
-// 448 is just above), and what they multiply rounds to 0 in fp16
-constexpr float kLeastScale = 1.f / (1ull << 33), kLeastLog = -33.f;
-
-// four codes as two packed fp16 pairs, exactly
-struct Int8Wide {
-  static __device__ __forceinline__ uint32_t pair(uint32_t w, uint32_t sel) {
-    // bytes biased by 128: 1024 + u, minus 1152 = the code
-    const __half2 h = u32_as_half2(__byte_perm(w, 0x64646464u, sel));
-    return half2_as_u32(__hsub2(h, __half2half2(__ushort_as_half(0x6480))));
-  }
-  static __device__ __forceinline__ uint2 four(uint32_t w) {
-    w ^= 0x80808080u;
-    return make_uint2(pair(w, 0x4140), pair(w, 0x4342));
-  }
-};
-struct E4m3Wide {
-  static __device__ __forceinline__ uint2 four(uint32_t w) {
-    return make_uint2(E4m3Code::half2_of(w & 0xffffu), E4m3Code::half2_of(w >> 16));
-  }
-};
 
 // The tile (counted from the unit's last) and kind of the at-th copy of a unit of n tiles:
 // K and V of each tile in turn; in a pair V after the next tile's K.
@@ -294,18 +263,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float k_sc = __shfl_sync(kFull, scs.x, in_batch * kBoxes + lane % kBoxes);
             const float v_sc = __shfl_sync(kFull, scs.y, in_batch * kBoxes + lane % kBoxes);
             if (lane < kBoxes) {
-              // a factor of 0 would turn a masked -infinity into a NaN (a scale that is
-              // not a number stays one)
-              const float f = k_sc * p.scale_log2, v = fmaxf(v_sc, kLeastScale);
-              const float kf = f < 1e-30f ? 1e-30f : f;
-              const float lv = v_sc <= kLeastScale ? kLeastLog : __log2f(v), inv = __frcp_rn(v);
+              const BlockScale b = block_scale(k_sc, v_sc, p.scale_log2);
               float* to = scales_at(tiles + i);
 #pragma unroll
               for (int e = 0; e < BS / Sc::gran; ++e) {
                 const int c = lane * (BS / Sc::gran) + e;
-                to[c] = kf;
-                to[Sc::n + c] = lv;
-                to[2 * Sc::n + c] = inv;
+                to[c] = b.k;
+                to[Sc::n + c] = b.v;
+                to[2 * Sc::n + c] = b.inv;
               }
             }
             __syncwarp();
@@ -931,6 +896,25 @@ int launch_any(int block_size, const Maps& m, const Q8Params& qp, dim3 grid, cud
   }
 }
 
+Plan plan_of(int num_tokens, int num_seqs, int num_kv_heads, int group_shift, int64_t max_context) {
+  const int64_t rows = static_cast<int64_t>(num_tokens) << group_shift;   // of a KV head
+  // Both kernels work for any batch; the rules go by the average sequence.  16 rows, 64 x 4096
+  // tokens, e4m3: 119 us and 132 here; 32 rows: 168 and 130.
+  if (rows <= 16ll * num_seqs)
+    return few_rows_plan(num_tokens, num_seqs, num_kv_heads, group_shift, max_context);
+  Plan plan = {};
+  plan.tiles = rows <= static_cast<int64_t>(num_seqs) * kTile ? 1 : 2;
+  plan.units = units_for(num_tokens, num_seqs, group_shift, plan.tiles);
+  plan.splits = splits_for(plan.units * num_kv_heads, max_context, &plan.split_tiles);
+  return plan;
+}
+
+size_t partial_bytes(const Plan& plan, int num_tokens, int num_q_heads) {
+  return plan.splits > 1 ? static_cast<size_t>(num_tokens) * num_q_heads * plan.splits *
+                               (kHeadDim + 2) * sizeof(float)
+                         : 0;
+}
+
 }  // namespace prompt_q8
 }  // namespace pkv
 
@@ -964,24 +948,21 @@ extern "C" int pkv_paged_attention_prefill_q8(
           15 ||
       (reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale)) & 3)
     return PKV_ERR_INVALID_ARG;
-  // one query tile a unit where a sequence brings, on average, no more rows than that (any
-  // batch works either way)
-  const int tiles = (static_cast<int64_t>(num_tokens) << shift) <= static_cast<int64_t>(num_seqs) * kTile
-                        ? 1
-                        : 2;
-  const int64_t units = units_for(num_tokens, num_seqs, shift, tiles);
-  if (units * num_kv_heads > INT32_MAX || num_q_heads > 65535) return PKV_ERR_UNSUPPORTED;
+  const Plan plan = plan_of(num_tokens, num_seqs, num_kv_heads, shift, max_context);
+  if (plan.units * num_kv_heads > INT32_MAX || num_q_heads > 65535 || plan.splits > 65535)
+    return PKV_ERR_UNSUPPORTED;
   Q8Params qp = {};
   Params& p = qp.p;
-  p.splits = splits_for(units * num_kv_heads, max_context, &p.split_tiles);
+  p.splits = plan.splits;
+  p.split_tiles = plan.split_tiles;
   if (p.splits > 1) {
-    const size_t rows = static_cast<size_t>(num_tokens) * num_q_heads;
-    if (!workspace || workspace_bytes < rows * p.splits * (kHeadDim + 2) * sizeof(float))
+    if (!workspace || workspace_bytes < partial_bytes(plan, num_tokens, num_q_heads))
       return PKV_ERR_INVALID_ARG;
     p.part_o = static_cast<float*>(workspace);
-    p.part_ml = p.part_o + rows * p.splits * kHeadDim;
+    p.part_ml = p.part_o + static_cast<size_t>(num_tokens) * num_q_heads * p.splits * kHeadDim;
   }
   p.out = static_cast<__half*>(out);
+  qp.q = static_cast<const __half*>(q);
   p.query_start = query_start;
   p.context_lens = context_lens;
   p.block_tables = block_tables;
@@ -1001,21 +982,42 @@ extern "C" int pkv_paged_attention_prefill_q8(
   qp.v_scale = v_scale;
   qp.scale_stride = scale_stride;
 
-  Maps m;
-  const int64_t rows = num_blocks * block_size;
-  if (!make_map(&m.q, q, num_q_heads, num_tokens, 1 << shift, kTile >> shift) ||
-      !make_out_map(&m.out, out, num_q_heads, num_tokens, 1 << shift) ||
-      !make_code_map(&m.k, k_cache, num_kv_heads, rows, block_size) ||
-      !make_code_map(&m.v, v_cache, num_kv_heads, rows, block_size))
-    return PKV_ERR_CUDA;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const dim3 grid(static_cast<unsigned>(units * num_kv_heads), p.splits);
-  const auto go = [&](auto wide) {
-    using Wide = decltype(wide);
-    return tiles == 1 ? launch_any<Wide, 1>(block_size, m, qp, grid, st)
-                      : launch_any<Wide, 2>(block_size, m, qp, grid, st);
-  };
-  const int rc = code == PKV_CODE_INT8 ? go(Int8Wide()) : go(E4m3Wide());
+  int rc;
+  if (plan.columns) {
+    rc = launch_few_rows(qp, plan, code, block_size, k_cache, v_cache, st);
+  } else {
+    Maps m;
+    const int64_t rows = num_blocks * block_size;
+    if (!make_map(&m.q, q, num_q_heads, num_tokens, 1 << shift, kTile >> shift) ||
+        !make_out_map(&m.out, out, num_q_heads, num_tokens, 1 << shift) ||
+        !make_code_map(&m.k, k_cache, num_kv_heads, rows, block_size) ||
+        !make_code_map(&m.v, v_cache, num_kv_heads, rows, block_size))
+      return PKV_ERR_CUDA;
+    const dim3 grid(static_cast<unsigned>(plan.units * num_kv_heads), p.splits);
+    const auto go = [&](auto wide) {
+      using Wide = decltype(wide);
+      return plan.tiles == 1 ? launch_any<Wide, 1>(block_size, m, qp, grid, st)
+                             : launch_any<Wide, 2>(block_size, m, qp, grid, st);
+    };
+    rc = code == PKV_CODE_INT8 ? go(Int8Wide()) : go(E4m3Wide());
+  }
   if (rc != PKV_OK || p.splits == 1) return rc;
   return launch_merge(p, max_context, st);
+}
+
+extern "C" size_t pkv_paged_attention_prefill_q8_workspace_bytes(int num_tokens, int num_seqs,
+                                                                 int num_q_heads,
+                                                                 int num_kv_heads,
+                                                                 int max_blocks_per_seq,
+                                                                 int block_size) {
+  using namespace pkv::prompt_q8;
+  if (num_tokens <= 0 || num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
+      max_blocks_per_seq <= 0 || block_size <= 0)
+    return 0;
+  const int shift = group_shift_of(num_q_heads, num_kv_heads);
+  if (shift < 0) return 0;
+  return partial_bytes(plan_of(num_tokens, num_seqs, num_kv_heads, shift,
+                               static_cast<int64_t>(max_blocks_per_seq) * block_size),
+                       num_tokens, num_q_heads);
 }

@@ -733,11 +733,20 @@ def paged_attention_decode_q8(out, q, k_cache, v_cache, k_scale, v_scale, block_
                 keep, out)
 
 
+@functools.lru_cache(maxsize=256)
+def prefill_q8_workspace_bytes(num_tokens, num_seqs, num_q_heads, num_kv_heads, max_blocks_per_seq,
+                               block_size=BLOCK_SIZE):
+    """Bytes of partials paged_attention_prefill_q8 needs for these sizes (0 unless it
+    splits the key axis)."""
+    return int(lib().pkv_paged_attention_prefill_q8_workspace_bytes(
+        num_tokens, num_seqs, num_q_heads, num_kv_heads, max_blocks_per_seq, block_size))
+
+
 def paged_attention_prefill_q8(out, q, k_cache, v_cache, k_scale, v_scale, block_tables,
                                context_lens, query_start, scale, workspace=None, dev_err=None,
                                stream=None, prepare=False):
     """paged_attention_prefill over an 8-bit cache (see q8_cache, reshape_and_cache_q8,
-    rope_and_cache_q8); same workspace (prefill_workspace_bytes).
+    rope_and_cache_q8); workspace: prefill_q8_workspace_bytes.
     prepare=True returns a PreparedLaunch instead of launching."""
     try:
         dev = _get_device()
@@ -765,7 +774,7 @@ def paged_attention_prefill_q8(out, q, k_cache, v_cache, k_scale, v_scale, block
     if workspace is not None or dev_err is not None:
         _check_side(workspace, dev_err)
     if workspace is None:
-        need = prefill_workspace_bytes(T, S, Hq, Hkv, max_blocks, bs)
+        need = prefill_q8_workspace_bytes(T, S, Hq, Hkv, max_blocks, bs)
         if need:
             workspace = _new_workspace(need, q.device, stream)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0

@@ -136,7 +136,7 @@ def test_matches_oracle(ops, code, bs, Hq, Hkv, new, cached):
 def test_split_key_axis(ops, code, new, cached, bs):
     """Few rows over long contexts: several units share a row, and a merge joins them."""
     c = Case(5, new, cached, 8, 2, bs, code, width=wl.blocks_for(9100, bs))
-    assert ops.prefill_workspace_bytes(len(c.q), len(new), 8, 2, c.tables.shape[1], bs) > 0
+    assert ops.prefill_q8_workspace_bytes(len(c.q), len(new), 8, 2, c.tables.shape[1], bs) > 0
     got, err = c.run(ops)
     assert err == 0
     c.check(got)
@@ -268,7 +268,7 @@ def test_streams_graphs_and_workspaces(ops):
     """Split launches on another stream than the current one, prepared, and two captured graphs with
     a workspace each, replayed one over the other on two streams."""
     cases = [Case(s, [4, 2], [3000, 900], 8, 2, 16, "int8", width=200) for s in (20, 21)]
-    need = ops.prefill_workspace_bytes(6, 2, 8, 2, 200)
+    need = ops.prefill_q8_workspace_bytes(6, 2, 8, 2, 200)
     assert need > 0
     runs = []
     for c in cases:

@@ -42,14 +42,14 @@ def test_entry_point_refuses_without_a_gpu(native_lib):
     for bs in (0, 4, 12, 128):
         assert run(bs=bs) == -2
     assert run(nb=2 ** 31) == -2 and run(mb=2 ** 22) == -2
-    need = native_lib.pkv_paged_attention_prefill_workspace_bytes(8, 1, 32, 8, 2048, 16)
+    need = native_lib.pkv_paged_attention_prefill_q8_workspace_bytes(8, 1, 32, 8, 2048, 16)
     assert need > 0
     few = dict(T=8, Hq=32, Hkv=8, mb=2048, stride=8)
     assert run(**few) == -1 and run(**few, ws=p, b=need - 1) == -1 and run(**few, ws=p + 8, b=need) == -1
 
 
 def test_wrapper_refuses(calls, monkeypatch):   # noqa: F811
-    monkeypatch.setattr(real_ops, "prefill_workspace_bytes", lambda *a: 0)
+    monkeypatch.setattr(real_ops, "prefill_q8_workspace_bytes", lambda *a: 0)
     i8 = torch.int8
     good = dict(out=Fake((5, 8, 128), F16), q=Fake((5, 8, 128), F16), k_cache=Fake((9, 16, 2, 128), i8),
                 v_cache=Fake((9, 16, 2, 128), i8), k_scale=Fake((9, 4), F32),
