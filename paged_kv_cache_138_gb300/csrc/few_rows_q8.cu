@@ -85,7 +85,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
   const int64_t max_context = static_cast<int64_t>(p.max_blocks) * BS;
   // a programmatic dependent of the stream's previous kernel
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (blockIdx.x == 0 && blockIdx.y == 0)   // every entry is looked at once, used or not
+  // every entry is looked at once, used or not, where seldom a unit is (see few_rows_plan)
+  if (blockIdx.x == gridDim.x - 1 && blockIdx.y == 0)
     for (int s = threadIdx.x; s < p.num_seqs; s += kFewThreads)
       packed_seq(p.query_start, p.context_lens, s, p.num_tokens, max_context, p.dev_err, true);
 

@@ -896,6 +896,10 @@ int launch_any(int block_size, const Maps& m, const Q8Params& qp, dim3 grid, cud
   }
 }
 
+// a warp that waits for a whole unit of the longest context: see kMaxContext (a tile takes
+// 2000 to 3000 cycles)
+static_assert(kMaxContext / kTile * 4000 <= kWaitLimit / 2, "a unit of the longest context");
+
 Plan plan_of(int num_tokens, int num_seqs, int num_kv_heads, int group_shift, int64_t max_context) {
   const int64_t rows = static_cast<int64_t>(num_tokens) << group_shift;   // of a KV head
   // Both kernels work for any batch; the rules go by the average sequence.  16 rows, 64 x 4096

@@ -16,6 +16,7 @@
 // What bounds it: HBM for prompts; a step of single tokens is a chain of dependent loads
 // (sequence, position, table and block id, scale).
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <initializer_list>
 
@@ -179,11 +180,15 @@ __global__ void __launch_bounds__(kRowWarps * 32, 7) rope_rows_kernel(const RowP
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int64_t max_context = static_cast<int64_t>(p.max_blocks) * p.block_size;
-  if (CACHE && blockIdx.x == 0 && blockIdx.y == 0)   // every entry is looked at once, used or not
-    for (int s = threadIdx.x; s < p.num_seqs; s += kRowWarps * 32)
-      packed_seq(p.query_start, p.context_lens, s, p.num_tokens, max_context, p.dev_err, true);
-  const int i = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-  if (i >= p.num_tokens) return;
+  if (CACHE && blockIdx.x == gridDim.x - 1) {   // a CTA that looks at every entry once, used or not
+    if (blockIdx.y == 0)
+      for (int s = threadIdx.x; s < p.num_seqs; s += kRowWarps * 32)
+        packed_seq(p.query_start, p.context_lens, s, p.num_tokens, max_context, p.dev_err, true);
+    return;
+  }
+  const int64_t i64 = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+  if (i64 >= p.num_tokens) return;
+  const int i = static_cast<int>(i64);
   const int row0 = blockIdx.y * p.part_rows + (lane >> 3);
   const int rows = min(p.num_q_heads + (CACHE ? 2 : 1) * p.num_kv_heads, (blockIdx.y + 1) * p.part_rows);
   const Chunks ch(lane & 7, p.rot.n);
@@ -344,6 +349,12 @@ __device__ __forceinline__ void drop_nonfinite(float (&f)[8]) {
   for (int e = 0; e < 8; ++e) f[e] = fabsf(f[e]) < INFINITY ? f[e] : 0.f;
 }
 
+// Codes are 0 under a scale whose inverse would pass fp32's range (rotated values can be as
+// small as a table makes them; fp16 ones cannot).
+__device__ __forceinline__ float inverse_of(float scale) {
+  return scale >= FLT_MIN ? __fdiv_rn(1.f, scale) : 0.f;
+}
+
 // codes of a chunk: no value times inv passes the largest code by more than a rounding
 template <class Code>
 __device__ __forceinline__ uint2 code8(const float (&f)[8], float inv) {
@@ -429,7 +440,7 @@ __device__ __forceinline__ void append_row(const Q8Params& qp, const Piece& c, i
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float scale = fmaxf(before, __fdiv_rn(__uint_as_float(top), Code::kMax));
-    const float inv = scale > 0.f ? __fdiv_rn(1.f, scale) : 0.f;
+    const float inv = inverse_of(scale);
     if (stores) {
       if (scale > before && c.r0 > 0) {   // earlier rows of the block
         const float ratio = __fdiv_rn(before, scale);
@@ -591,7 +602,7 @@ __device__ __forceinline__ void append_rows(const Q8Params& qp, const Piece& c, 
       top = largest();
     }
     const float scale = fmaxf(before, __fdiv_rn(__uint_as_float(top), Code::kMax));
-    const float inv = scale > 0.f ? __fdiv_rn(1.f, scale) : 0.f;
+    const float inv = inverse_of(scale);
     if (scale > before && c.r0 > 0) {   // earlier rows of the block, under the grown scale
       const float ratio = __fdiv_rn(before, scale);
       for (int r = own; r < min(c.r0, kRows * (warp % kTeam) + kRows); r += 4)
@@ -619,10 +630,13 @@ __global__ void __launch_bounds__(kQ8Warps * 32, BS > 16 ? 4 : 0) rope_q8_kernel
   __shared__ float4 table[BS * 32];
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (blockIdx.x == 0 && blockIdx.y == 0)   // every entry is looked at once, used or not
-    for (int s = threadIdx.x; s < p.num_seqs; s += kQ8Warps * 32)
-      packed_seq(p.query_start, p.context_lens, s, p.num_tokens,
-                 static_cast<int64_t>(p.max_blocks) * BS, p.dev_err, true);
+  if (blockIdx.x == gridDim.x - 1) {   // a CTA that looks at every entry once, used or not
+    if (blockIdx.y == 0)
+      for (int s = threadIdx.x; s < p.num_seqs; s += kQ8Warps * 32)
+        packed_seq(p.query_start, p.context_lens, s, p.num_tokens,
+                   static_cast<int64_t>(p.max_blocks) * BS, p.dev_err, true);
+    return;
+  }
   Piece c;
   if (!find_piece<BS>(qp, c)) return;
   if (c.blk < 0 && threadIdx.x == 0) report(p.dev_err, PKV_DEV_BAD_BLOCK_ID);
@@ -696,7 +710,7 @@ int launch_rows(RowParams& p, bool adjacent, void* stream) {
   p.part_rows = static_cast<int>((rows + 4 * parts - 1) / (4 * parts) * 4);
   parts = (rows + p.part_rows - 1) / p.part_rows;
   if (parts > 65535) return PKV_ERR_UNSUPPORTED;
-  const dim3 grid((static_cast<unsigned>(p.num_tokens) + kRowWarps - 1) / kRowWarps,
+  const dim3 grid((static_cast<unsigned>(p.num_tokens) + kRowWarps - 1) / kRowWarps + CACHE,
                   static_cast<unsigned>(parts));
   const auto go = [&](auto kernel) { return launch(kernel, grid, kRowWarps * 32, stream, p); };
   if (p.rot.num_axes == 1)
@@ -892,8 +906,8 @@ extern "C" int pkv_rope_and_cache_q8(void* q_out, const void* q, const void* k, 
   const int64_t parts = p.by_token ? heads : (kRounds + units - 1) / units;
   const int64_t per = std::max(kLeast, (heads + parts * kLeast - 1) / (parts * kLeast) * kLeast);
   p.heads_per_cta = static_cast<int>(per);
-  if (units > INT32_MAX || (heads + per - 1) / per > 65535) return PKV_ERR_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(units), static_cast<unsigned>((heads + per - 1) / per));
+  if (units >= INT32_MAX || (heads + per - 1) / per > 65535) return PKV_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>(units + 1), static_cast<unsigned>((heads + per - 1) / per));
   return code == PKV_CODE_INT8 ? launch_q8<Int8Near>(p, adjacent != 0, block_size, grid, stream)
                                : launch_q8<E4m3Near>(p, adjacent != 0, block_size, grid, stream);
 }

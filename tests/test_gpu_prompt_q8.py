@@ -142,6 +142,45 @@ def test_split_key_axis(ops, code, new, cached, bs):
     c.check(got)
 
 
+def split_tokens(ops, c, Hq, Hkv):
+    """Tokens of a split of the case's launch, from the workspace's size."""
+    T, S, width = len(c.q), len(c.new), c.tables.shape[1]
+    splits = ops.prefill_q8_workspace_bytes(T, S, Hq, Hkv, width, c.bs) // (T * Hq * 130 * 4)
+    tiles = -(-width * c.bs // 128)
+    assert splits > 1
+    return -(-tiles // splits) * 128
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("new,Hq,Hkv", [([4, 2, 3], 8, 2), ([8, 8, 5], 4, 4), ([2, 1, 2], 8, 1),
+                                        ([20, 9, 30], 4, 2), ([60, 33, 50], 8, 2)])
+def test_rows_on_both_sides_of_a_split(ops, code, new, Hq, Hkv):
+    """Contexts that end on a split's first tokens: some of a unit's rows see the split, some do
+    not, and some have one split less to join."""
+    bs, width = 16, 640
+    c = Case(30, new, [0] * 3, Hq, Hkv, bs, code, width=width)
+    each = split_tokens(ops, c, Hq, Hkv)
+    for d in (0, 1, 2, max(new) - 1, max(new)):
+        lens = [each + d, 2 * each + d, 3 * each + d]
+        lens = [max(n, min(L, width * bs)) for n, L in zip(new, lens)]
+        c = Case(31 + d, new, [L - n for n, L in zip(new, lens)], Hq, Hkv, bs, code, width=width)
+        assert split_tokens(ops, c, Hq, Hkv) == each
+        got, err = c.run(ops)
+        assert err == 0
+        c.check(got)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(8, 8), (8, 2), (8, 1)])
+def test_few_rows_with_a_long_chunk_among_them(ops, Hq, Hkv):
+    """The kernel for few rows goes by the average: one sequence that brings many is cut into units."""
+    new = [1] * 60 + [77, 0, 2, 0, 1] + [1] * 35
+    cached = [0, 5, 130, 700, 33] * 20
+    c = Case(13, new, cached, Hq, Hkv, 16, "int8")
+    got, err = c.run(ops)
+    assert err == 0
+    c.check(got)
+
+
 def test_many_units_of_every_kind(ops):
     """Units of one and of two query tiles, long and short, more than there are SMs, so that CTAs go
     from one kind to another; sampled rows against the oracle."""

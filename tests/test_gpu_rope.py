@@ -411,3 +411,85 @@ def test_pool_past_32_bits(ops):
     oq.write(rk, qs, small, lens, codes, scales, bs, "int8")
     got = codes_of(cache[0][[0, nb - 2, nb - 1]], "int8")
     assert np.array_equal(got, codes)
+
+
+@pytest.mark.parametrize("new", [[1, 1, 1], [20, 3, 1]])
+def test_q8_tiny_values(ops, new):
+    """A table that shrinks keys until their scale has no finite inverse: codes are 0, values are off
+    by less than fp32's smallest normal number."""
+    rng = np.random.default_rng(5)
+    Hq, Hkv, bs = 4, 1, 16
+    lens, qs, T = np.array(new, np.int32), starts(new), int(np.sum(new))
+    nb, tables = batch(rng, lens, bs)
+    (q, k, v), (tq, tk, tv) = projection(rng, T, Hq, Hkv)
+    table = (table_of(64, 100) * 1e-38).astype(np.float32)
+    cache = ops.q8_cache(nb, Hkv, bs)
+    err = ops.new_error_word()
+    qo = torch.empty((T, Hq, D), dtype=torch.float16, device="cuda")
+    ops.rope_and_cache_q8(qo, tq, tk, tv, dev(qs), dev(tables), dev(lens), *cache, dev(table), dev_err=err)
+    assert ops.read_error_word(err) == 0
+    seq, place = orope.places(qs, lens, T)
+    at = tables[seq, place // bs], place % bs
+    got = codes_of(cache[0], "int8")[at] * cache[2].cpu().numpy()[at[0], :Hkv, None]
+    ref = orope.rotate(k, place, table)
+    off = np.abs(got - ref)
+    tiny = np.abs(ref).max(axis=(1, 2)).max() / 127 < 2.0 ** -126
+    assert off.max() <= (127 * 2.0 ** -126 if tiny else np.abs(ref).max() / 127)
+    codes, scales = np.zeros((nb, bs, Hkv, D)), np.zeros((nb, 4), np.float32)
+    oq.write(v, qs, tables, lens, codes, scales, bs, "int8")
+    assert np.array_equal(codes_of(cache[1], "int8"), codes)
+
+
+def test_append_in_place(ops):
+    """q_out q itself, a slice of the projection's output, in both caches' calls."""
+    rng = np.random.default_rng(6)
+    new, Hq, Hkv, bs = [3, 1, 30], 8, 2, 16
+    lens, qs, T = np.array(new, np.int32), starts(new), 34
+    nb, tables = batch(rng, lens, bs)
+    table = table_of(64, 100)
+    (q, k, v), (tq, tk, tv) = projection(rng, T, Hq, Hkv)
+    _, place = orope.places(qs, lens, T)
+    ref = orope.rotate(q, place, table).astype(np.float16)
+    kc = torch.zeros((nb, bs, Hkv, D), dtype=torch.float16, device="cuda")
+    args = (dev(qs), dev(tables), dev(lens))
+    ops.rope_and_cache(tq, tq, tk, tv, *args, kc, torch.zeros_like(kc), dev(table))
+    assert np.array_equal(bits(tq.cpu().numpy()), bits(ref))
+    assert np.array_equal(bits(tk.cpu().numpy()), bits(k))       # beside it nothing has changed
+    ops.rope_and_cache_q8(tq, tq, tk, tv, *args, *ops.q8_cache(nb, Hkv, bs), dev(table))
+    assert np.array_equal(bits(tq.cpu().numpy()), bits(orope.rotate(ref, place, table)))
+    assert np.array_equal(bits(tv.cpu().numpy()), bits(v))
+
+
+def test_many_sequences_and_heads(ops):
+    """More sequences than a search step holds, more heads than a part does, a long chunk among
+    single tokens."""
+    rng = np.random.default_rng(7)
+    S, Hq, Hkv, bs = 1500, 64, 8, 8
+    new = rng.integers(0, 4, S)
+    new[700] = 150
+    cached = rng.integers(0, 20, S)
+    lens, qs, T = (new + cached).astype(np.int32), starts(new), int(new.sum())
+    nb, tables = batch(rng, lens, bs)
+    table = table_of(64, 400)
+    (q, k, v), (tq, tk, tv) = projection(rng, T, Hq, Hkv)
+    seq, place = orope.places(qs, lens, T)
+    qo = torch.empty((T, Hq, D), dtype=torch.float16, device="cuda")
+    cache = ops.q8_cache(nb, Hkv, bs)
+    err = ops.new_error_word()
+    assert T < 4 * S
+    ops.rope_and_cache_q8(qo, tq, tk, tv, dev(qs), dev(tables), dev(lens), *cache, dev(table), dev_err=err)
+    assert ops.read_error_word(err) == 0
+    at = rng.choice(T, 200, replace=False)
+    assert np.array_equal(bits(qo.cpu().numpy()[at]), bits(orope.rotate(q[at], place[at], table)))
+    codes = {n: np.zeros((nb, bs, Hkv, D)) for n in "kv"}
+    scales = {n: np.zeros((nb, 8), np.float32) for n in "kv"}
+    for n, x, c, s in (("k", orope.rotate(k, place, table), cache[0], cache[2]), ("v", v, cache[1], cache[3])):
+        oq.write(x, qs, tables, lens, codes[n], scales[n], bs, "int8")
+        assert np.array_equal(s.cpu().numpy(), scales[n]) and np.array_equal(codes_of(c, "int8"), codes[n])
+    kc = torch.zeros((nb, bs, Hkv, D), dtype=torch.float16, device="cuda")
+    vc = torch.zeros_like(kc)
+    ops.rope_and_cache(qo, tq, tk, tv, dev(qs), dev(tables), dev(lens), kc, vc, dev(table), dev_err=err)
+    assert ops.read_error_word(err) == 0
+    ref = np.zeros((nb, bs, Hkv, D), np.float16)
+    ref[tables[seq, place // bs], place % bs] = orope.rotate(k, place, table).astype(np.float16)
+    assert np.array_equal(bits(kc.cpu().numpy()), bits(ref))
