@@ -606,8 +606,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int step = u.pair ? 2 : 1, top = u.pair ? u.last - 1 - x : u.end[x] - 1;
       for (int j = top; j >= u.begin; j -= step) {
         const uint32_t slot = tile0 + (u.last - 1 - j);
-        ok = wait(bar(Smem::sc_full, slot & (kSlots - 1)), slot / kSlots & 1) &&
-             wait(bar(Smem::s_full, x), ns & 1);
+        ok = wait(bar(Smem::sc_full, slot & (kSlots - 1)), slot / kSlots & 1);
+        if (!ok) break;
+        // K's factors and the logarithms of V's scales, read while the scores are under way
+        const float4* scale4 = reinterpret_cast<const float4*>(scales_at(slot));
+        constexpr bool kHeld = Sc::n == 8;   // 16 registers; with 8-token blocks read twice
+        float4 held[kHeld ? 4 : 1];
+        if (kHeld)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) held[kHeld ? e : 0] = scale4[e];
+        ok = wait(bar(Smem::s_full, x), ns & 1);
         if (!ok) break;
         ++ns;
         if (!rows) {   // none of the warp's rows is a token's: whatever the weights are, nobody reads
@@ -636,7 +644,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           wait_st();
         }
-        const float4* scale4 = reinterpret_cast<const float4*>(scales_at(slot));
         float s[kTile];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, reinterpret_cast<uint32_t*>(s + 32 * c));
@@ -645,7 +652,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         float bm[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int e4 = 0; e4 < Sc::n / 4; ++e4) {
-          const float4 f4 = scale4[e4], g4 = scale4[Sc::n / 4 + e4];
+          const float4 f4 = kHeld ? held[kHeld ? e4 : 0] : scale4[e4];
+          const float4 g4 = kHeld ? held[kHeld ? Sc::n / 4 + e4 : 0] : scale4[Sc::n / 4 + e4];
           const float f[4] = {f4.x, f4.y, f4.z, f4.w}, g[4] = {g4.x, g4.y, g4.z, g4.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -687,7 +695,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e4 = 0; e4 < Sc::n / 8; ++e4) {
             const int at = c * (Sc::n / 8) + e4;
-            const float4 f4 = scale4[at], g4 = scale4[Sc::n / 4 + at], h4 = scale4[Sc::n / 2 + at];
+            const float4 f4 = kHeld ? held[kHeld ? at : 0] : scale4[at];
+            const float4 g4 = kHeld ? held[kHeld ? Sc::n / 4 + at : 0] : scale4[Sc::n / 4 + at];
+            const float4 h4 = scale4[Sc::n / 2 + at];
             const float f[4] = {f4.x, f4.y, f4.z, f4.w}, g[4] = {g4.x, g4.y, g4.z, g4.w};
             const float h[4] = {h4.x, h4.y, h4.z, h4.w};
 #pragma unroll
