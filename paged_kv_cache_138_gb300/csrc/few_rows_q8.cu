@@ -330,6 +330,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
     ok = landed(k);
     if (!ok) break;
     process(k);
+    fence_proxy_async_smem();   // the stage is read before the copy engine writes it again
     __syncwarp();
     if (issued < mine) {
       issue(issued);

@@ -330,6 +330,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < 8; ++c)
             w[c] = ld_shared16(from + raw.st * kRawBytes + ((c << 4) ^ x7));
+          // the codes are in registers before the copy engine may write their place again: an
+          // arrival alone does not wait for reads (other tiles' codes came out, 8 tokens x 16
+          // dims now and then)
+          fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(Smem::raw_empty, raw.st));
           // a weight of 0 must not meet a NaN: codes past the context are any bytes
