@@ -17,10 +17,12 @@ LIB = os.path.join(HERE, "libpagedkv.so")
 
 SOURCES = ["attention_bs16.cu", "attention_bs8.cu", "attention_bs32.cu", "attention_bs64.cu",
            "paged_attention.cu", "attention_q8.cu", "q8_cache.cu", "prompt_attention.cu",
-           "prompt_q8.cu", "few_rows_q8.cu", "rope.cu", "cache_ops.cu", "synthetic.cu", "block_manager.cpp", "scheduler.cpp", "api.cpp"]
+           "prompt_q8.cu", "few_rows_q8.cu", "rope.cu", "rope_q8_int8.cu", "rope_q8_e4m3.cu",
+           "cache_ops.cu", "synthetic.cu", "block_manager.cpp", "scheduler.cpp", "api.cpp"]
 HEADERS = [os.path.join(CSRC, "pkv_device.cuh"), os.path.join(CSRC, "attention_kernel.cuh"),
            os.path.join(CSRC, "q8_device.cuh"), os.path.join(CSRC, "prompt_device.cuh"),
-           os.path.join(CSRC, "prompt_q8.cuh"),
+           os.path.join(CSRC, "prompt_q8.cuh"), os.path.join(CSRC, "rope.cuh"),
+           os.path.join(CSRC, "rope_q8.cuh"),
            os.path.join(INCLUDE, "pagedkv.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
