@@ -7,10 +7,11 @@
 //
 // The units of work, the two query tiles that take turns, the places in tensor memory and
 // the softmax are those of the prompt attention over the fp16 cache.  What differs:
-//  * Codes come by TMA through a ring of three 16 KB tiles; a warpgroup widens them
-//    to fp16, exactly (int8 by placing the byte under the exponent of 1024 and
-//    subtracting, e4m3 by its conversion), into a ring of three 32 KB tiles in the layout
-//    that the products read.  An 8-bit product would need q and the weights in 8 bits.
+//  * Codes come by TMA through a ring of three 16 KB tiles (five where units have one query
+//    tile); a warpgroup widens them to fp16, exactly (int8 by placing the byte under the
+//    exponent of 1024 and subtracting, e4m3 by its conversion), into a ring of three 32 KB
+//    tiles in the layout that the products read.  An 8-bit product would need q and the
+//    weights in 8 bits.
 //  * The scales never touch the values.  A block's K scale multiplies its scores
 //    (columns of one block lie together, so that it is one factor for 8 or 16 columns of
 //    a row); its V scale enters the weight's exponent, w = 2^(x + log2 v_scale - m), and
@@ -20,6 +21,16 @@
 //    again, a block's sum at a time.
 //  * Output rows leave through 2 KB a warp (the fp16 kernel: 4), which makes room for the
 //    third ring stage of each kind.
+//  * What bounds it: a query tile's softmax (1550 cycles a tile of 128 tokens, 500 of its
+//    scheduler's instructions being the widening's) and its own products (1024) follow one
+//    another, 2800 cycles a turn where the tensor core is busy for 2048.  16,384 tokens of 32/8
+//    heads, int8: 1304 us in short runs, 1371-1412 in loops of seconds, 1.56-1.69 PFLOP/s (fp16
+//    cache: 1180-1310 and 1370-1460); 16 x 2048 428 us, e4m3 400 (fp16 376); 8 of 64..512 rows
+//    behind 2048, 32 heads, e4m3: 95 us.  4 x 5..8 rows over 30k of 32/8 heads, int8: 78 us, 3.4
+//    TB/s: a tile of codes is widened in 1000 cycles, 550 of them instructions of one warp a
+//    scheduler.  Tried and not kept: two warpgroups that widen, in turn or one tile together
+//    (the softmax has 24 registers less; no faster), the next codes read ahead of the
+//    widening (their place comes free later: 10 % slower with few rows).
 #include "prompt_q8.cuh"
 
 namespace pkv {
