@@ -4,7 +4,6 @@
 
 #include <algorithm>
 #include <climits>
-#include <initializer_list>
 
 #include "q8_device.cuh"
 

@@ -18,14 +18,15 @@ namespace rope {
 // The new rows of one block of one sequence.
 struct Piece {
   int s, row0;      // its sequence; the packed row that would be the block's row 0
+  int nth;          // of a step's units of the piece (0 of long chunks')
   int base, r0, r1; // place of the block's row 0; new rows [r0, r1)
   int64_t blk;      // -1: no valid id
 };
 
 // Units are cut in one of two ways.  Long chunks: the write's units of BS rows, numbered
-// without a prefix sum, two to spare for each sequence.  Steps (fewer than 4 tokens a
-// sequence): every token is a unit, and the first new one of its block takes the
-// block's others along; no unit is empty when each sequence brings one.
+// without a prefix sum, two to spare for each sequence.  Steps (few tokens a
+// sequence on average): every token is a unit; the first of a piece of two or three rows does
+// them all, those of a longer one share its heads.
 template <int BS, bool STEP>
 __device__ __forceinline__ bool find_piece(const Q8Params& qp, Piece& c) {
   const RowParams& p = qp.r;
@@ -38,12 +39,14 @@ __device__ __forceinline__ bool find_piece(const Q8Params& qp, Piece& c) {
   int64_t lb;
   if (STEP) {
     const int nth = unit - q.row0;
-    if (nth < 0 || nth >= q.n || (nth > 0 && (start + nth) % BS != 0)) return false;
+    if (nth < 0 || nth >= q.n) return false;
     lb = (start + nth) / BS;
+    c.nth = start + nth - max(start, static_cast<int>(lb) * BS);
   } else {
     const int nth = unit - unit_base(p.query_start, c.s, BS, 2);
     lb = start / BS + static_cast<int64_t>(nth);
     if (nth < 0 || lb * BS >= q.ctx) return false;
+    c.nth = 0;
   }
   c.base = static_cast<int>(lb) * BS;
   c.r0 = max(start - c.base, 0);
@@ -200,79 +203,128 @@ __device__ __forceinline__ void append_row(const Q8Params& qp, const Piece& c, i
   }
 }
 
-// Pieces of a few rows in a step, the same way: the rows one after another, twice, for the
-// maximum and for the codes.
-template <class Code, int BS, bool ADJACENT, int AXES>
-__device__ __forceinline__ void append_few(const Q8Params& qp, const Piece& c, int first, int last) {
-  const RowParams& p = qp.r;
-  const int lane = threadIdx.x & 31;
-  const Chunks ch(lane & 7, p.rot.n);
-  const int64_t row_elems = static_cast<int64_t>(p.num_kv_heads) * kHeadDim;
+// Several rows in a step, one after another and twice, for the maximum and for the codes: what
+// is in registers then does not depend on how many there are.
+template <class Code, bool ADJACENT, int AXES>
+struct StepHead {
+  const Q8Params& qp;
+  const Piece& c;
+  const HeadAt at;
+  const Chunks ch;
+  const bool stores;
+  uint32_t top = 0;      // the largest of the finite values as bits
+
+  __device__ __forceinline__ StepHead(const Q8Params& params, const Piece& piece, int block_size, int head)
+      : qp(params), c(piece), at(params, piece, block_size, head), ch(threadIdx.x & 7, params.r.rot.n),
+        stores(!at.is_q && piece.blk >= 0) {}
+  // row r's values in 32 bits; false: it is left out
+  __device__ __forceinline__ bool values(int r, float (&a)[8], float (&b)[8]) const {
+    const RowParams& p = qp.r;
+    const uint4* from = reinterpret_cast<const uint4*>(at.src + (c.row0 + r) * at.stride);
+    const uint4 xa = from[ch.a], xb = from[ch.b];
+    int32_t pos[AXES];
+    load_positions(p.rot, c.row0 + r, c.base + r, pos);
+    if (!on_table(p.rot, pos)) return false;
+    widen(xa, a);
+    widen(xb, b);
+    if (!at.is_v && ch.turns) {
+      float4 cs[4];
+      load_turn<ADJACENT>(p.rot, ch, pos, cs);
+      rotate<ADJACENT>(a, b, cs);
+    }
+    return true;
+  }
+  // rows own, own + every, ..: q's to their place, what is stored to its maximum
+  __device__ __forceinline__ void look(int own, int every) {
+    const RowParams& p = qp.r;
+    uint32_t all = 0;
 #pragma unroll 1
-  for (int h0 = first; h0 < last; h0 += 4) {
-    const bool valid = h0 + (lane >> 3) < last;
-    const HeadAt at(qp, c, BS, min(h0 + (lane >> 3), last - 1));
-    const bool stores = valid && !at.is_q && c.blk >= 0;
-    // row r's values in 32 bits; false: it is left out
-    const auto values = [&](int r, float (&a)[8], float (&b)[8]) {
-      int32_t pos[AXES];
-      load_positions(p.rot, c.row0 + r, c.base + r, pos);
-      if (!on_table(p.rot, pos)) return false;
-      const uint4* from = reinterpret_cast<const uint4*>(at.src + (c.row0 + r) * at.stride);
-      widen(from[ch.a], a);
-      widen(from[ch.b], b);
-      if (!at.is_v && ch.turns) {
-        float4 cs[4];
-        load_turn<ADJACENT>(p.rot, ch, pos, cs);
-        rotate<ADJACENT>(a, b, cs);
-      }
-      return true;
-    };
-    const float before = stores && c.r0 > 0 ? *at.scale : 0.f;
-    uint32_t top = 0, all = 0;   // of the finite values, of all
-    if (valid && (at.is_q || stores))
-#pragma unroll 1
-      for (int r = c.r0; r < c.r1; ++r) {
-        float a[8], b[8];
-        if (!values(r, a, b)) {
-          report(p.dev_err, PKV_DEV_BAD_POSITION);
-          continue;
-        }
-        if (at.is_q) {
-          uint4* to = reinterpret_cast<uint4*>(p.q_out + (c.row0 + r) * p.q_out_stride + at.g * kHeadDim);
-          to[ch.a] = narrow(a);
-          to[ch.b] = narrow(b);
-          continue;
-        }
+    for (int r = c.r0 + own; r < c.r1; r += every) {
+      float a[8], b[8];
+      if (!values(r, a, b)) {
+        report(p.dev_err, PKV_DEV_BAD_POSITION);
+      } else if (at.is_q) {
+        uint4* to = reinterpret_cast<uint4*>(p.q_out + (c.row0 + r) * p.q_out_stride + at.g * kHeadDim);
+        to[ch.a] = narrow(a);
+        to[ch.b] = narrow(b);
+      } else {
         all = max(all, __float_as_uint(top_of(top_of(0.f, a), b)));
         drop_nonfinite(a);
         drop_nonfinite(b);
         top = max(top, __float_as_uint(top_of(top_of(0.f, a), b)));
       }
-    if (all >= kInf) report(p.dev_err, PKV_DEV_NONFINITE);
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (stores) {
-      const float scale = fmaxf(before, __fdiv_rn(__uint_as_float(top), Code::kMax));
-      const float inv = inverse_of(scale);
-      if (scale > before && c.r0 > 0) {   // earlier rows of the block
-        const float ratio = __fdiv_rn(before, scale);
-        for (int r = 0; r < c.r0; ++r) recode16<Code>(at.dst + r * row_elems + 16 * (lane & 7), ratio);
-      }
-#pragma unroll 1
-      for (int r = c.r0; r < c.r1; ++r) {
-        float a[8], b[8];
-        if (!values(r, a, b)) continue;
-        drop_nonfinite(a);
-        drop_nonfinite(b);
-        uint8_t* to = at.dst + r * row_elems;
-        *reinterpret_cast<uint2*>(to + 8 * ch.a) = code8<Code>(a, inv);
-        *reinterpret_cast<uint2*>(to + 8 * ch.b) = code8<Code>(b, inv);
-      }
     }
+    if (stores && all >= kInf) report(p.dev_err, PKV_DEV_NONFINITE);
+  }
+  // and their codes, under the maximum of all of them; the block's scale
+  __device__ __forceinline__ float code(int own, int every, float before) const {
+    const int64_t row_elems = static_cast<int64_t>(qp.r.num_kv_heads) * kHeadDim;
+    const float scale = fmaxf(before, __fdiv_rn(__uint_as_float(top), Code::kMax));
+    const float inv = inverse_of(scale);
+    if (scale > before && c.r0 > 0) {   // earlier rows of the block
+      const float ratio = __fdiv_rn(before, scale);
+      for (int r = own; r < c.r0; r += every)
+        recode16<Code>(at.dst + r * row_elems + 16 * (threadIdx.x & 7), ratio);
+    }
+#pragma unroll 1
+    for (int r = c.r0 + own; r < c.r1; r += every) {
+      float a[8], b[8];
+      if (!values(r, a, b)) continue;
+      drop_nonfinite(a);
+      drop_nonfinite(b);
+      uint8_t* to = at.dst + r * row_elems;
+      *reinterpret_cast<uint2*>(to + 8 * ch.a) = code8<Code>(a, inv);
+      *reinterpret_cast<uint2*>(to + 8 * ch.b) = code8<Code>(b, inv);
+    }
+    return scale;
+  }
+};
+
+// Two or three rows: each 8 lanes take a head of their own, as for one.
+template <class Code, int BS, bool ADJACENT, int AXES>
+__device__ __forceinline__ void append_few(const Q8Params& qp, const Piece& c, int first, int last) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int h0 = first; h0 < last; h0 += 4) {
+    const bool valid = h0 + (lane >> 3) < last;
+    StepHead<Code, ADJACENT, AXES> head(qp, c, BS, min(h0 + (lane >> 3), last - 1));
+    const bool stores = valid && head.stores;
+    const float before = stores && c.r0 > 0 ? *head.at.scale : 0.f;
+    if (valid) head.look(0, 1);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1)
+      head.top = max(head.top, __shfl_xor_sync(0xffffffffu, head.top, o));
+    float scale = 0.f;
+    if (stores) scale = head.code(0, 1, before);
     __syncwarp();   // every lane has read the earlier scale
-    if (stores && (lane & 7) == 0)
-      *at.scale = fmaxf(before, __fdiv_rn(__uint_as_float(top), Code::kMax));
+    if (stores && (lane & 7) == 0) *head.at.scale = scale;
+  }
+}
+
+// More (a chunk that comes with a batch's single tokens): 16 rows at a time, one for each 8
+// lanes of the CTA; of the CTA's heads, unit j takes each (r1 - r0)-th from j on.  With 255
+// single tokens 250 rows take 4.5 us more; done by a unit a block, 18 (16-token blocks) to 82
+// (64).
+template <class Code, int BS, bool ADJACENT, int AXES>
+__device__ __forceinline__ void append_shared(const Q8Params& qp, const Piece& c, int first, int last,
+                                              uint32_t (&tops)[2][kQ8Warps]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, own = threadIdx.x >> 3;
+  int turns = 0;
+#pragma unroll 1
+  for (int h = first + c.nth; h < last; h += c.r1 - c.r0) {
+    StepHead<Code, ADJACENT, AXES> head(qp, c, BS, h);
+    const float before = head.stores && c.r0 > 0 ? *head.at.scale : 0.f;
+    head.look(own, kQ8Warps * 4);
+    if (!head.stores) continue;
+    const uint32_t top = __reduce_max_sync(0xffffffffu, head.top);
+    if (lane == 0) tops[turns & 1][warp] = top;
+    __syncthreads();   // and every thread has read the earlier scale
+    head.top = top;
+#pragma unroll
+    for (int w = 0; w < kQ8Warps; ++w) head.top = max(head.top, tops[turns & 1][w]);
+    ++turns;
+    const float scale = head.code(own, kQ8Warps * 4, before);
+    if (threadIdx.x == 0) *head.at.scale = scale;
   }
 }
 
@@ -282,8 +334,8 @@ __device__ __forceinline__ void append_few(const Q8Params& qp, const Piece& c, i
 // block of 32 or 64 rows is a team of 2 or 4 warps, which join their maxima.  The rotated
 // values stay in 32 bits from the maximum to the codes, while the next head's rows are under
 // way; computed twice instead, at 96 registers, they took 10 to 20 % longer.  Four CTAs an SM
-// (128 registers) for teams, three (0: left to the compiler) where a warp is alone and keeps its cosines in
-// registers: 32-token blocks 46 us (three CTAs: 54), 16-token blocks 110 us (four: 113).
+// (128 registers) for teams, three (0: left to the compiler) where a warp is alone and keeps
+// its cosines in registers: 32-token blocks 46 us (three CTAs: 54), 16-token blocks 110 us (four: 113).
 constexpr int kWarpRows = 16;
 
 // The rows' cosines and sines in shared memory: 8 lanes of a row read a 16-byte chunk each at
@@ -445,7 +497,7 @@ __device__ __forceinline__ void append_rows(const Q8Params& qp, const Piece& c, 
 // One CTA per (unit, range of heads).  A step's code without that of long pieces takes half
 // the registers, so that its CTAs are all there at once.
 template <class Code, int BS, bool ADJACENT, int AXES, bool STEP>
-__global__ void __launch_bounds__(kQ8Warps * 32, STEP ? 8 : BS > 16 ? 4 : 0)
+__global__ void __launch_bounds__(kQ8Warps * 32, STEP ? (AXES == 1 ? 8 : 6) : BS > 16 ? 4 : 0)
     rope_q8_kernel(const Q8Params qp) {
   const RowParams& p = qp.r;
   asm volatile("griddepcontrol.launch_dependents;");
@@ -466,10 +518,15 @@ __global__ void __launch_bounds__(kQ8Warps * 32, STEP ? 8 : BS > 16 ? 4 : 0)
   const int from = first + warp * per, to = min(last, from + per);   // the warp's heads
   if (c.r1 - c.r0 == 1) {
     append_row<Code, BS, ADJACENT, AXES>(qp, c, from, to);
-  } else if constexpr (STEP) {
-    append_few<Code, BS, ADJACENT, AXES>(qp, c, from, to);
+    return;
+  }
+  __shared__ uint32_t tops[2][kQ8Warps];
+  if constexpr (STEP) {
+    if (c.r1 - c.r0 >= 4)
+      append_shared<Code, BS, ADJACENT, AXES>(qp, c, first, last, tops);
+    else if (c.nth == 0)
+      append_few<Code, BS, ADJACENT, AXES>(qp, c, from, to);
   } else {
-    __shared__ uint32_t tops[2][kQ8Warps];
     __shared__ float4 table[BS * 32];
     append_rows<Code, BS, ADJACENT, AXES>(qp, c, first, last, tops, table);
   }

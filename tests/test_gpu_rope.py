@@ -251,6 +251,72 @@ def test_q8_step_after_step(ops, code, new):
         assert np.array_equal(s.cpu().numpy(), scales[n]) and np.array_equal(codes_of(c, code), codes[n])
 
 
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("bs", [8, 16, 32, 64])
+@pytest.mark.parametrize("new,cached", [
+    ([1] * 40 + [70] + [1] * 9, [11 * i % 130 for i in range(50)]),      # a chunk among single tokens
+    ([4, 9, 15, 5, 31], [3, 60, 1, 0, 40]),           # pieces that share their heads, ends of blocks
+    ([30, 1, 0, 25, 64], [0, 64, 5, 63, 0]),          # whole blocks
+])
+def test_q8_long_pieces_of_steps(ops, code, bs, new, cached):
+    """Several rows of a block in a call of few tokens a sequence, a token off the table
+    and values that are not finite among them."""
+    rng = np.random.default_rng([bs, len(new)])
+    Hq, Hkv, rows = 13, 3, 200
+    lens = (np.array(new) + np.array(cached)).astype(np.int32)
+    nb, tables = batch(rng, lens, bs)
+    qs, T = starts(new), int(np.sum(new))
+    (q, k, v), (tq, tk, tv) = projection(rng, T, Hq, Hkv)
+    table, axes = table_of(64, rows, seed=2), axes_of(64, 3, rng)
+    pos = rng.integers(0, rows, (3, T)).astype(np.int32)
+    seq, place = orope.places(qs, lens, T)
+    s_long = int(np.argmax(new))
+    out, bad = int(qs[s_long]) + 2, int(qs[s_long]) + 3
+    k, v = k.copy(), v.copy()
+    k[bad, 1, 40], v[bad, 2, 7] = np.inf, np.nan
+    tk, tv = dev(k), dev(v)
+    codes = {n: oq.nearest_code(rng.standard_normal((nb, bs, Hkv, D)) * 40, code) for n in "kv"}
+    scales = {n: (np.abs(rng.standard_normal((nb, 4))) * 0.02).astype(np.float32) for n in "kv"}
+    with np.errstate(invalid="ignore"):
+        x = {"k": orope.rotate(k, pos, table, axes), "v": v.astype(np.float32)}
+
+    def call(pos):
+        t = {n: codes_to_dev(codes[n], code) for n in "kv"}
+        sc = {n: dev(scales[n]) for n in "kv"}
+        qo = torch.full((T, Hq, D), 7.0, dtype=torch.float16, device="cuda")
+        err = ops.new_error_word()
+        ops.rope_and_cache_q8(qo, tq, tk, tv, dev(qs), dev(tables), dev(lens), t["k"], t["v"],
+                              sc["k"], sc["v"], dev(table), positions=dev(pos), axes=axes, dev_err=err)
+        return qo.cpu().numpy(), t, sc, ops.read_error_word(err)
+
+    qo, t, sc, err = call(pos)
+    assert err == 8
+    want = {n: (codes[n].copy(), scales[n].copy()) for n in "kv"}
+    for n in "kv":
+        oq.write(x[n], qs, tables, lens, *want[n], bs, code)
+        assert np.array_equal(sc[n].cpu().numpy(), want[n][1])
+        assert np.array_equal(codes_of(t[n], code), want[n][0])
+    assert np.array_equal(bits(qo), bits(orope.rotate(q, pos, table, axes)))
+    # a token off the table on one axis: its q and its codes as they were, all else as before
+    off = pos.copy()
+    off[2, out] = rows
+    qo, t, sc, err = call(off)
+    assert err in (5, 8) and (qo[out] == 7).all()
+    keep = np.arange(T) != out
+    assert np.array_equal(bits(qo[keep]), bits(orope.rotate(q, pos, table, axes)[keep]))
+    blk, row = tables[s_long, place[out] // bs], place[out] % bs
+    for n in "kv":
+        y = x[n].copy()
+        y[out] = 0
+        c, s = codes[n].copy(), scales[n].copy()
+        oq.write(y, qs, tables, lens, c, s, bs, code)
+        got = codes_of(t[n], code)
+        assert np.array_equal(sc[n].cpu().numpy(), s)
+        assert np.array_equal(got[blk, row], codes[n][blk, row])
+        got[blk, row] = c[blk, row]
+        assert np.array_equal(got, c)
+
+
 @pytest.mark.parametrize("T,S", [(3, 3), (40, 3)])
 def test_q8_not_finite_and_bad_metadata(ops, T, S):
     rng = np.random.default_rng(T)
