@@ -603,7 +603,7 @@ int pkv_rope_and_cache(void* q_out, const void* q, const void* k, const void* v,
  * the code, and on v.  block_size 8, 16, 32 or 64.  Values of k that are not finite
  * after the rotation, and such values of v, are stored as 0 and reported
  * (PKV_DEV_NONFINITE); a token that is left out for its position takes no part in its
- * block's scale; codes under a scale below 2^-126 are 0.
+ * block's scale (0 for a block that begins with such tokens alone); codes under a scale below 2^-126 are 0.
  */
 int pkv_rope_and_cache_q8(void* q_out, const void* q, const void* k, const void* v,
                           int64_t q_out_stride, int64_t q_stride, int64_t k_stride,

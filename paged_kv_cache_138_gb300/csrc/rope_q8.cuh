@@ -159,16 +159,17 @@ __device__ __forceinline__ void append_row(const Q8Params& qp, const Piece& c, i
   if (ok && ch.turns) load_turn<ADJACENT>(p.rot, ch, pos, cs);
 #pragma unroll 1
   for (int h0 = first; h0 < last; h0 += 4) {
-    const bool valid = h0 + (lane >> 3) < last && ok;
+    const bool there = h0 + (lane >> 3) < last, valid = there && ok;
     const HeadAt at(qp, c, BS, min(h0 + (lane >> 3), last - 1));
-    const bool stores = valid && !at.is_q && c.blk >= 0;
+    // a token that is left out still starts its block's scale, at 0: it would be its last owner's
+    const bool scales = there && !at.is_q && c.blk >= 0, stores = scales && ok;
     uint4 xa = make_uint4(0u, 0u, 0u, 0u), xb = xa;
     if (valid) {
       const uint4* from = reinterpret_cast<const uint4*>(at.src + token * at.stride);
       xa = from[ch.a];
       xb = from[ch.b];
     }
-    const float before = stores && c.r0 > 0 ? *at.scale : 0.f;
+    const float before = scales && c.r0 > 0 ? *at.scale : 0.f;
     float a[8], b[8];
     widen(xa, a);
     widen(xb, b);
@@ -199,7 +200,7 @@ __device__ __forceinline__ void append_row(const Q8Params& qp, const Piece& c, i
       *reinterpret_cast<uint2*>(to + 8 * ch.b) = code8<Code>(b, inv);
     }
     __syncwarp();   // every lane has read the earlier scale
-    if (stores && (lane & 7) == 0) *at.scale = scale;
+    if (scales && (lane & 7) == 0) *at.scale = scale;
   }
 }
 

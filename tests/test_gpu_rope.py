@@ -317,6 +317,35 @@ def test_q8_long_pieces_of_steps(ops, code, bs, new, cached):
         assert np.array_equal(got, c)
 
 
+@pytest.mark.parametrize("bs", [8, 32])
+@pytest.mark.parametrize("n", [1, 2, 7, 70])
+def test_q8_left_out_tokens_start_a_block(ops, n, bs):
+    """A block that held another sequence's tokens, whose new first tokens are all left out:
+    its scale starts again, and the next token gets one of its own."""
+    rng = np.random.default_rng(n)
+    Hq, Hkv, rows = 4, 2, 50
+    table = table_of(64, rows)
+    nb = n // bs + 2
+    tables = rng.permutation(nb).astype(np.int32)[None, :(n + 1 + bs - 1) // bs]
+    (q, k, v), (tq, tk, tv) = projection(rng, n + 1, Hq, Hkv)
+    pos = np.array([rows] * n + [3], np.int32)
+    cache = ops.q8_cache(nb, Hkv, bs)
+    cache[2].fill_(5.0), cache[3].fill_(5.0)
+    err = ops.new_error_word()
+    for a, b in ((0, n), (n, n + 1)):
+        qo = torch.empty((b - a, Hq, D), dtype=torch.float16, device="cuda")
+        ops.rope_and_cache_q8(qo, tq[a:b], tk[a:b], tv[a:b], dev(starts([b - a])), dev(tables),
+                              dev(np.array([b], np.int32)), *cache, dev(table),
+                              positions=dev(pos[a:b]), dev_err=err)
+        assert ops.read_error_word(err) == 5
+    blk = tables[0, n // bs]
+    for x, c, s in ((orope.rotate(k[n:], pos[n:], table), cache[0], cache[2]),
+                    (v[n:].astype(np.float32), cache[1], cache[3])):
+        amax = np.abs(x[0]).max(axis=-1).astype(np.float32)
+        assert np.array_equal(s[blk, :Hkv].cpu().numpy(), amax / np.float32(127))
+        assert (codes_of(c, "int8")[tables[0], :].reshape(-1, Hkv, D)[:n] == 0).all()
+
+
 @pytest.mark.parametrize("T,S", [(3, 3), (40, 3)])
 def test_q8_not_finite_and_bad_metadata(ops, T, S):
     rng = np.random.default_rng(T)
