@@ -24,13 +24,15 @@
 //  * What bounds it: a query tile's softmax (1550 cycles a tile of 128 tokens, 500 of its
 //    scheduler's instructions being the widening's) and its own products (1024) follow one
 //    another, 2800 cycles a turn where the tensor core is busy for 2048.  16,384 tokens of 32/8
-//    heads, int8: 1304 us in short runs, 1371-1412 in loops of seconds, 1.56-1.69 PFLOP/s (fp16
-//    cache: 1180-1310 and 1370-1460); 16 x 2048 428 us, e4m3 400 (fp16 376); 8 of 64..512 rows
-//    behind 2048, 32 heads, e4m3: 95 us.  4 x 5..8 rows over 30k of 32/8 heads, int8: 78 us, 3.4
-//    TB/s: a tile of codes is widened in 1000 cycles, 550 of them instructions of one warp a
+//    heads, int8: 1283-1305 us in short runs, 1363-1384 in loops of seconds, 1.59-1.71 PFLOP/s
+//    (fp16 cache: 1180-1310 and 1370-1460); 16 x 2048 413-422 us, e4m3 399 (fp16 376); 8 of
+//    64..512 rows behind 2048, 32 heads, e4m3: 94 us.  4 x 5..8 rows over 30k of 32/8 heads,
+//    int8: 80 us, 3.2 TB/s: a tile of codes is widened in 1000 cycles, 550 of them instructions of one warp a
 //    scheduler.  Tried and not kept: two warpgroups that widen, in turn or one tile together
 //    (the softmax has 24 registers less; no faster), the next codes read ahead of the
 //    widening (their place comes free later: 10 % slower with few rows).
+#include <cmath>
+
 #include "prompt_q8.cuh"
 
 namespace pkv {
@@ -45,6 +47,11 @@ constexpr int kThreads = 512;                    // 2 softmax warpgroups; 2 copy
 constexpr int kLaunchRegs = 128, kSoftmaxRegs = 200, kOtherRegs = 56;
 static_assert(256 * kSoftmaxRegs + 256 * kOtherRegs <= kThreads * kLaunchRegs, "register split");
 constexpr int kCopyWarp = 8, kMmaWarp = 9, kWorkWarp = 10, kCopyVWarp = 11, kWidenWarp = 12;
+// The next unit is asked for when this one's last tiles are about to be copied.  Asked for as
+// soon as a unit began, a CTA with a long one kept another from those that had none: 16 x 32
+// rows over 4096 78 us instead of 48, 4 x 70..563 over 0..16,000 337 for 273, 16 x 2048 430 for
+// 420 (2, 4 and 8 tiles ahead are alike).
+constexpr int kAhead = 4;
 constexpr int kReaders = 15;                     // warps that read a unit's description
 // Scale entries of a tile, one for each `gran` tokens, in a ring: a tile's are written
 // before its K is waited for and read until its weights are done.  K of the tile kSlots
@@ -86,7 +93,8 @@ struct Layout {
   static constexpr int lm_free = lm_full + 8;            // and read, tile 1's output too
   static constexpr int unit_full = lm_free + 8;          // the next unit is described
   static constexpr int unit_empty = unit_full + 8;       // and every warp has read it
-  static constexpr int stolen = unit_empty + 8;          // the scheduler's answer is there
+  static constexpr int near_end = unit_empty + 8;        // most of a unit's copies are under way
+  static constexpr int stolen = near_end + 8;            // the scheduler's answer is there
   static constexpr int drained = stolen + 8;
   static constexpr int answer = (drained + 8 + 15) / 16 * 16;
   static constexpr int unit = answer + 16;
@@ -176,6 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(Smem::lm_free, 0), 4);
     mbar_init(bar(Smem::unit_full, 0), 1);
     mbar_init(bar(Smem::unit_empty, 0), kReaders);
+    mbar_init(bar(Smem::near_end, 0), 1);
     mbar_init(bar(Smem::stolen, 0), 1);
     mbar_init(bar(Smem::drained, 0), 1);
     *gave_up = 0;
@@ -239,6 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int i = 0; i < n && ok; ++i) {
           const int j = u.last - 1 - i, in_batch = i % kBatch;
+          if (!mine && i == max(0, n - kAhead) && lane == 0) mbar_arrive(bar(Smem::near_end, 0));
           if (in_batch == 0) {
             if (i > 0) {
               ids = ids1;
@@ -558,7 +568,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
           if (bx < 0) break;
-          ok = wait(bar(Smem::unit_empty, 0), published & 1);
+          ok = wait(bar(Smem::unit_empty, 0), published & 1) &&
+               wait(bar(Smem::near_end, 0), published & 1);
           ++published;
           if (!ok) break;
         }
@@ -925,6 +936,38 @@ int launch_any(int block_size, const Maps& m, const Q8Params& qp, dim3 grid, cud
 // 2000 to 3000 cycles)
 static_assert(kMaxContext / kTile * 4000 <= kWaitLimit / 2, "a unit of the longest context");
 
+// Splits of the key axis for units of one query tile, by a model of the time in key tiles
+// (1.2 us): a unit takes its tiles and one to four (128 rows), partials what they write and
+// read, the merge four.  What counts is the sum for contexts that are all as long as the
+// table and for contexts of every length up to it, where a unit is half as long on average
+// and the last one ends half a unit late.  int8, 32/8 heads, against two units for each SM by
+// the largest number of units: 4 x 8 rows over 32,760 81 us (92), 4 x 5..8 over 30k to 32.7k
+// 80 (78), 1 x 20 over 32k 34 (43), 16 x 16 over 0..16,000 106 (133), 7 x 7..56 over 0..16,000
+// 70 (75), 4 x 32 over 16,384 58 (50).  Units of two tiles keep that rule: their partials are
+// larger (8 x 128 over 8192 as three splits 142 us instead of 104).
+void cut_axis(Plan* plan, int num_tokens, int num_seqs, int num_kv_heads, int group_shift,
+              int64_t max_context) {
+  const int64_t all = (max_context + kTile - 1) / kTile;
+  const double units = static_cast<double>(num_seqs) * num_kv_heads;   // mostly one a sequence
+  const double rows = static_cast<double>(num_tokens) * (num_kv_heads << group_shift);
+  const double filled = rows / (units * kTile);   // of a unit's rows
+  const int most = static_cast<int>(std::min<int64_t>(32, std::max<int64_t>(1, all / kMinSplitTiles)));
+  double least = 0;
+  for (int s = 1; s <= most; ++s) {
+    const int64_t per = (all + s - 1) / s;
+    const int splits = static_cast<int>((all + per - 1) / per);
+    const double unit = per + 1 + 3 * filled;
+    const double alike = std::ceil(units * splits / kSms) * unit;
+    const double mixed = std::max(unit, units * splits * unit / (2 * kSms) + unit / 2);
+    // 1040 bytes a row and split, 8.2 MB in a tile's time
+    const double time = alike + mixed + (splits > 1 ? 2 * (4 + rows * splits / 7900) : 0);
+    if (s > 1 && time >= least) continue;
+    least = time;
+    plan->splits = splits;
+    plan->split_tiles = static_cast<int>(per);
+  }
+}
+
 Plan plan_of(int num_tokens, int num_seqs, int num_kv_heads, int group_shift, int64_t max_context) {
   const int64_t rows = static_cast<int64_t>(num_tokens) << group_shift;   // of a KV head
   // Both kernels work for any batch; the rules go by the average sequence.  16 rows, 64 x 4096
@@ -934,7 +977,10 @@ Plan plan_of(int num_tokens, int num_seqs, int num_kv_heads, int group_shift, in
   Plan plan = {};
   plan.tiles = rows <= static_cast<int64_t>(num_seqs) * kTile ? 1 : 2;
   plan.units = units_for(num_tokens, num_seqs, group_shift, plan.tiles);
-  plan.splits = splits_for(plan.units * num_kv_heads, max_context, &plan.split_tiles);
+  if (plan.tiles == 1)
+    cut_axis(&plan, num_tokens, num_seqs, num_kv_heads, group_shift, max_context);
+  else
+    plan.splits = splits_for(plan.units * num_kv_heads, max_context, &plan.split_tiles);
   return plan;
 }
 

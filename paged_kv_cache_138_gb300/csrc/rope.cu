@@ -343,11 +343,13 @@ extern "C" int pkv_rope_and_cache_q8(void* q_out, const void* q, const void* k, 
   const int64_t heads = num_q_heads + 2ll * num_kv_heads;
   const int64_t units =
       step ? num_tokens : static_cast<int64_t>(num_tokens) / block_size + 2ll * num_seqs;
-  // a step's heads are spread over as many warps as there are; a prompt's stay together, as
-  // they share cosines and sines, as long as there are two rounds of CTAs (four are 3 to 6 %
-  // slower on prompts of 32/8 and 32/32 heads)
-  constexpr int64_t kLeast = 4 * kQ8Warps, kRounds = 152 * 4 * 2;
-  const int64_t parts = step ? heads : (kRounds + units - 1) / units;
+  // A token's heads share its cosines and the search for its place: they stay together as
+  // long as there are two rounds of CTAs (prompts of 32/8 and 32/32 heads: four rounds are 3 to
+  // 6 % slower; steps of 32/32: 1024 tokens 13 us, with CTAs of 16 heads 17, with one round 12,
+  // but 128 x 3 tokens 12 instead of 9).
+  constexpr int64_t kLeast = 4 * kQ8Warps;
+  const int64_t rounds = 2 * 152 * (step ? 8 : 4);
+  const int64_t parts = (rounds + units - 1) / units;
   const int64_t per = std::max(kLeast, (heads + parts * kLeast - 1) / (parts * kLeast) * kLeast);
   p.heads_per_cta = static_cast<int>(per);
   if (units >= INT32_MAX || (heads + per - 1) / per > 65535) return PKV_ERR_UNSUPPORTED;
