@@ -941,29 +941,29 @@ static_assert(kMaxContext / kTile * 4000 <= kWaitLimit / 2, "a unit of the longe
 // read, the merge four.  What counts is the sum for contexts that are all as long as the
 // table and for contexts of every length up to it, where a unit is half as long on average
 // and the last one ends half a unit late.  int8, 32/8 heads, against two units for each SM by
-// the largest number of units: 4 x 8 rows over 32,760 81 us (92), 4 x 5..8 over 30k to 32.7k
-// 80 (78), 1 x 20 over 32k 34 (43), 16 x 16 over 0..16,000 106 (133), 7 x 7..56 over 0..16,000
-// 70 (75), 4 x 32 over 16,384 58 (50).  Units of two tiles keep that rule: their partials are
-// larger (8 x 128 over 8192 as three splits 142 us instead of 104).
+// the largest number of units that there can be: 4 x 8 rows over 32,760 81 us (92), 4 x 5..8 over
+// 30k to 32.7k 80 (78), 1 x 20 over 32k 34 (43), 16 x 16 over 0..16,000 98 (133), 7 x 7..56 over
+// 0..16,000 62 (67), 4 x 32 over 16,384, e4m3, 54 (47).  Units of two tiles keep that rule: by the
+// model 4 x 200 over 8000 took 132 us (121), 1 x 200 over 3000 40 (31).
 void cut_axis(Plan* plan, int num_tokens, int num_seqs, int num_kv_heads, int group_shift,
               int64_t max_context) {
   const int64_t all = (max_context + kTile - 1) / kTile;
   const double units = static_cast<double>(num_seqs) * num_kv_heads;   // mostly one a sequence
   const double rows = static_cast<double>(num_tokens) * (num_kv_heads << group_shift);
-  const double filled = rows / (units * kTile);   // of a unit's rows
-  const int most = static_cast<int>(std::min<int64_t>(32, std::max<int64_t>(1, all / kMinSplitTiles)));
+  // as many as fill the SMs three times, eight at least, of two tiles or more
+  const int64_t most = std::min(std::max<int64_t>(1, all / 2),
+                                std::max<int64_t>(8, static_cast<int64_t>(3 * kSms / units)));
   double least = 0;
-  for (int s = 1; s <= most; ++s) {
-    const int64_t per = (all + s - 1) / s;
-    const int splits = static_cast<int>((all + per - 1) / per);
-    const double unit = per + 1 + 3 * filled;
+  for (int64_t s = 1; s <= most; ++s) {
+    const int64_t per = (all + s - 1) / s, splits = (all + per - 1) / per;
+    const double unit = per + 1 + 3 * rows / (units * kTile);
     const double alike = std::ceil(units * splits / kSms) * unit;
     const double mixed = std::max(unit, units * splits * unit / (2 * kSms) + unit / 2);
     // 1040 bytes a row and split, 8.2 MB in a tile's time
     const double time = alike + mixed + (splits > 1 ? 2 * (4 + rows * splits / 7900) : 0);
     if (s > 1 && time >= least) continue;
     least = time;
-    plan->splits = splits;
+    plan->splits = static_cast<int>(splits);
     plan->split_tiles = static_cast<int>(per);
   }
 }
@@ -971,8 +971,11 @@ void cut_axis(Plan* plan, int num_tokens, int num_seqs, int num_kv_heads, int gr
 Plan plan_of(int num_tokens, int num_seqs, int num_kv_heads, int group_shift, int64_t max_context) {
   const int64_t rows = static_cast<int64_t>(num_tokens) << group_shift;   // of a KV head
   // Both kernels work for any batch; the rules go by the average sequence.  16 rows, 64 x 4096
-  // tokens, e4m3: 119 us and 132 here; 32 rows: 168 and 130.
-  if (rows <= 16ll * num_seqs)
+  // tokens, e4m3: 119 us and 132 here; 32 rows: 168 and 130.  Contexts of one tile whose units
+  // are all there at once take less time in the other kernel (5 of 7..63 rows, 8 heads 5.8 us
+  // and 8.9 here; 4 x 64 of 32/8 heads, more units than places, 14 and 9.3).
+  const int64_t few = (rows / 16 + num_seqs) * num_kv_heads;   // units of the other kernel
+  if (rows <= 16ll * num_seqs || (max_context <= kTile && few <= 3 * kSms))
     return few_rows_plan(num_tokens, num_seqs, num_kv_heads, group_shift, max_context);
   Plan plan = {};
   plan.tiles = rows <= static_cast<int64_t>(num_seqs) * kTile ? 1 : 2;
