@@ -343,15 +343,22 @@ extern "C" int pkv_rope_and_cache_q8(void* q_out, const void* q, const void* k, 
   const int64_t heads = num_q_heads + 2ll * num_kv_heads;
   const int64_t units =
       step ? num_tokens : static_cast<int64_t>(num_tokens) / block_size + 2ll * num_seqs;
-  // A token's heads share its cosines and the search for its place: they stay together as
-  // long as there are two rounds of CTAs (prompts of 32/8 and 32/32 heads: four rounds are 3 to
-  // 6 % slower; steps of 32/32: 1024 tokens 13 us, with CTAs of 16 heads 17, with one round 12,
-  // but 128 x 3 tokens 12 instead of 9).
-  constexpr int64_t kLeast = 4 * kQ8Warps;
+  // A token's heads share its cosines and the search for its place: they are cut apart where
+  // that makes no more than two rounds of CTAs (blocks of 8 and 16 and single warps: about two).
+  // Prompts of 32/8 and 32/32 heads: four rounds are 3 to 6 % slower; 32-token blocks, 32/32
+  // heads: 46 us of two, as three 50; 8-token blocks, 2 x 3000 of 32/8: 30 us of three, as one
+  // and a half 34.  Steps of 32/32 heads: 1024 tokens 12 us, in CTAs of 16 heads 17.  Few long
+  // chunks: 64 rows of 32/8 heads in 64-token blocks 4.6 us, in CTAs of 16 heads 22, of 4 heads 8.4.
+  const int64_t least =   // 4 heads for each of a step's warps, one for each team of a chunk's
+      step ? 4 * kQ8Warps : block_size == 64 ? 1 : block_size == 32 ? 2 : kQ8Warps;
   const int64_t rounds = 2 * 152 * (step ? 8 : 4);
-  const int64_t parts = (rounds + units - 1) / units;
-  const int64_t per = std::max(kLeast, (heads + parts * kLeast - 1) / (parts * kLeast) * kLeast);
+  // of two units to spare for a sequence one is empty
+  const int64_t likely = std::max<int64_t>(1, step ? units : units - num_seqs);
+  const bool teams = !step && block_size > 16;
+  const int64_t parts = std::max<int64_t>(1, (rounds + (teams ? 0 : likely - 1)) / likely);
+  const int64_t per = (heads + parts * least - 1) / (parts * least) * least;
   p.heads_per_cta = static_cast<int>(per);
+  p.heads_per_warp = static_cast<int>((per + kQ8Warps - 1) / kQ8Warps);
   if (units >= INT32_MAX || (heads + per - 1) / per > 65535) return PKV_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(units + 1), static_cast<unsigned>((heads + per - 1) / per));
   return (code == PKV_CODE_INT8 ? launch_q8_int8 : launch_q8_e4m3)(p, step, adjacent != 0, block_size,

@@ -155,7 +155,7 @@ struct Q8Params {
   uint8_t *k_codes, *v_codes;
   float *k_scale, *v_scale;    // [num_blocks, scale_stride]
   int scale_stride;
-  int heads_per_cta;           // a multiple of 4 kQ8Warps
+  int heads_per_cta, heads_per_warp;   // of single rows
 };
 
 // launches of the 8-bit kernels, a translation unit each

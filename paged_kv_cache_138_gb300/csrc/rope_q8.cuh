@@ -515,8 +515,9 @@ __global__ void __launch_bounds__(kQ8Warps * 32, STEP ? (AXES == 1 ? 8 : 6) : BS
   if (c.blk < 0 && threadIdx.x == 0) report(p.dev_err, PKV_DEV_BAD_BLOCK_ID);
   const int first = blockIdx.y * qp.heads_per_cta;
   const int last = min(first + qp.heads_per_cta, p.num_q_heads + 2 * p.num_kv_heads);
-  const int per = qp.heads_per_cta / kQ8Warps, warp = threadIdx.x >> 5;
-  const int from = first + warp * per, to = min(last, from + per);   // the warp's heads
+  // the warp's heads
+  const int from = first + (threadIdx.x >> 5) * qp.heads_per_warp;
+  const int to = min(last, from + qp.heads_per_warp);
   if (c.r1 - c.r0 == 1) {
     append_row<Code, BS, ADJACENT, AXES>(qp, c, from, to);
     return;
