@@ -334,10 +334,10 @@ extern "C" int pkv_rope_and_cache_q8(void* q_out, const void* q, const void* k, 
   p.k_scale = k_scale;
   p.v_scale = v_scale;
   p.scale_stride = scale_stride;
-  // A step's way does rows twice, the long chunks' a whole block whatever is new of it: 128 x 4
-  // tokens of 32/8 heads 10.6 to 11.9 us against 7.4, 9.2, 16 and 29 in blocks of 8 to 64; 64 x
-  // 15 11 (16-token blocks 13) against 8.4, 16 and 27, 256 x 15 33 against 28 and 48 (32, 64);
-  // 256 x 30 71 against 45 and 77.
+  // A step's way does rows twice, the long chunks' a whole block whatever is new of it.  Of 32/8
+  // heads, in blocks of 16, 32 and 64: 128 x 4 tokens 10.5 to 11.5 us against 10, 14 and 23; 64 x
+  // 15 12, 10 and 10 against 9, 11 and 16; 256 x 15 35, 26 and 26 against 26, 29 and 50; 256 x 30
+  // in 64-token blocks 59 against 82.
   const int few = block_size == 64 ? 32 : block_size == 32 ? 8 : 4;   // tokens a sequence
   const bool step = num_tokens < static_cast<int64_t>(few) * num_seqs;
   const int64_t heads = num_q_heads + 2ll * num_kv_heads;
