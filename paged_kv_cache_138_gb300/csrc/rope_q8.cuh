@@ -25,8 +25,7 @@ struct Piece {
 
 // Units are cut in one of two ways.  Long chunks: the write's units of BS rows, numbered
 // without a prefix sum, two to spare for each sequence.  Steps (few tokens a
-// sequence on average): every token is a unit; the first of a piece of two or three rows does
-// them all, those of a longer one share its heads.
+// sequence on average): every token is a unit, and the units of a piece share its heads.
 template <int BS, bool STEP>
 __device__ __forceinline__ bool find_piece(const Q8Params& qp, Piece& c) {
   const RowParams& p = qp.r;
@@ -130,6 +129,18 @@ struct E4m3Near : E4m3Code {
   }
 };
 
+// The barrier of a team of two warps, or of all four.  Numbers that the compiler sees: with one
+// in a register a CTA holds all 16 barriers, and an SM has room for half as many CTAs (a step
+// of 256 tokens 5.4 us instead of 4.6).
+__device__ __forceinline__ void join_team(int team, bool all) {
+  if (all)
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+  else if (team == 0)
+    asm volatile("bar.sync 1, 64;" ::: "memory");
+  else
+    asm volatile("bar.sync 2, 64;" ::: "memory");
+}
+
 // 16 codes of a row under a scale that has grown
 template <class Code>
 __device__ __forceinline__ void recode16(uint8_t* at, float ratio) {
@@ -204,8 +215,8 @@ __device__ __forceinline__ void append_row(const Q8Params& qp, const Piece& c, i
   }
 }
 
-// Several rows in a step, one after another and twice, for the maximum and for the codes: what
-// is in registers then does not depend on how many there are.
+// More than 16 rows in a step, one after another and twice, for the maximum and for the codes:
+// what is in registers then does not depend on how many there are.
 template <class Code, bool ADJACENT, int AXES>
 struct StepHead {
   const Q8Params& qp;
@@ -281,24 +292,80 @@ struct StepHead {
   }
 };
 
-// Two or three rows: each 8 lanes take a head of their own, as for one.
+// Up to 16 rows: a head is a team of 1, 2 or 4 warps, 8 lanes a row, whose values stay in
+// registers from the maximum to the codes; unit j of n takes each n-th group of heads.
 template <class Code, int BS, bool ADJACENT, int AXES>
-__device__ __forceinline__ void append_few(const Q8Params& qp, const Piece& c, int first, int last) {
-  const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void append_held(const Q8Params& qp, const Piece& c, int first, int last,
+                                            uint32_t (&tops)[2][kQ8Warps]) {
+  const RowParams& p = qp.r;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = c.r1 - c.r0;
+  const int shift = n <= 4 ? 0 : n <= 8 ? 1 : 2, warps = 1 << shift, teams = kQ8Warps >> shift;
+  const int team = warp >> shift, own = (warp & (warps - 1)) * 4 + (lane >> 3);
+  const Chunks ch(lane & 7, p.rot.n);
+  const int64_t row_elems = static_cast<int64_t>(p.num_kv_heads) * kHeadDim;
+  const int row = c.row0 + c.r0 + own;   // packed
+  bool in = own < n;
+  float4 cs[4];
+  if (in) {
+    int32_t pos[AXES];
+    load_positions(p.rot, row, c.base + c.r0 + own, pos);
+    in = on_table(p.rot, pos);
+    if (!in) report(p.dev_err, PKV_DEV_BAD_POSITION);
+    if (in && ch.turns) load_turn<ADJACENT>(p.rot, ch, pos, cs);
+  }
+  int turns = 0;
 #pragma unroll 1
-  for (int h0 = first; h0 < last; h0 += 4) {
-    const bool valid = h0 + (lane >> 3) < last;
-    StepHead<Code, ADJACENT, AXES> head(qp, c, BS, min(h0 + (lane >> 3), last - 1));
-    const bool stores = valid && head.stores;
-    const float before = stores && c.r0 > 0 ? *head.at.scale : 0.f;
-    if (valid) head.look(0, 1);
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1)
-      head.top = max(head.top, __shfl_xor_sync(0xffffffffu, head.top, o));
-    float scale = 0.f;
-    if (stores) scale = head.code(0, 1, before);
-    __syncwarp();   // every lane has read the earlier scale
-    if (stores && (lane & 7) == 0) *head.at.scale = scale;
+  for (int h = first + c.nth * teams + team; h < last; h += n * teams) {
+    const HeadAt at(qp, c, BS, h);
+    const bool stores = !at.is_q && c.blk >= 0;
+    uint4 xa = make_uint4(0u, 0u, 0u, 0u), xb = xa;
+    if (in) {
+      const uint4* from = reinterpret_cast<const uint4*>(at.src + row * at.stride);
+      xa = from[ch.a];
+      xb = from[ch.b];
+    }
+    const float before = stores && c.r0 > 0 ? *at.scale : 0.f;
+    float a[8], b[8];
+    widen(xa, a);
+    widen(xb, b);
+    if (in && !at.is_v && ch.turns) rotate<ADJACENT>(a, b, cs);
+    if (at.is_q) {
+      if (in) {
+        uint4* to = reinterpret_cast<uint4*>(p.q_out + row * p.q_out_stride + at.g * kHeadDim);
+        to[ch.a] = narrow(a);
+        to[ch.b] = narrow(b);
+      }
+      continue;
+    }
+    if (!stores) continue;
+    uint32_t top = __float_as_uint(top_of(top_of(0.f, a), b));
+    if (top >= kInf) {
+      report(p.dev_err, PKV_DEV_NONFINITE);
+      drop_nonfinite(a);
+      drop_nonfinite(b);
+      top = __float_as_uint(top_of(top_of(0.f, a), b));
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (shift > 0) {
+      if (lane == 0) tops[turns & 1][warp] = top;
+      join_team(team, shift == 2);
+      for (int w = 0; w < warps; ++w) top = max(top, tops[turns & 1][team * warps + w]);
+      ++turns;
+    }
+    const float scale = fmaxf(before, __fdiv_rn(__uint_as_float(top), Code::kMax));
+    const float inv = inverse_of(scale);
+    if (scale > before && c.r0 > 0) {   // earlier rows of the block
+      const float ratio = __fdiv_rn(before, scale);
+      for (int r = own; r < c.r0; r += 4 << shift)
+        recode16<Code>(at.dst + r * row_elems + 16 * (lane & 7), ratio);
+    }
+    if (in) {
+      uint8_t* to = at.dst + (c.r0 + own) * row_elems;
+      *reinterpret_cast<uint2*>(to + 8 * ch.a) = code8<Code>(a, inv);
+      *reinterpret_cast<uint2*>(to + 8 * ch.b) = code8<Code>(b, inv);
+    }
+    __syncwarp();   // every lane has read the earlier scale (every warp, before they joined)
+    if (lane == 0 && (warp & (warps - 1)) == 0) *at.scale = scale;
   }
 }
 
@@ -409,7 +476,7 @@ __device__ __forceinline__ void append_rows(const Q8Params& qp, const Piece& c, 
     top = __reduce_max_sync(0xffffffffu, top);
     if (kTeam > 1) {
       if (lane == 0) tops[turns & 1][warp] = top;
-      asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(kTeam * 32) : "memory");
+      join_team(team, kTeam == kQ8Warps);
 #pragma unroll
       for (int w = 0; w < kTeam; ++w) top = max(top, tops[turns & 1][team * kTeam + w]);
       ++turns;
@@ -524,10 +591,10 @@ __global__ void __launch_bounds__(kQ8Warps * 32, STEP ? (AXES == 1 ? 8 : 6) : BS
   }
   __shared__ uint32_t tops[2][kQ8Warps];
   if constexpr (STEP) {
-    if (c.r1 - c.r0 >= 4)
+    if (BS <= 16 || c.r1 - c.r0 <= 16)
+      append_held<Code, BS, ADJACENT, AXES>(qp, c, first, last, tops);
+    else
       append_shared<Code, BS, ADJACENT, AXES>(qp, c, first, last, tops);
-    else if (c.nth == 0)
-      append_few<Code, BS, ADJACENT, AXES>(qp, c, from, to);
   } else {
     __shared__ float4 table[BS * 32];
     append_rows<Code, BS, ADJACENT, AXES>(qp, c, first, last, tops, table);
