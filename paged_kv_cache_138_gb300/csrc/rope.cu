@@ -334,11 +334,11 @@ extern "C" int pkv_rope_and_cache_q8(void* q_out, const void* q, const void* k, 
   p.k_scale = k_scale;
   p.v_scale = v_scale;
   p.scale_stride = scale_stride;
-  // A step's way does rows twice, the long chunks' a whole block whatever is new of it.  Of 32/8
-  // heads, in blocks of 16, 32 and 64: 128 x 4 tokens 10.5 to 11.5 us against 10, 14 and 23; 64 x
-  // 15 12, 10 and 10 against 9, 11 and 16; 256 x 15 35, 26 and 26 against 26, 29 and 50; 256 x 30
-  // in 64-token blocks 59 against 82.
-  const int few = block_size == 64 ? 32 : block_size == 32 ? 8 : 4;   // tokens a sequence
+  // A step's way holds up to 16 rows of a head, the long chunks' a whole block's whatever is new
+  // of it.  Of 32/8 heads, in blocks of 8, 16, 32 and 64: 128 x 4 tokens 6.2 us against 8, 10, 14
+  // and 23; 64 x 15 9.4 to 10 against 8.5, 9, 11 and 16; 256 x 30 45, 50, 55 and 55 against 40,
+  // 42, 49 and 82.
+  const int few = std::max(8, block_size / 2);   // tokens a sequence
   const bool step = num_tokens < static_cast<int64_t>(few) * num_seqs;
   const int64_t heads = num_q_heads + 2ll * num_kv_heads;
   const int64_t units =

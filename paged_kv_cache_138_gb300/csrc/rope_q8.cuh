@@ -369,10 +369,9 @@ __device__ __forceinline__ void append_held(const Q8Params& qp, const Piece& c, 
   }
 }
 
-// More (a chunk that comes with a batch's single tokens): 16 rows at a time, one for each 8
-// lanes of the CTA; of the CTA's heads, unit j takes each (r1 - r0)-th from j on.  With 255
-// single tokens 250 rows take 4.5 us more; done by a unit a block, 18 (16-token blocks) to 82
-// (64).
+// More than 16 rows: 16 at a time, one for each 8 lanes of the CTA, twice; of the CTA's heads,
+// unit j takes each (r1 - r0)-th from j on.  With 255 single tokens a chunk of 250 takes 2.6 us
+// (16-token blocks) to 4.2 (64) more; done by a unit a block, 18 to 82.
 template <class Code, int BS, bool ADJACENT, int AXES>
 __device__ __forceinline__ void append_shared(const Q8Params& qp, const Piece& c, int first, int last,
                                               uint32_t (&tops)[2][kQ8Warps]) {
