@@ -27,10 +27,10 @@
 //    heads, int8: 1283-1305 us in short runs, 1363-1384 in loops of seconds, 1.59-1.71 PFLOP/s
 //    (fp16 cache: 1180-1310 and 1370-1460); 16 x 2048 413-422 us, e4m3 399 (fp16 376); 8 of
 //    64..512 rows behind 2048, 32 heads, e4m3: 94 us.  4 x 5..8 rows over 30k of 32/8 heads,
-//    int8: 80 us, 3.2 TB/s: a tile of codes is widened in 1000 cycles, 550 of them instructions of one warp a
-//    scheduler.  Tried and not kept: two warpgroups that widen, in turn or one tile together
-//    (the softmax has 24 registers less; no faster), the next codes read ahead of the
-//    widening (their place comes free later: 10 % slower with few rows).
+//    int8: 80 us, 3.2 TB/s: a tile of codes is widened in 1000 cycles, 550 of them instructions
+//    of one warp a scheduler.  Tried and not kept: two warpgroups that widen, in turn or one
+//    tile together (the softmax has 24 registers less; no faster), the next codes read ahead
+//    of the widening (their place comes free later: 10 % slower with few rows).
 #include <cmath>
 
 #include "prompt_q8.cuh"
