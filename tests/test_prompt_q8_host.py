@@ -71,3 +71,17 @@ def test_wrapper_refuses(calls, monkeypatch):   # noqa: F811
         with pytest.raises((TypeError, ValueError)):
             fn(**{**good, **change})
     assert calls == []
+
+
+@pytest.mark.parametrize("T,S,Hq,Hkv", [(1, 1, 8, 8), (26, 4, 32, 8), (512, 16, 32, 8), (800, 8, 32, 32),
+                                        (2048, 4, 32, 8), (256, 256, 32, 8), (40, 1, 64, 8)])
+@pytest.mark.parametrize("width", [1, 8, 9, 64, 2048, 1 << 21])
+def test_workspace_is_whole_splits(native_lib, T, S, Hq, Hkv, width):
+    """Partials of 130 floats a row and split, no more splits than the table has tiles of 128
+    tokens, none where it has one."""
+    need = native_lib.pkv_paged_attention_prefill_q8_workspace_bytes(T, S, Hq, Hkv, width, 16)
+    splits, rest = divmod(need, T * Hq * 130 * 4)
+    tiles = -(-width * 16 // 128)
+    assert rest == 0 and splits != 1 and splits <= tiles
+    if tiles == 1:
+        assert need == 0
