@@ -403,6 +403,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       __syncwarp();
     }
     q8_tile<Half, kBoxes>(st, qb, s0, ks, lv, valid, lane, a);
+    // the stage is read before the copy engine writes it again: a warp barrier orders the reads
+    // with other threads' accesses, not with the engine's
+    fence_proxy_async_smem();
     __syncwarp();
     if (issued < mine) {
       issue(issued);
