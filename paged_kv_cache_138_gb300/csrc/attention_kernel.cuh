@@ -408,6 +408,9 @@ struct TileStream {
       ok = __all_sync(kFull, ok && landed) != 0;
       const TileIds t = ids_of(k);
       if (ok && t.a >= 0) f(smem_u32(stages + stage * kStageBytes), tile_begin + warp + k * kWarps, t);
+      // the stage is read before the copy engine writes it again: a warp barrier orders the
+      // reads with other threads' accesses, not with the engine's
+      fence_proxy_async_smem();
       __syncwarp();
       const TileIds nt = ids_of(issued < 32 ? issued : 0);
       if (ok && issued < my_count) {

@@ -8,7 +8,12 @@ import numpy as np
 import pytest
 import torch
 
+import test_gpu_grouped as tg
 import test_gpu_q8 as tq
+from oracle import attention as oa
+from oracle import cache_ops as oc
+from parity_helpers import assert_matches_oracle
+from paged_kv_cache_138_gb300 import workloads as wl
 
 pytestmark = pytest.mark.gpu
 D = 128
@@ -54,3 +59,56 @@ def test_decode_over_8_bit_cache(ops, code, bs, lens, Hq, Hkv):
         outs.append(out)
     for got, (q, codes, scales, tables, lens_) in zip(repeat(launches, outs), cases):
         tq.check_decode(got[:4].astype(np.float64), q[:4], codes, scales, tables[:4], lens_[:4], bs)
+
+
+def paged(seed, lens, Hq, Hkv, bs):
+    rng = np.random.default_rng([seed, bs])
+    nb, tables = tq.batch(rng, lens, bs, pad=-7)
+    q = wl.host_normal_fp16(rng, (len(lens), Hq, D))
+    kc, vc = (wl.host_normal_fp16(rng, (nb, bs, Hkv, D)) for _ in "kv")
+    return q, kc, vc, tables, np.asarray(lens, np.int32)
+
+
+def check(got, q, kc, vc, tables, lens):
+    at = [0, 1, 2, len(lens) - 1]
+    assert_matches_oracle(got[at], oa.paged_attention_decode(q[at], kc, vc, tables[at], lens[at], SCALE))
+
+
+@pytest.mark.parametrize("fused", [False, True])
+@pytest.mark.parametrize("bs", [8, 16, 64])
+@pytest.mark.parametrize("lens,Hq,Hkv", [([1500] * 60, 8, 8), ([4000, 1, 900, 2047] * 10, 8, 2)])
+def test_decode(ops, fused, bs, lens, Hq, Hkv):
+    cases = [paged(s, lens, Hq, Hkv, bs) for s in (60, 61)]
+    outs, launches = [], []
+    for i, (q, kc, vc, tables, lens_) in enumerate(cases):
+        out = torch.empty(q.shape, dtype=torch.float16, device="cuda")
+        new = [wl.host_normal_fp16(np.random.default_rng([i, n]), (len(lens), Hkv, D)) for n in (0, 1)]
+        cache = [dev(kc), dev(vc)]
+        if fused:
+            launches.append(ops.paged_attention_decode_fused(
+                out, dev(q), dev(new[0]), dev(new[1]), *cache, dev(tables), dev(lens_), SCALE,
+                prepare=True))
+            slots = np.array([oc.slot(tables[s], int(L) - 1, bs) for s, L in enumerate(lens)], np.int64)
+            oc.reshape_and_cache(new[0], new[1], slots, kc, vc)
+        else:
+            launches.append(ops.paged_attention_decode(out, dev(q), *cache, dev(tables), dev(lens_),
+                                                       SCALE, prepare=True))
+        outs.append(out)
+    for got, c in zip(repeat(launches, outs), cases):
+        check(got, *c)
+
+
+@pytest.mark.parametrize("bs", [8, 16, 64])
+@pytest.mark.parametrize("Hq,Hkv,groups", [(8, 8, [16, 16, 9]), (32, 8, [4] * 12)])
+def test_grouped(ops, bs, Hq, Hkv, groups):
+    cases = [tg.forked_case(s, groups, Hq, Hkv, bs, 1536, own_min=1) for s in (70, 71)]
+    outs, launches = [], []
+    for q, kc, vc, tables, lens in cases:
+        gf, sg, gs, mx, mo = ops.shared_prefix_groups(tables, lens, bs, 16 // (Hq // Hkv))
+        out = torch.empty(q.shape, dtype=torch.float16, device="cuda")
+        launches.append(ops.paged_attention_decode_grouped(
+            out, dev(q), dev(kc), dev(vc), dev(tables), dev(lens), dev(gf), dev(sg), dev(gs), mx, mo,
+            SCALE, prepare=True))
+        outs.append(out)
+    for got, c in zip(repeat(launches, outs), cases):
+        check(got, *c)
