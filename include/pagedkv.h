@@ -512,13 +512,13 @@ int pkv_paged_attention_decode_q8(void* out, const void* q, const void* k_cache,
  * of a KV head or fewer on average).  All of the context's K and V must already be in the cache
  * (pkv_reshape_and_cache_q8, pkv_rope_and_cache_q8).
  *   k_cache, v_cache  codes, 16-byte aligned; k_scale, v_scale 4-byte aligned
- * Scales must be finite and not negative (a zero scale is a block of zeros; a V scale
- * below 2^-33 counts as 2^-33), and so must the e4m3 codes of a context; codes past the
- * context may be any bytes, scales of blocks past it anything.  fp32 scores, sums and
- * accumulators; the softmax weights, with the V scale folded in, are rounded to fp16 for
- * the product with V (by half a step, or by 2^-32 of the largest), the result once.  A
- * row with a score that is NaN or +infinity (an infinity or NaN in q, a softmax scale
- * that is not finite) is NaN.
+ * Scales must be finite and not negative (a zero scale is a block of zeros, whatever its
+ * codes; a V scale below 2^-60 counts as 2^-60), and so must the e4m3 codes of a context;
+ * codes past the context may be any bytes, scales of blocks past it anything.  fp32 scores,
+ * sums and accumulators; the softmax weights, with the V scale folded in, are rounded to
+ * fp16 for the product with V (by half a step, or by 2^-32 of the largest), the result
+ * once.  A row with a score that is NaN or +infinity (an infinity or NaN in q, a softmax
+ * scale that is not finite), or with none above -infinity, is NaN.
  */
 int pkv_paged_attention_prefill_q8(void* out, const void* q, const void* k_cache,
                                    const void* v_cache, const float* k_scale,

@@ -17,9 +17,11 @@ struct Q8Params {
   int scale_stride;
 };
 
-// V scales from here down count as this one: fp16 values give none as small but 0 (2^-24 /
-// 448 is just above), and what they multiply rounds to 0 in fp16
-constexpr float kLeastScale = 1.f / (1ull << 33), kLeastLog = -33.f;
+// V scales from here down count as this one, 0 among them: what such a block adds to an output,
+// 448 * 2^-60 at most, is nothing in fp16, while its weights, 2^60 times what meets the codes,
+// count in the softmax's sum.  Scales of fp16 values are 0 or from 2^-33 on (2^-24 / 448).  With
+// 2^-33 for the least, e4m3 codes above 256 under a scale of 0 came out as 2^-24.
+constexpr float kLeastScale = 1.f / (1ull << 60), kLeastLog = -60.f;
 
 // four codes as two packed fp16 pairs, exactly
 struct Int8Wide {

@@ -448,3 +448,26 @@ def test_prompts_in_chunks_then_steps(ops, code):
     assert ops.read_error_word(err) == 0
     for t, a in zip(cache, c.codes):
         assert np.array_equal(tq.codes_of(t, code), a)
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("new,cached,width", [([3], [125], 0), ([130, 40], [200, 700], 0),
+                                              ([2, 5], [3000, 40], 200)])
+def test_zero_scales_with_codes_left(ops, code, new, cached, width):
+    """Blocks of scale 0 are zeros whatever codes lie in them (a block that begins with left-out
+    tokens keeps its last owner's): rows that see no other V are exactly 0, others the definition."""
+    largest = {"int8": 127, "e4m3": 448}[code]
+    c = Case(60, new, cached, 8, 2, 16, code, width=width)
+    c.codes[1][:] = largest
+    c.scales[1][:] = 0
+    got, err = c.run(ops)
+    assert err == 0 and (got == 0).all()
+    rng = np.random.default_rng(61)
+    c = Case(62, new, cached, 8, 2, 16, code, width=width)
+    for k in range(2):
+        none = rng.random(c.scales[k].shape) < 0.5
+        c.scales[k][none] = 0
+        c.codes[k] = np.where(none[:, None, :2, None], -largest, c.codes[k])
+    got, err = c.run(ops)
+    assert err == 0
+    c.check(got)
