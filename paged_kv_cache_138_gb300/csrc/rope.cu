@@ -139,7 +139,7 @@ int make_rotation(Rotation* r, const int32_t* positions, int num_axes, const uin
     return PKV_ERR_UNSUPPORTED;
   *r = {};
   r->n = rot_dim / 2;
-  r->num_axes = axes ? num_axes : 1;
+  r->num_axes = num_axes;   // all are looked at, whatever axes the pairs follow
   if (axes)
     for (int j = 0; j < r->n; ++j) {
       if (axes[j] >= num_axes) return PKV_ERR_INVALID_ARG;

@@ -588,3 +588,54 @@ def test_many_sequences_and_heads(ops):
     ref = np.zeros((nb, bs, Hkv, D), np.float16)
     ref[tables[seq, place // bs], place % bs] = orope.rotate(k, place, table).astype(np.float16)
     assert np.array_equal(bits(kc.cpu().numpy()), bits(ref))
+
+
+@pytest.mark.parametrize("adjacent", [0, 1])
+def test_positions_of_axes_that_no_pair_follows(ops, native_lib, adjacent):
+    """C callers that pass several axes and no axes of the pairs: every pair follows axis 0, and a
+    position off the table on any axis leaves its token out, as where the pairs name their axes."""
+    rng = np.random.default_rng(8)
+    T, Hq, Hkv, bs = 9, 4, 2, 16
+    lens, qs = np.array([4, 5], np.int32), starts([4, 5])
+    nb, tables = batch(rng, lens, bs)
+    (q, k, _), (tq, tk, tv) = projection(rng, T, Hq, Hkv)
+    table = table_of(64, 50)
+    pos = rng.integers(0, 50, (3, T)).astype(np.int32)
+    pos[0, 1], pos[1, 4], pos[2, 6] = 50, -1, 50
+    gone = np.isin(np.arange(T), [1, 4, 6])
+    d = [dev(a) for a in (pos, table, qs, tables, lens)]
+    p = [t.data_ptr() for t in d]
+    st = torch.cuda.current_stream().cuda_stream
+    stride = (Hq + 2 * Hkv) * D
+
+    def run(name):
+        qo = torch.full((T, Hq, D), 7.0, dtype=torch.float16, device="cuda")
+        ko = torch.full((T, Hkv, D), 7.0, dtype=torch.float16, device="cuda")
+        err = ops.new_error_word()
+        rot = (p[0], 3, None, p[1], 50, 128, adjacent)
+        if name == "rotary":
+            rc = native_lib.pkv_rotary_embedding(qo.data_ptr(), ko.data_ptr(), tq.data_ptr(), tk.data_ptr(),
+                                                 Hq * D, Hkv * D, stride, stride, *rot, T, Hq, Hkv, D,
+                                                 err.data_ptr(), st)
+        else:
+            cache = ops.q8_cache(nb, Hkv, bs) if name == "q8" else \
+                [torch.zeros((nb, bs, Hkv, D), dtype=torch.float16, device="cuda") for _ in "kv"]
+            sizes = (T, 2, Hq, Hkv, D, bs, nb, tables.shape[1])
+            args = (qo.data_ptr(), tq.data_ptr(), tk.data_ptr(), tv.data_ptr(), Hq * D, stride, stride,
+                    stride, p[2], p[3], p[4], *[t.data_ptr() for t in cache])
+            if name == "q8":
+                rc = native_lib.pkv_rope_and_cache_q8(*args, 0, *rot, *sizes, cache[2].shape[1],
+                                                      err.data_ptr(), st)
+            else:
+                rc = native_lib.pkv_rope_and_cache(*args, *rot, *sizes, err.data_ptr(), st)
+        assert rc == 0
+        return qo.cpu().numpy(), ko.cpu().numpy(), ops.read_error_word(err)
+
+    for name in ("rotary", "fp16", "q8"):
+        qo, ko, err = run(name)
+        assert err == 5 and (qo[gone] == 7).all()
+        ref = orope.rotate(q[~gone], pos[0, ~gone], table, None, bool(adjacent))
+        assert np.array_equal(bits(qo[~gone]), bits(ref))
+        if name == "rotary":
+            ref = orope.rotate(k[~gone], pos[0, ~gone], table, None, bool(adjacent))
+            assert (ko[gone] == 7).all() and np.array_equal(bits(ko[~gone]), bits(ref))
