@@ -471,3 +471,26 @@ def test_zero_scales_with_codes_left(ops, code, new, cached, width):
     got, err = c.run(ops)
     assert err == 0
     c.check(got)
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("new,cached,Hq,Hkv,width", [
+    ([200, 3], [77, 500], 4, 4, 0),        # units of two tiles; a pair of warpgroups on one
+    ([60, 40], [4000, 2500], 8, 2, 640),   # a split key axis, units of one tile
+    ([2, 5], [4000, 2500], 8, 2, 640),     # the kernel for few rows, split
+])
+def test_scores_that_are_all_minus_infinity(ops, code, new, cached, Hq, Hkv, width):
+    """An infinity in q where the keys have the other sign: NaN, as the softmax of such a row is,
+    and the rows beside it the same bits as without it."""
+    c = Case(63, new, cached, Hq, Hkv, 16, code, width=width)
+    c.codes[0][..., 3] = -np.maximum(np.abs(c.codes[0][..., 3]), 1)
+    clean, err = c.run(ops)
+    assert err == 0 and np.isfinite(clean).all()
+    q = c.q
+    for i in (0, new[0] - 1, new[0]):
+        c.q = q.copy()
+        c.q[i, 1, 3] = np.inf
+        got, err = c.run(ops)
+        want = clean.copy()
+        want[i, 1] = np.nan
+        assert err == 0 and np.array_equal(got, want, equal_nan=True), i

@@ -639,3 +639,86 @@ def test_positions_of_axes_that_no_pair_follows(ops, native_lib, adjacent):
         if name == "rotary":
             ref = orope.rotate(k[~gone], pos[0, ~gone], table, None, bool(adjacent))
             assert (ko[gone] == 7).all() and np.array_equal(bits(ko[~gone]), bits(ref))
+
+
+def takes_the_steps_way(new, bs):
+    """Which of the 8-bit append's two kernels a batch takes: few tokens a sequence, or long chunks."""
+    return sum(new) < max(8, bs // 2) * len(new)
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("bs", [8, 16, 32, 64])
+@pytest.mark.parametrize("new,cached", [([100, 64, 40], [3, 60, 0]), ([300], [5]),
+                                        ([70, 33, 90, 65], [63, 0, 31, 1])])
+def test_q8_long_chunks_not_finite_and_off_the_table(ops, code, bs, new, cached):
+    """As test_q8_long_pieces_of_steps, by the kernel of long chunks at every block size: its teams
+    exchange their maxima twice for a head whose values are not finite."""
+    assert not takes_the_steps_way(new, bs)
+    test_q8_long_pieces_of_steps(ops, code, bs, new, cached)
+
+
+@pytest.mark.parametrize("bs", [16, 64])
+@pytest.mark.parametrize("n", [1, 2, 7, 70])
+def test_q8_left_out_tokens_start_a_block_of_more_sizes(ops, n, bs):
+    test_q8_left_out_tokens_start_a_block(ops, n, bs)
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("bs,new", [(64, [40, 1, 1]), (32, [30, 1, 1]), (16, [13, 1, 1, 1]),
+                                    (64, [64, 1, 64]), (32, [90, 64])])
+@pytest.mark.parametrize("off", ["first", "some", "all"])
+def test_q8_pieces_that_begin_with_left_out_tokens(ops, code, bs, new, off):
+    """A block that held another sequence's tokens under a large scale: its new rows begin with tokens
+    off the table, and the scale comes from the others alone (0 where there are none)."""
+    rng = np.random.default_rng([bs, len(new)])
+    Hq, Hkv, rows = 5, 3, 100
+    lens, qs, T = np.array(new, np.int32), starts(new), sum(new)
+    nb, tables = batch(rng, lens, bs)
+    (q, k, v), (tq, tk, tv) = projection(rng, T, Hq, Hkv)
+    table = table_of(64, rows)
+    seq, place = orope.places(qs, lens, T)
+    out = {"first": (seq == 0) & (place == 0), "all": seq == 0,
+           "some": (seq == 0) & ((place < 3) | (place % 5 == 4))}[off]
+    pos = np.where(out, rows, place).astype(np.int32)
+    codes = {n: oq.nearest_code(rng.standard_normal((nb, bs, Hkv, D)) * 40, code) for n in "kv"}
+    t = {n: codes_to_dev(codes[n], code) for n in "kv"}
+    sc = {n: torch.full((nb, 4), 5.0, device="cuda") for n in "kv"}
+    qo = torch.full((T, Hq, D), 7.0, dtype=torch.float16, device="cuda")
+    err = ops.new_error_word()
+    ops.rope_and_cache_q8(qo, tq, tk, tv, dev(qs), dev(tables), dev(lens), t["k"], t["v"], sc["k"],
+                          sc["v"], dev(table), positions=dev(pos), dev_err=err)
+    assert ops.read_error_word(err) == 5
+    at = tables[seq, place // bs], place % bs
+    for n, x in (("k", orope.rotate(k, place, table)), ("v", v.astype(np.float32))):
+        x = x.copy()
+        x[out] = 0
+        want, scale = codes[n].copy(), np.full((nb, 4), 5.0, np.float32)
+        oq.write(x, qs, tables, lens, want, scale, bs, code)
+        want[at[0][out], at[1][out]] = codes[n][at[0][out], at[1][out]]    # as they were
+        assert np.array_equal(sc[n].cpu().numpy(), scale)
+        assert np.array_equal(codes_of(t[n], code), want)
+    qo = qo.cpu().numpy()
+    assert (qo[out] == 7).all()
+    assert np.array_equal(bits(qo[~out]), bits(orope.rotate(q[~out], place[~out], table)))
+
+
+@pytest.mark.parametrize("new,cached,Hq,Hkv", CASES)
+def test_append_equals_two_steps(ops, new, cached, Hq, Hkv):
+    """rope_and_cache against rotary_embedding and reshape_and_cache: the same bits of K and V."""
+    rng = np.random.default_rng([Hkv, len(new)])
+    bs, T = 16, int(np.sum(new))
+    lens, qs = (np.array(new) + np.array(cached)).astype(np.int32), starts(new)
+    nb, tables = batch(rng, lens, bs)
+    _, (tq, tk, tv) = projection(rng, T, Hq, Hkv)
+    table = dev(table_of(64, 1000))
+    seq, place = orope.places(qs, lens, T)
+    one = [torch.zeros((nb, bs, Hkv, D), dtype=torch.float16, device="cuda") for _ in "kv"]
+    two = [torch.zeros_like(c) for c in one]
+    qo, qo2 = (torch.empty((T, Hq, D), dtype=torch.float16, device="cuda") for _ in range(2))
+    ko = torch.empty((T, Hkv, D), dtype=torch.float16, device="cuda")
+    ops.rope_and_cache(qo, tq, tk, tv, dev(qs), dev(tables), dev(lens), *one, table)
+    ops.rotary_embedding(qo2, ko, tq, tk, dev(place.astype(np.int32)), table)
+    slots = tables[seq, place // bs].astype(np.int64) * bs + place % bs
+    ops.reshape_and_cache(ko, tv.contiguous(), dev(slots), *two)
+    for a, b in zip([qo] + one, [qo2] + two):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))

@@ -85,3 +85,20 @@ def test_workspace_is_whole_splits(native_lib, T, S, Hq, Hkv, width):
     assert rest == 0 and splits != 1 and splits <= tiles
     if tiles == 1:
         assert need == 0
+
+
+@pytest.mark.parametrize("T,S,Hq,Hkv", [(1, 1, 8, 8), (26, 4, 32, 8), (40, 1, 64, 8), (100, 2, 8, 8)])
+@pytest.mark.parametrize("width", [2048, 16384])
+def test_few_rows_over_long_contexts_are_split(native_lib, T, S, Hq, Hkv, width):
+    """The key axis is cut where the rows alone leave SMs idle, and a workspace that is short by a
+    byte, or none, is refused."""
+    need = native_lib.pkv_paged_attention_prefill_q8_workspace_bytes(T, S, Hq, Hkv, width, 16)
+    splits = need // (T * Hq * 130 * 4)
+    assert splits > 1
+    p = 4096
+
+    def run(ws, b):
+        return native_lib.pkv_paged_attention_prefill_q8(
+            p, p, p, p, p, p, 0, p, p, p, T, S, Hq, Hkv, 128, 16, 64, width, -(-Hkv // 4) * 4, 0.1,
+            ws, b, None, None)
+    assert run(p, need - 1) == -1 and run(None, need) == -1 and run(p + 8, need) == -1
