@@ -404,7 +404,8 @@ int pkv_copy_blocks(void* const* k_caches, void* const* v_caches, int num_layers
  * fp32 scores, maxima, sums and accumulators; the softmax weights are rounded
  * to fp16 for the product with V (by half a step, or by 2^-32 of the largest), the
  * result once.  A row with a score that is NaN or +infinity, or with none above
- * -infinity, is NaN.
+ * -infinity, is NaN.  Scores past 2^22 in magnitude (times log2 e) are beyond what
+ * fp32 tells apart to a unit: rows of such scores may be far off, infinite or NaN.
  */
 int pkv_paged_attention_prefill(void* out, const void* q, const void* k_cache,
                                 const void* v_cache, const int32_t* block_tables,
@@ -509,7 +510,9 @@ int pkv_paged_attention_decode_q8(void* out, const void* q, const void* k_cache,
  * with K_s[t] = code * k_scale[block of t, g] and V_s[t] likewise.  Same packed batch,
  * shapes, limits, errors and output: whole prompts, chunks behind earlier ones or behind a
  * cached prefix, a few draft tokens (a kernel of its own where the sequences bring 16 rows
- * of a KV head or fewer on average).  All of the context's K and V must already be in the cache
+ * of a KV head or fewer on average: it is right for a long chunk among them, but reads the
+ * chunk's context again for every 8 or 16 rows, so that the chunk is better off in a call of
+ * its own).  All of the context's K and V must already be in the cache
  * (pkv_reshape_and_cache_q8, pkv_rope_and_cache_q8).
  *   k_cache, v_cache  codes, 16-byte aligned; k_scale, v_scale 4-byte aligned
  * Scales must be finite and not negative (a zero scale is a block of zeros, whatever its

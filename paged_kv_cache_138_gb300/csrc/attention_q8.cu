@@ -27,7 +27,7 @@
 //  * Splits and their fp32 partials are the fp16 kernel's.
 //  * What bounds it: HBM.  64 x 4096 of 32 heads, int8 (2.15 GB): 317 us, 6.8 TB/s, the
 //    rate of a plain copy (327 on another card); the same copies without the arithmetic take 319.  256 x 4096 of
-//    32/8 heads, e4m3: 328-339 us (332 without the arithmetic).  Two contexts of 100k-131k tokens:
+//    32/8 heads, e4m3: 328-342 us (332 without the arithmetic).  Two contexts of 100k-131k tokens:
 //    92 us, 5.2 TB/s: 83-85 us of it here (3.6 rounds of CTAs), the rest the merge.
 #include <cuda.h>
 #include <cudaTypedefs.h>

@@ -18,7 +18,7 @@
 //  * The warps' maxima, sums and outputs join in shared memory, splits in
 //    prompt_merge_kernel.
 //  * What bounds it: HBM for 8 columns, 256 x 1 rows over 4096 of 32/8 heads 330-337 us (the
-//    single-token kernel 328-339); 64 x 2 rows 103-106 us, 80 of them the bytes', the rest the last
+//    single-token kernel 328-342); 64 x 2 rows 103-106 us, 80 of them the bytes', the rest the last
 //    round of CTAs and the merge; arithmetic for 16, 64 x 4 rows 119-125 us (prompt_q8.cu
 //    132-144).  32 columns took 166 us (64 x 8 rows; prompt_q8.cu 130-142): the products
 //    of warps alone take as long as the copies then, with two CTAs an SM to hide them.

@@ -24,8 +24,8 @@
 //  * What bounds it: a query tile's softmax (1550 cycles a tile of 128 tokens, 500 of its
 //    scheduler's instructions being the widening's) and its own products (1024) follow one
 //    another, 2800 cycles a turn where the tensor core is busy for 2048.  16,384 tokens of 32/8
-//    heads, int8: 1283-1305 us in short runs, 1363-1384 in loops of seconds, 1.59-1.71 PFLOP/s
-//    (fp16 cache: 1180-1310 and 1370-1460); 16 x 2048 413-422 us, e4m3 399 (fp16 376); 8 of
+//    heads, int8: 1283-1305 us in short runs, 1363-1391 in loops of seconds, 1.58-1.71 PFLOP/s
+//    (fp16 cache: 1180-1310 and 1370-1460); 16 x 2048 413-422 us, e4m3 399-405 (fp16 376-385); 8 of
 //    64..512 rows behind 2048, 32 heads, e4m3: 94 us.  4 x 5..8 rows over 30k of 32/8 heads,
 //    int8: 80 us, 3.2 TB/s: a tile of codes is widened in 1000 cycles, 550 of them instructions
 //    of one warp a scheduler.  Tried and not kept: two warpgroups that widen, in turn or one
@@ -970,7 +970,11 @@ void cut_axis(Plan* plan, int num_tokens, int num_seqs, int num_kv_heads, int gr
 
 Plan plan_of(int num_tokens, int num_seqs, int num_kv_heads, int group_shift, int64_t max_context) {
   const int64_t rows = static_cast<int64_t>(num_tokens) << group_shift;   // of a KV head
-  // Both kernels work for any batch; the rules go by the average sequence.  16 rows, 64 x 4096
+  // Both kernels work for any batch; the rules go by the average sequence, since the host knows
+  // no lengths.  A long chunk among single tokens pays for it: its units of 16 rows each stream
+  // the whole context (255 single tokens over 1000 and 700 rows over 16k of 32/8 heads 1006 us,
+  // as two calls 256; 63 single tokens and 100 rows over 4096 145 and 132).
+  //  16 rows, 64 x 4096
   // tokens, e4m3: 119 us and 132 here; 32 rows: 168 and 130.  Contexts of one tile whose units
   // are all there at once take less time in the other kernel (5 of 7..63 rows, 8 heads 5.8 us
   // and 8.9 here; 4 x 64 of 32/8 heads, more units than places, 14 and 9.3).
