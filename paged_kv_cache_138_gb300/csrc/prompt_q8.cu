@@ -971,13 +971,12 @@ void cut_axis(Plan* plan, int num_tokens, int num_seqs, int num_kv_heads, int gr
 Plan plan_of(int num_tokens, int num_seqs, int num_kv_heads, int group_shift, int64_t max_context) {
   const int64_t rows = static_cast<int64_t>(num_tokens) << group_shift;   // of a KV head
   // Both kernels work for any batch; the rules go by the average sequence, since the host knows
-  // no lengths.  A long chunk among single tokens pays for it: its units of 16 rows each stream
-  // the whole context (255 single tokens over 1000 and 700 rows over 16k of 32/8 heads 1006 us,
-  // as two calls 256; 63 single tokens and 100 rows over 4096 145 and 132).
-  //  16 rows, 64 x 4096
-  // tokens, e4m3: 119 us and 132 here; 32 rows: 168 and 130.  Contexts of one tile whose units
-  // are all there at once take less time in the other kernel (5 of 7..63 rows, 8 heads 5.8 us
-  // and 8.9 here; 4 x 64 of 32/8 heads, more units than places, 14 and 9.3).
+  // no lengths.  16 rows, 64 x 4096 tokens, e4m3: 119 us and 132 here; 32 rows: 168 and 130.
+  // Contexts of one tile whose units are all there at once take less time in the other kernel
+  // (5 of 7..63 rows, 8 heads 5.8 us and 8.9 here; 4 x 64 of 32/8 heads, more units than places,
+  // 14 and 9.3).  A long chunk among single tokens pays for the average: its units of 16 rows
+  // each stream the whole context (255 single tokens over 1000 and 700 rows over 16k of 32/8
+  // heads, int8, 1006 us, as two calls 256; 63 single tokens and 100 rows over 4096 145 and 132).
   const int64_t few = (rows / 16 + num_seqs) * num_kv_heads;   // units of the other kernel
   if (rows <= 16ll * num_seqs || (max_context <= kTile && few <= 3 * kSms))
     return few_rows_plan(num_tokens, num_seqs, num_kv_heads, group_shift, max_context);
